@@ -23,9 +23,10 @@ _LIB_PATH = os.path.join(_HERE, "libmoeq.so")
 _HEADER = os.path.join(os.path.dirname(_HERE), "include", "moeq.h")
 
 FMT_MXFP4, FMT_NVFP4, FMT_Q2_K, FMT_IQ2_XXS, FMT_FP8_B128 = 1, 2, 3, 4, 5
-FMT_MXFP8, FMT_FP8_B32, FMT_MXFP8_TILED = 6, 7, 8
+FMT_MXFP8, FMT_FP8_B32, FMT_MXFP8_TILED, FMT_INT8 = 6, 7, 8, 9
 FMT_BY_NAME = {"mxfp4": 1, "nvfp4": 2, "q2_k": 3, "iq2_xxs": 4, "fp8_b128": 5, "mxfp8": 6, "fp8_b32": 7,
-               "mxfp8_tiled": 8}
+               "mxfp8_tiled": 8, "int8": 9}
+OUT_F32, OUT_BF16 = 0, 1
 
 MOEQ_OK = 0
 MOEQ_E_SCRATCH = -8
@@ -76,6 +77,11 @@ _SIGS = {
     "moeq_linear": (_i, [ctypes.POINTER(MoeqWeight), _i, _vp, _i, _vp, _vp]),
     "moeq_quantize_mxfp8": (_i, [_vp, _i, _i, _vp, _vp, _vp]),
     "moeq_quantize_mxfp8_f32": (_i, [_vp, _i, _i, _vp, _vp, _vp]),
+    "moeq_quantize_int8": (_i, [_vp, _i, _i, _vp, _vp, _vp]),
+    "moeq_quantize_int8_f32": (_i, [_vp, _i, _i, _vp, _vp, _vp]),
+    "moeq_linear_int8": (_i, [ctypes.POINTER(MoeqWeight), _i, _vp, _vp, _i, _vp, _i, _vp, _vp]),
+    "moeq_linear_int8_workspace_bytes": (_sz, [_i, _i]),
+    "moeq_linear_int8_dynamic": (_i, [ctypes.POINTER(MoeqWeight), _i, _vp, _i, _vp, _i, _vp, _vp, _sz, _vp]),
     "moeq_check_device_error": (_i, [_vp, _vp, ctypes.POINTER(ctypes.c_uint32), _i]),
     "moeq_mxfp8_to_tiled": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp]),
     "moeq_mxfp4_to_nvfp4_device": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]),
@@ -466,6 +472,97 @@ def quantize_mxfp8(x, q=None, e=None):
         rc = _lib().moeq_quantize_mxfp8(_ptr(x), T, K, _ptr(q), _ptr(e), _stream_ptr())
     _check("moeq_quantize_mxfp8", rc)
     return q, e
+
+
+def _on_device(*ts):
+    """The tensors are on the current GPU (the library launches there)."""
+    _require_cuda(*ts)
+    dev = _torch().cuda.current_device()
+    for t in ts:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def quantize_int8(x, q=None, scale=None):
+    """int8 codes [T, K] and one fp32 scale per token [T] of a bf16 or fp32 [T, K] tensor."""
+    torch = _torch()
+    if x is None or len(x.shape) != 2:
+        raise ValueError("x: expected a [T, K] tensor")
+    T, K = x.shape
+    _want("x", x, (torch.bfloat16, torch.float32), (T, K))
+    if q is None:
+        q = torch.empty((T, K), dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty((T,), dtype=torch.float32, device=x.device)
+    _want("q", q, (torch.int8,), (T, K))
+    _want("scale", scale, (torch.float32,), (T,))
+    _on_device(x, q, scale)
+    if T == 0:
+        return q, scale
+    fn = _lib().moeq_quantize_int8_f32 if x.dtype == torch.float32 else _lib().moeq_quantize_int8
+    _check("moeq_quantize_int8", fn(x.data_ptr(), T, K, q.data_ptr(), scale.data_ptr(), _stream_ptr()))
+    return q, scale
+
+
+def _int8_out(w, T, bias, y, out_dtype, device):
+    torch = _torch()
+    if bias is not None:
+        _want("bias", bias, (torch.float32,), (w.rows,))
+    if y is None:
+        y = torch.empty((T, w.rows), dtype=out_dtype or torch.bfloat16, device=device)
+    _want("y", y, (torch.float32, torch.bfloat16) if out_dtype is None else (out_dtype,), (T, w.rows))
+    return y, OUT_BF16 if y.dtype == torch.bfloat16 else OUT_F32
+
+
+def linear_int8(w: Weight, xq, xs, expert: int = 0, bias=None, y=None, out_dtype=None):
+    """y [T, rows] = xs * scale * (xq W^T) (+ bias) of int8 tokens (quantize_int8) and an
+    INT8 weight; bf16 unless y or out_dtype says fp32."""
+    torch = _torch()
+    T = _tokens("xq", xq, w.cols)
+    _want("xq", xq, (torch.int8,), (T, w.cols))
+    _want("xs", xs, (torch.float32,), (T,))
+    y, out = _int8_out(w, T, bias, y, out_dtype, xq.device)
+    s = w.struct()
+    _on_device(xq, xs, bias, y, w.data, w.scales)
+    if T == 0:
+        return y
+    _check("moeq_linear_int8", _lib().moeq_linear_int8(ctypes.byref(s), expert, xq.data_ptr(), xs.data_ptr(), T,
+                                                       None if bias is None else bias.data_ptr(), out, y.data_ptr(),
+                                                       _stream_ptr()))
+    return y
+
+
+def linear_int8_workspace(T: int, cols: int, device="cuda"):
+    """A workspace for linear_int8_dynamic on up to T tokens."""
+    torch = _torch()
+    n = int(_lib().moeq_linear_int8_workspace_bytes(T, cols))
+    if n == 0:
+        raise MoeqError("moeq_linear_int8_workspace_bytes", -4)
+    ws = torch.empty(n + 256, dtype=torch.uint8, device=device)
+    off = (-ws.data_ptr()) % 256
+    return ws[off:off + n]
+
+
+def linear_int8_dynamic(w: Weight, x, expert: int = 0, bias=None, y=None, out_dtype=None, ws=None):
+    """linear_int8 from bf16 tokens x [T, cols], quantised within the call. Without ws the
+    workspace is allocated for the call from torch's caching allocator (on the current
+    stream, so calls on different streams never share one)."""
+    torch = _torch()
+    T = _tokens("x", x, w.cols)
+    _want("x", x, (torch.bfloat16,), (T, w.cols))
+    y, out = _int8_out(w, T, bias, y, out_dtype, x.device)
+    _on_device(x, bias, y, ws, w.data, w.scales)
+    if T == 0:
+        return y
+    if ws is None:
+        ws = linear_int8_workspace(T, w.cols, x.device)
+    _want("ws", ws, (torch.uint8,), (ws.numel(),))
+    s = w.struct()
+    _check("moeq_linear_int8_dynamic",
+           _lib().moeq_linear_int8_dynamic(ctypes.byref(s), expert, x.data_ptr(), T,
+                                           None if bias is None else bias.data_ptr(), out, y.data_ptr(),
+                                           ws.data_ptr(), ws.numel(), _stream_ptr()))
+    return y
 
 
 def check_device_error(ws, clear=True) -> int:

@@ -29,12 +29,15 @@ int block_k(int fmt) {
     case MOEQ_FMT_MXFP8: return 32;
     case MOEQ_FMT_FP8_B32: return 32;
     case MOEQ_FMT_MXFP8_TILED: return 512;
+    case MOEQ_FMT_INT8: return 16;
   }
   return 0;
 }
 
-// Formats for dense linears only (moeq_linear, moeq_dequant), not for layers.
-bool dense_only(int fmt) { return fmt == MOEQ_FMT_MXFP8 || fmt == MOEQ_FMT_FP8_B32 || fmt == MOEQ_FMT_MXFP8_TILED; }
+// Formats for dense linears only (moeq_linear, moeq_linear_int8, moeq_dequant), not for layers.
+bool dense_only(int fmt) {
+  return fmt == MOEQ_FMT_MXFP8 || fmt == MOEQ_FMT_FP8_B32 || fmt == MOEQ_FMT_MXFP8_TILED || fmt == MOEQ_FMT_INT8;
+}
 
 size_t plane_bytes(int fmt, int rows, int cols, int plane) {
   int bk = block_k(fmt);
@@ -55,6 +58,7 @@ size_t plane_bytes(int fmt, int rows, int cols, int plane) {
     case MOEQ_FMT_MXFP8_TILED:
       if (rows % 16) return 0;
       return plane == 0 ? n : n / 32;
+    case MOEQ_FMT_INT8: return plane == 0 ? n : (size_t)rows * 4;
   }
   return 0;
 }
@@ -372,6 +376,36 @@ int run_down(const moeq_layer* L, const float* h, const int32_t* ids, const floa
   return hip_rc(launch_combine(partial, T, L->top_k, L->hidden, y, s));
 }
 
+// Expert `expert` of an INT8 tensor; the activation side is the caller's to fill.
+Int8Params int8_params(const moeq_weight& w, int expert) {
+  Int8Params p;
+  memset(&p, 0, sizeof(p));
+  p.w = static_cast<const int8_t*>(w.data) + (size_t)expert * w.expert_stride;
+  p.ws = reinterpret_cast<const float*>(static_cast<const uint8_t*>(w.scales) + (size_t)expert * w.scale_expert_stride);
+  p.rows = w.rows;
+  p.cols = w.cols;
+  return p;
+}
+
+// The checks of the INT8 linears up to the token operand.
+int check_linear_int8(const moeq_weight* w, int expert, int T, const float* bias, int out_type, const void* y) {
+  int rc = check_weight(w, false);
+  if (rc) return rc;
+  if (w->fmt != MOEQ_FMT_INT8) return MOEQ_E_FMT;
+  if (w->cols > INT8_MAX_COLS) return MOEQ_E_SHAPE;
+  if (expert < 0 || expert >= w->n_experts || T < 0 || !y) return MOEQ_E_INVAL;
+  if (out_type != MOEQ_OUT_F32 && out_type != MOEQ_OUT_BF16) return MOEQ_E_INVAL;
+  if (!aligned(y, out_type == MOEQ_OUT_BF16 ? 2 : 4) || (bias && !aligned(bias, 4))) return MOEQ_E_ALIGN;
+  return MOEQ_OK;
+}
+
+int check_quant_int8(const void* x, int T, int K, const void* q, const void* scale) {
+  if (!x || !q || !scale || T < 0) return MOEQ_E_INVAL;
+  if (K <= 0 || K % 16 || K > INT8_MAX_COLS) return MOEQ_E_SHAPE;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return MOEQ_E_ALIGN;
+  return MOEQ_OK;
+}
+
 // The W4A8 prefill stage of the gate/up pair (gate_up) or of down: its weights
 // MXFP4, K advancing in chunks of 256 (hidden and inter multiples of 256), scale
 // planes staged in 8-byte pieces.
@@ -591,6 +625,10 @@ int moeq_dequant(const moeq_weight* w, int expert, float* out, void* stream) {
   if (expert < 0 || expert >= w->n_experts) return MOEQ_E_INVAL;
   if (!out) return MOEQ_E_INVAL;
   if (!aligned(out, 4)) return MOEQ_E_ALIGN;
+  if (w->fmt == MOEQ_FMT_INT8) {
+    const Int8Params p = int8_params(*w, expert);
+    return hip_rc(launch_dequant_int8(p.w, p.ws, w->rows, w->cols, out, S(stream)));
+  }
   return hip_rc(launch_dequant(w->fmt, ref_of(*w), w->grid, w->rows, w->cols, expert, out, S(stream)));
 }
 
@@ -739,6 +777,7 @@ int moeq_prefill_down(const moeq_layer* L, const uint8_t* hq, const uint8_t* hs,
 int moeq_linear(const moeq_weight* w, int expert, const void* x, int T, float* y, void* stream) {
   int rc = check_weight(w, false);
   if (rc) return rc;
+  if (w->fmt == MOEQ_FMT_INT8) return MOEQ_E_FMT;  // moeq_linear_int8 takes it
   const bool mx8 = dense_only(w->fmt);
   if (mx8 && !linear_mx8_fits(w->fmt, w->rows, w->cols)) return MOEQ_E_SHAPE;
   const bool mfma = w->fmt == MOEQ_FMT_FP8_B128 && T > 1 && linear_fp8_fits(w->rows, w->cols);
@@ -795,6 +834,62 @@ int moeq_quantize_mxfp8_f32(const float* x, int T, int K, uint8_t* q, uint8_t* e
   if (!aligned(x, 16) || !aligned(q, 16)) return MOEQ_E_ALIGN;
   if (T == 0) return MOEQ_OK;
   return hip_rc(launch_quant_mxfp8(1, x, T, K, q, e8m0, S(stream)));
+}
+
+int moeq_quantize_int8(const void* x, int T, int K, int8_t* q, float* scale, void* stream) {
+  int rc = check_quant_int8(x, T, K, q, scale);
+  if (rc || T == 0) return rc;
+  return hip_rc(launch_quant_int8(0, x, T, K, q, scale, S(stream)));
+}
+
+int moeq_quantize_int8_f32(const float* x, int T, int K, int8_t* q, float* scale, void* stream) {
+  int rc = check_quant_int8(x, T, K, q, scale);
+  if (rc || T == 0) return rc;
+  return hip_rc(launch_quant_int8(1, x, T, K, q, scale, S(stream)));
+}
+
+int moeq_linear_int8(const moeq_weight* w, int expert, const int8_t* xq, const float* xs, int T, const float* bias,
+                     int out_type, void* y, void* stream) {
+  int rc = check_linear_int8(w, expert, T, bias, out_type, y);
+  if (rc) return rc;
+  if (!xq || !xs) return MOEQ_E_INVAL;
+  if (!aligned(xq, 16) || !aligned(xs, 4)) return MOEQ_E_ALIGN;
+  if (T == 0) return MOEQ_OK;
+  Int8Params p = int8_params(*w, expert);
+  p.xq = xq;
+  p.xs = xs;
+  p.T = T;
+  p.bias = bias;
+  p.out_bf16 = out_type == MOEQ_OUT_BF16;
+  p.y = y;
+  return hip_rc(launch_linear_int8(p, S(stream)));
+}
+
+size_t moeq_linear_int8_workspace_bytes(int T, int cols) {
+  if (T < 0 || cols <= 0 || cols % 16 || cols > INT8_MAX_COLS) return 0;
+  return align_up((size_t)T * 4, 256) + align_up((size_t)T * cols, 256) + 256;
+}
+
+int moeq_linear_int8_dynamic(const moeq_weight* w, int expert, const void* x, int T, const float* bias, int out_type,
+                             void* y, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_linear_int8(w, expert, T, bias, out_type, y);
+  if (rc) return rc;
+  if (!x) return MOEQ_E_INVAL;
+  if (!aligned(x, 16)) return MOEQ_E_ALIGN;
+  if (!ws || ws_bytes < moeq_linear_int8_workspace_bytes(T, w->cols)) return MOEQ_E_WORKSPACE;
+  if (!aligned(ws, 256)) return MOEQ_E_ALIGN;
+  if (T == 0) return MOEQ_OK;
+  float* xs = (float*)ws;
+  int8_t* xq = (int8_t*)ws + align_up((size_t)T * 4, 256);
+  if ((rc = hip_rc(launch_quant_int8(0, x, T, w->cols, xq, xs, S(stream))))) return rc;
+  Int8Params p = int8_params(*w, expert);
+  p.xq = xq;
+  p.xs = xs;
+  p.T = T;
+  p.bias = bias;
+  p.out_bf16 = out_type == MOEQ_OUT_BF16;
+  p.y = y;
+  return hip_rc(launch_linear_int8(p, S(stream)));
 }
 
 int moeq_check_device_error(void* ws, void* stream, uint32_t* err_host, int clear) {

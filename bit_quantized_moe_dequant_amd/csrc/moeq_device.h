@@ -27,7 +27,8 @@ enum {
   FMT_FP8_B128 = 5,
   FMT_MXFP8 = 6,
   FMT_FP8_B32 = 7,
-  FMT_MXFP8_TILED = 8
+  FMT_MXFP8_TILED = 8,
+  FMT_INT8 = 9
 };
 enum { ACT_BF16 = 0, ACT_F32 = 1 };
 
@@ -62,6 +63,22 @@ __device__ __forceinline__ float half_bits_f32(uint32_t h) {
 __device__ __forceinline__ uint32_t f32_bf16_rne(float f) {
   uint32_t u = __builtin_bit_cast(uint32_t, f);
   return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+}
+
+// The same for any input: NaNs stay NaN (quiet), infinities are kept.
+__device__ __forceinline__ uint32_t f32_bf16_rne_nan(float f) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, f);
+  return (u & 0x7FFFFFFFu) > 0x7F800000u ? ((u >> 16) | 0x40u) : f32_bf16_rne(f);
+}
+
+// Token scale of the int8 quantisation from the bits of the row's largest magnitude,
+// and the code of one value under it (IEEE divisions: the codes are defined by them).
+__device__ __forceinline__ float int8_scale(uint32_t amax_bits) {
+  return amax_bits >= 0x7F800000u ? u2f(0x7FC00000u) : u2f(amax_bits) / 127.0f;
+}
+__device__ __forceinline__ int int8_code(float v, float s) {
+  const float q = __builtin_fminf(__builtin_fmaxf(__builtin_rintf(v / s), -127.0f), 127.0f);
+  return s > 0.f ? (int)q : 0;
 }
 
 // Split two fp32 values into hi and lo bf16 pairs with a + b ~ value to 16 bits.

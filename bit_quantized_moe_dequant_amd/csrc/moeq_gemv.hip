@@ -381,6 +381,7 @@ int weights_per_chunk(int fmt) {
     case FMT_MXFP8: return 16;
     case FMT_FP8_B32: return 16;
     case FMT_MXFP8_TILED: return 16;
+    case FMT_INT8: return 16;
   }
   return 0;
 }

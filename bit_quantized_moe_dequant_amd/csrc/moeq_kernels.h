@@ -104,6 +104,18 @@ struct Mx8Params {
   int rows, cols, T;
 };
 
+// 8-bit integer linear of one expert tensor.
+constexpr int INT8_MAX_COLS = 65536;  // 2^14 per product: the int32 sum stays below 2^31
+struct Int8Params {
+  const int8_t* w;    // [rows][cols], 16-byte aligned
+  const float* ws;    // [rows]
+  const int8_t* xq;   // [T][cols], 16-byte aligned
+  const float* xs;    // [T]
+  const float* bias;  // [rows] or null
+  void* y;            // fp32 or bf16 [T][rows]
+  int rows, cols, T, out_bf16;
+};
+
 // Launchers (return hipError_t of the launch).
 hipError_t launch_dequant(int fmt, const WeightRef& w, const uint8_t* grid, int rows, int cols, int expert, float* out,
                           hipStream_t s);
@@ -170,6 +182,11 @@ hipError_t launch_mx4_to_nv4(const uint8_t* nib, const uint8_t* e8m0, int rows, 
                              uint8_t* e4m3_out, float* scale2_out, uint32_t* status, hipStream_t s);
 hipError_t launch_nv4_to_mx4(const uint8_t* nib, const uint8_t* e4m3, const float* scale2, int rows, int cols, int n,
                              uint8_t* nib_out, uint8_t* e8m0_out, uint32_t* status, hipStream_t s);
+
+// Per-token int8 codes and scales of bf16 (in_f32 = 0) or fp32 rows; K % 16 == 0.
+hipError_t launch_quant_int8(int in_f32, const void* x, int T, int K, int8_t* q, float* scale, hipStream_t s);
+hipError_t launch_linear_int8(const Int8Params& p, hipStream_t s);
+hipError_t launch_dequant_int8(const int8_t* w, const float* ws, int rows, int cols, float* out, hipStream_t s);
 
 // Chunk geometry: weights per 16-byte chunk; lanes per row and chunks per lane.
 int weights_per_chunk(int fmt);

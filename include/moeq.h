@@ -89,6 +89,11 @@ extern "C" {
  *   + Q2_K + FP8 hybrid card, format table; W4A16-FP8 card, FP8 block 128x128).
  *   data: u8 [rows][cols] e4m3fn codes. scales: u8 [rows/128][cols/128].
  *
+ * MOEQ_FMT_INT8 - 8-bit integers with one fp32 scale per row (output channel);
+ *   moeq_linear_int8, moeq_linear_int8_dynamic, moeq_dequant and the shared expert
+ *   of moeq_moe_forward only (elsewhere MOEQ_E_FMT). data: i8 [rows][cols], cols a
+ *   multiple of 16; scales: fp32 [rows]; weight = code * scale (codes -128..127).
+ *
  * Dense-linear formats (moeq_linear and moeq_dequant only; a layer using one is
  * refused with MOEQ_E_FMT):
  * MOEQ_FMT_FP8_B32 - E4M3 weights with one UE8M0 scale per 32x32 tile, the dense
@@ -117,6 +122,11 @@ extern "C" {
 #define MOEQ_FMT_MXFP8 6
 #define MOEQ_FMT_FP8_B32 7
 #define MOEQ_FMT_MXFP8_TILED 8
+#define MOEQ_FMT_INT8 9
+
+/* Types of the outputs that come in more than one. */
+#define MOEQ_OUT_F32 0
+#define MOEQ_OUT_BF16 1
 
 /* ------------------------------------------------------------------ status */
 #define MOEQ_OK 0
@@ -161,7 +171,7 @@ const char* moeq_status_string(int status);
 
 /* Bytes of plane 0 (data) or plane 1 (scales) of one expert tensor [rows, cols];
  * 0 for an invalid format, plane or shape. cols must be a multiple of the format's
- * block: 32 MXFP4, 16 NVFP4, 256 Q2_K and IQ2_XXS, 128 FP8_B128 (rows too). */
+ * block: 32 MXFP4, 16 NVFP4, 256 Q2_K and IQ2_XXS, 128 FP8_B128 (rows too), 16 INT8. */
 size_t moeq_plane_bytes(int fmt, int rows, int cols, int plane);
 
 /* Total bytes of one expert tensor, both planes plus NVFP4's 4-byte scale_2. The
@@ -314,6 +324,35 @@ int moeq_linear(const moeq_weight* w, int expert, const void* x, int T, float* y
  * [T][K/32] overwritten. MOEQ_E_SHAPE if K is not a positive multiple of 32. */
 int moeq_quantize_mxfp8(const void* x, int T, int K, uint8_t* q, uint8_t* e8m0, void* stream);
 int moeq_quantize_mxfp8_f32(const float* x, int T, int K, uint8_t* q, uint8_t* e8m0, void* stream);
+
+/* ------------------------------------------------------------------ 8-bit integers */
+
+/* Codes and scale of every token for the INT8 linears: s = fl32(max |x| / 127), q =
+ * round-half-even(fl32(x / s)) clamped to +-127, in fp32 with correctly rounded
+ * divisions. A token of zeros gives s = 0 and codes 0; one that holds an infinity or a
+ * NaN gives s = NaN and codes 0 (its outputs are NaN). x [T][K] bf16 (fp32 in the _f32
+ * form) and q i8 [T][K] 16-byte aligned, scale fp32 [T]; q and scale overwritten.
+ * MOEQ_E_SHAPE unless K is a multiple of 16, 16 .. 65536. T == 0 is a no-op. */
+int moeq_quantize_int8(const void* x, int T, int K, int8_t* q, float* scale, void* stream);
+int moeq_quantize_int8_f32(const float* x, int T, int K, int8_t* q, float* scale, void* stream);
+
+/* y[t][r] = xs[t] * scale[r] * sum_k xq[t][k] W[r][k] (+ bias[r]) for expert `expert`
+ * of an MOEQ_FMT_INT8 weight. The sum is exact (int32; cols at most 65536, any codes);
+ * the scales and the bias are applied in fp32. xq i8 [T][cols], 16-byte aligned; xs
+ * fp32 [T]; bias fp32 [rows] or NULL; y [T][rows] overwritten, fp32 (MOEQ_OUT_F32) or
+ * bf16 rounded to nearest even (MOEQ_OUT_BF16), aligned to its element. Any T and
+ * rows; T == 0 is a no-op. The same inputs give the same bits whatever the batch they
+ * are part of. */
+int moeq_linear_int8(const moeq_weight* w, int expert, const int8_t* xq, const float* xs, int T, const float* bias,
+                     int out_type, void* y, void* stream);
+
+/* The same product from bf16 tokens x [T][cols] (16-byte aligned), quantised as by
+ * moeq_quantize_int8 within the call. ws: at least
+ * moeq_linear_int8_workspace_bytes(T, cols) bytes, 256-byte aligned, contents
+ * arbitrary, not shared with an overlapping call. */
+size_t moeq_linear_int8_workspace_bytes(int T, int cols);
+int moeq_linear_int8_dynamic(const moeq_weight* w, int expert, const void* x, int T, const float* bias, int out_type,
+                             void* y, void* ws, size_t ws_bytes, void* stream);
 
 /* Synchronise `stream`, then read (and with clear != 0, zero) the device error word. */
 int moeq_check_device_error(void* ws, void* stream, uint32_t* err_host, int clear);
