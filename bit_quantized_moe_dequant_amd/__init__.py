@@ -27,6 +27,7 @@ FMT_MXFP8, FMT_FP8_B32, FMT_MXFP8_TILED, FMT_INT8 = 6, 7, 8, 9
 FMT_BY_NAME = {"mxfp4": 1, "nvfp4": 2, "q2_k": 3, "iq2_xxs": 4, "fp8_b128": 5, "mxfp8": 6, "fp8_b32": 7,
                "mxfp8_tiled": 8, "int8": 9}
 OUT_F32, OUT_BF16 = 0, 1
+SCORE_BY_NAME = {"softmax": 0, "sigmoid": 1, "sqrtsoftplus": 2}
 
 MOEQ_OK = 0
 MOEQ_E_SCRATCH = -8
@@ -51,6 +52,16 @@ class MoeqWeight(ctypes.Structure):
 class MoeqLayer(ctypes.Structure):
     _fields_ = [("hidden", ctypes.c_int), ("inter", ctypes.c_int), ("n_experts", ctypes.c_int),
                 ("top_k", ctypes.c_int), ("gate", MoeqWeight), ("up", MoeqWeight), ("down", MoeqWeight)]
+
+
+class MoeqRouter(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int), ("n_experts", ctypes.c_int), ("top_k", ctypes.c_int),
+                ("scoring", ctypes.c_int), ("normalize", ctypes.c_int), ("scale", ctypes.c_float),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class MoeqShared(ctypes.Structure):
+    _fields_ = [("inter", ctypes.c_int), ("gate", MoeqWeight), ("up", MoeqWeight), ("down", MoeqWeight)]
 
 
 _LIB = None
@@ -82,6 +93,10 @@ _SIGS = {
     "moeq_linear_int8": (_i, [ctypes.POINTER(MoeqWeight), _i, _vp, _vp, _i, _vp, _i, _vp, _vp]),
     "moeq_linear_int8_workspace_bytes": (_sz, [_i, _i]),
     "moeq_linear_int8_dynamic": (_i, [ctypes.POINTER(MoeqWeight), _i, _vp, _i, _vp, _i, _vp, _vp, _sz, _vp]),
+    "moeq_router_workspace_bytes": (_sz, [ctypes.POINTER(MoeqRouter), _i]),
+    "moeq_router_topk": (_i, [ctypes.POINTER(MoeqRouter), _vp, _i, _vp, _vp, _vp, _sz, _vp]),
+    "moeq_moe_workspace_bytes": (_sz, [_vp, _vp, _vp, _i]),
+    "moeq_moe_forward": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
     "moeq_check_device_error": (_i, [_vp, _vp, ctypes.POINTER(ctypes.c_uint32), _i]),
     "moeq_mxfp8_to_tiled": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp]),
     "moeq_mxfp4_to_nvfp4_device": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]),
@@ -563,6 +578,139 @@ def linear_int8_dynamic(w: Weight, x, expert: int = 0, bias=None, y=None, out_dt
                                            None if bias is None else bias.data_ptr(), out, y.data_ptr(),
                                            ws.data_ptr(), ws.numel(), _stream_ptr()))
     return y
+
+
+class Router:
+    """Router weights (bf16 [E, H]), an optional fp32 [E] bias for the choice, and the
+    rule: scoring "softmax", "sigmoid" or "sqrtsoftplus"; normalize divides the chosen
+    scores by their sum; scale multiplies the route weights. The tensors are kept, their
+    contents are read by every call."""
+
+    def __init__(self, weight, top_k: int, scoring="softmax", normalize=False, scale=1.0, bias=None):
+        torch = _torch()
+        if weight is None or len(weight.shape) != 2:
+            raise ValueError("weight: expected an [E, H] tensor")
+        _want("weight", weight, (torch.bfloat16,), tuple(weight.shape))
+        self.n_experts, self.hidden = (int(n) for n in weight.shape)
+        if bias is not None:
+            _want("bias", bias, (torch.float32,), (self.n_experts,))
+        if scoring not in SCORE_BY_NAME:
+            raise ValueError(f"scoring: {scoring!r}, expected one of {', '.join(SCORE_BY_NAME)}")
+        self.weight, self.bias, self.top_k = weight, bias, int(top_k)
+        self.scoring, self.normalize, self.scale = scoring, bool(normalize), float(scale)
+        self._struct = MoeqRouter(self.hidden, self.n_experts, self.top_k, SCORE_BY_NAME[scoring],
+                                  int(self.normalize), self.scale, weight.data_ptr(),
+                                  0 if bias is None else bias.data_ptr())
+        self._ws = _Workspaces(lambda T: _lib().moeq_router_workspace_bytes(ctypes.byref(self._struct), T))
+
+    def workspace(self, T: int):
+        """An initialised workspace for T tokens; the current stream's own (kept per stream)."""
+        return self._ws.get(T, self.weight.device)
+
+
+class SharedExpert:
+    """The expert every token passes, as three INT8 weights: gate and up [I, H], down [H, I]."""
+
+    def __init__(self, gate: Weight, up: Weight, down: Weight):
+        self.gate, self.up, self.down, self.inter = gate, up, down, gate.rows
+
+    def struct(self) -> MoeqShared:
+        return MoeqShared(self.inter, self.gate.struct(), self.up.struct(), self.down.struct())
+
+
+class MoeLayer:
+    """A whole MoE layer: routed experts, their router and an optional shared expert.
+    The descriptors are taken when it is made (the tensors' contents are read by every
+    call); make a new one after replacing a tensor."""
+
+    def __init__(self, layer: Layer, router: Router, shared: SharedExpert = None):
+        self.layer, self.router, self.shared = layer, router, shared
+        self.hidden, self.top_k = layer.hidden, layer.top_k
+        self._structs = (layer.struct(), router._struct, None if shared is None else shared.struct())
+        self._refs = tuple(None if s is None else ctypes.addressof(s) for s in self._structs)
+        self._weights = [w for p in (layer, shared) if p is not None for w in (p.gate, p.up, p.down)]
+        self._ws = _Workspaces(lambda T: _lib().moeq_moe_workspace_bytes(*self._refs, T))
+
+    def workspace(self, T: int):
+        """An initialised workspace for T tokens; the current stream's own (kept per stream)."""
+        return self._ws.get(T, self.router.weight.device)
+
+
+class _Workspaces:
+    """Initialised, 256-byte aligned workspaces, one per stream and number of tokens: calls
+    on different streams may overlap, and must not share one. A call under graph capture
+    gets one of its own that is not kept: the graph may be replayed beside anything, and
+    what capture records (the initialisation among it) has not run yet."""
+
+    def __init__(self, need):
+        self.need, self.kept = need, {}
+
+    def get(self, T, device):
+        torch = _torch()
+        if torch.cuda.is_current_stream_capturing():
+            return self._make(T, device)
+        key = (torch.cuda.current_stream().cuda_stream, T)
+        ws = self.kept.get(key)
+        if ws is None:
+            ws = self.kept[key] = self._make(T, device)
+        return ws
+
+    def _make(self, T, device):
+        n = int(self.need(T))
+        if n == 0:
+            raise MoeqError("workspace size", -4)
+        ws = _torch().empty(n + 256, dtype=_torch().uint8, device=device)
+        off = (-ws.data_ptr()) % 256
+        ws = ws[off:off + n]
+        _check("moeq_workspace_init", _lib().moeq_workspace_init(ws.data_ptr(), n, _stream_ptr()))
+        return ws
+
+
+def router_topk(router: Router, x, ids=None, rw=None, ws=None):
+    """(ids [T, K] int32, route weights [T, K] fp32) of bf16 tokens x [T, H]."""
+    torch = _torch()
+    T = _tokens("x", x, router.hidden)
+    _want("x", x, (torch.bfloat16,), (T, router.hidden))
+    if ids is None:
+        ids = torch.empty((T, router.top_k), dtype=torch.int32, device=x.device)
+    if rw is None:
+        rw = torch.empty((T, router.top_k), dtype=torch.float32, device=x.device)
+    _want("ids", ids, (torch.int32,), (T, router.top_k))
+    _want("rw", rw, (torch.float32,), (T, router.top_k))
+    _on_device(x, ids, rw, ws, router.weight, router.bias)
+    if T == 0:
+        return ids, rw
+    if ws is None:
+        ws = router.workspace(T)
+    _want("ws", ws, (torch.uint8,), (ws.numel(),))
+    _check("moeq_router_topk", _lib().moeq_router_topk(ctypes.byref(router._struct), x.data_ptr(), T, ids.data_ptr(),
+                                                       rw.data_ptr(), ws.data_ptr(), ws.numel(), _stream_ptr()))
+    return ids, rw
+
+
+def moe_forward(moe: MoeLayer, x, y=None, ids=None, rw=None, ws=None):
+    """The whole layer on bf16 tokens x [T, H]: (y [T, H] bf16, ids [T, K], route weights [T, K])."""
+    torch = _torch()
+    T = _tokens("x", x, moe.hidden)
+    _want("x", x, (torch.bfloat16,), (T, moe.hidden))
+    if y is None:
+        y = torch.empty((T, moe.hidden), dtype=torch.bfloat16, device=x.device)
+    if ids is None:
+        ids = torch.empty((T, moe.top_k), dtype=torch.int32, device=x.device)
+    if rw is None:
+        rw = torch.empty((T, moe.top_k), dtype=torch.float32, device=x.device)
+    _want("y", y, (torch.bfloat16,), (T, moe.hidden))
+    _want("ids", ids, (torch.int32,), (T, moe.top_k))
+    _want("rw", rw, (torch.float32,), (T, moe.top_k))
+    _on_device(x, y, ids, rw, ws, moe.router.weight)
+    if T == 0:
+        return y, ids, rw
+    if ws is None:
+        ws = moe.workspace(T)
+    _want("ws", ws, (torch.uint8,), (ws.numel(),))
+    _check("moeq_moe_forward", _lib().moeq_moe_forward(*moe._refs, x.data_ptr(), T, y.data_ptr(), ids.data_ptr(),
+                                                       rw.data_ptr(), ws.data_ptr(), ws.numel(), _stream_ptr()))
+    return y, ids, rw
 
 
 def check_device_error(ws, clear=True) -> int:

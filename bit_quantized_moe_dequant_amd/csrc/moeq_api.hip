@@ -480,6 +480,126 @@ int run_prefill_down(const moeq_layer* L, const uint8_t* hq, const uint8_t* hs, 
 int forward(const moeq_layer* L, const void* x, const int32_t* ids, const float* rw, int T, float* y, void* ws,
             const WsLayout& lay, hipStream_t s);
 
+// ---------------------------------------------------------------- router, whole layer
+int check_router(const moeq_router* R) {
+  if (!R) return MOEQ_E_INVAL;
+  if (R->hidden <= 0 || R->n_experts <= 0 || R->top_k < 1 || R->top_k > 16 || R->top_k > R->n_experts)
+    return MOEQ_E_INVAL;
+  if (R->scoring < MOEQ_SCORE_SOFTMAX || R->scoring > MOEQ_SCORE_SQRT_SOFTPLUS) return MOEQ_E_INVAL;
+  if (R->n_experts > 1024 || R->hidden % 8 || R->hidden > 65536) return MOEQ_E_SHAPE;
+  if (!R->weight) return MOEQ_E_INVAL;
+  if (!aligned(R->weight, 16) || (R->bias && !aligned(R->bias, 4))) return MOEQ_E_ALIGN;
+  return MOEQ_OK;
+}
+
+int check_shared(const moeq_layer* L, const moeq_shared* S) {
+  if (!S) return MOEQ_OK;
+  int rc;
+  for (const moeq_weight* w : {&S->gate, &S->up, &S->down}) {
+    if ((rc = check_weight(w, false))) return rc;
+    if (w->fmt != MOEQ_FMT_INT8) return MOEQ_E_FMT;
+    if (w->cols > INT8_MAX_COLS) return MOEQ_E_SHAPE;
+  }
+  for (const moeq_weight* w : {&S->gate, &S->up})
+    if (w->rows != S->inter || w->cols != L->hidden) return MOEQ_E_SHAPE;
+  if (S->down.rows != L->hidden || S->down.cols != S->inter) return MOEQ_E_SHAPE;
+  return MOEQ_OK;
+}
+
+int check_moe(const moeq_layer* L, const moeq_router* R, const moeq_shared* S) {
+  int rc;
+  if ((rc = check_layer(L)) || (rc = check_router(R))) return rc;
+  if (R->hidden != L->hidden || R->n_experts != L->n_experts || R->top_k != L->top_k) return MOEQ_E_SHAPE;
+  return check_shared(L, S);
+}
+
+size_t router_bytes(const moeq_router* R, int T) { return 256 + align_up((size_t)T * R->n_experts * 8, 256); }
+
+RouterParams router_params(const moeq_router* R, const void* x, int T, int32_t* ids, float* rw, double* logits) {
+  RouterParams p;
+  memset(&p, 0, sizeof(p));
+  p.x = (const uint16_t*)x;
+  p.w = (const uint16_t*)R->weight;
+  p.bias = R->bias;
+  p.logits = logits;
+  p.ids = ids;
+  p.rw = rw;
+  p.hidden = R->hidden;
+  p.n_experts = R->n_experts;
+  p.top_k = R->top_k;
+  p.scoring = R->scoring;
+  p.normalize = R->normalize;
+  p.T = T;
+  p.scale = R->scale;
+  return p;
+}
+
+// The routed layer's workspace first (its header holds the error word), then the rest.
+struct MoeLayout {
+  WsLayout routed;
+  size_t logits, ids, rw, y, xq, xs, h, hq, hs, total;
+};
+
+MoeLayout moe_layout(const moeq_layer* L, const moeq_shared* S, int T) {
+  MoeLayout m;
+  m.routed = ws_layout(L, T);
+  size_t off = m.routed.total;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align_up(bytes, 256);
+    return at;
+  };
+  m.logits = take((size_t)T * L->n_experts * 8);
+  m.ids = take((size_t)T * L->top_k * 4);
+  m.rw = take((size_t)T * L->top_k * 4);
+  m.y = take((size_t)T * L->hidden * 4);
+  const size_t I = S ? S->inter : 0, H = S ? L->hidden : 0;
+  m.xq = take(T * H);
+  m.xs = take((size_t)T * 4);
+  m.h = take(T * I * 4);
+  m.hq = take(T * I);
+  m.hs = take((size_t)T * 4);
+  m.total = off;
+  return m;
+}
+
+int moe_forward(const moeq_layer* L, const moeq_router* R, const moeq_shared* Sh, const void* x, int T, void* y,
+                int32_t* ids, float* rw, void* ws, hipStream_t s) {
+  const MoeLayout m = moe_layout(L, Sh, T);
+  uint8_t* base = (uint8_t*)ws;
+  if (!ids) ids = (int32_t*)(base + m.ids);
+  if (!rw) rw = (float*)(base + m.rw);
+  float* y32 = (float*)(base + m.y);
+  int rc = hip_rc(launch_router(router_params(R, x, T, ids, rw, (double*)(base + m.logits)), s));
+  if (rc) return rc;
+  if ((rc = forward(L, x, ids, rw, T, y32, ws, m.routed, s))) return rc;
+  if (!Sh) return hip_rc(launch_to_bf16(y32, (size_t)T * L->hidden, (uint16_t*)y, s));
+  int8_t* xq = (int8_t*)(base + m.xq);
+  int8_t* hq = (int8_t*)(base + m.hq);
+  float* xs = (float*)(base + m.xs);
+  float* hs = (float*)(base + m.hs);
+  float* h = (float*)(base + m.h);
+  if ((rc = hip_rc(launch_quant_int8(0, x, T, L->hidden, xq, xs, s)))) return rc;
+  Int8Params p = int8_params(Sh->gate, 0);
+  const Int8Params up = int8_params(Sh->up, 0);
+  p.w2 = up.w;
+  p.ws2 = up.ws;
+  p.xq = xq;
+  p.xs = xs;
+  p.T = T;
+  p.y = h;
+  if ((rc = hip_rc(launch_gate_up_int8(p, s)))) return rc;
+  if ((rc = hip_rc(launch_quant_int8(1, h, T, Sh->inter, hq, hs, s)))) return rc;
+  p = int8_params(Sh->down, 0);
+  p.xq = hq;
+  p.xs = hs;
+  p.T = T;
+  p.add = y32;
+  p.out_bf16 = 1;
+  p.y = y;
+  return hip_rc(launch_linear_int8(p, s));
+}
+
 // ---------------------------------------------------------------- allocation-free scratch
 // Device memory of moeq_expert_forward_noalloc: a file-scope array that each GPU
 // holds for the life of the process (no hipMalloc on any call). Host code never
@@ -890,6 +1010,40 @@ int moeq_linear_int8_dynamic(const moeq_weight* w, int expert, const void* x, in
   p.out_bf16 = out_type == MOEQ_OUT_BF16;
   p.y = y;
   return hip_rc(launch_linear_int8(p, S(stream)));
+}
+
+size_t moeq_router_workspace_bytes(const moeq_router* R, int T) {
+  if (check_router(R) || T < 0) return 0;
+  return router_bytes(R, T);
+}
+
+int moeq_router_topk(const moeq_router* R, const void* x, int T, int32_t* ids, float* rw, void* ws, size_t ws_bytes,
+                     void* stream) {
+  int rc = check_router(R);
+  if (rc) return rc;
+  if (T < 0 || !x || !ids || !rw) return MOEQ_E_INVAL;
+  if (!aligned(x, 16) || !aligned(ids, 4) || !aligned(rw, 4)) return MOEQ_E_ALIGN;
+  if (!ws || ws_bytes < router_bytes(R, T)) return MOEQ_E_WORKSPACE;
+  if (!aligned(ws, 256)) return MOEQ_E_ALIGN;
+  if (T == 0) return MOEQ_OK;
+  return hip_rc(launch_router(router_params(R, x, T, ids, rw, (double*)((uint8_t*)ws + 256)), S(stream)));
+}
+
+size_t moeq_moe_workspace_bytes(const moeq_layer* L, const moeq_router* R, const moeq_shared* Sh, int T) {
+  if (check_moe(L, R, Sh) || T < 0) return 0;
+  return moe_layout(L, Sh, T).total;
+}
+
+int moeq_moe_forward(const moeq_layer* L, const moeq_router* R, const moeq_shared* Sh, const void* x, int T, void* y,
+                     int32_t* ids, float* rw, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_moe(L, R, Sh);
+  if (rc) return rc;
+  if (T < 0 || !x || !y) return MOEQ_E_INVAL;
+  if (!aligned(x, 16) || !aligned(y, 16) || (ids && !aligned(ids, 4)) || (rw && !aligned(rw, 4))) return MOEQ_E_ALIGN;
+  if (!ws || ws_bytes < moe_layout(L, Sh, T).total) return MOEQ_E_WORKSPACE;
+  if (!aligned(ws, 256)) return MOEQ_E_ALIGN;
+  if (T == 0) return MOEQ_OK;
+  return moe_forward(L, R, Sh, x, T, y, ids, rw, ws, S(stream));
 }
 
 int moeq_check_device_error(void* ws, void* stream, uint32_t* err_host, int clear) {

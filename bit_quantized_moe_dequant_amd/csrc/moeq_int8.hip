@@ -21,6 +21,13 @@ typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
+// The bias and the added term of one output.
+__device__ __forceinline__ float finish(const Int8Params& P, size_t t, int r, float v) {
+  if (P.bias) v += P.bias[r];
+  if (P.add) v += P.add[t * P.rows + r];
+  return v;
+}
+
 __device__ __forceinline__ void store_out(const Int8Params& P, size_t t, int r, float v) {
   if (P.out_bf16) reinterpret_cast<uint16_t*>(P.y)[t * P.rows + r] = (uint16_t)f32_bf16_rne_nan(v);
   else reinterpret_cast<float*>(P.y)[t * P.rows + r] = v;
@@ -121,9 +128,10 @@ __global__ __launch_bounds__(Q_THREADS) void k_quant_int8(const void* x, int K, 
 // contiguous runs of K steps and their int32 partials meet in LDS.
 constexpr int S_WAVES = 8;
 
-template <int NT, int U>
+// MATS = 2: a gate/up pair, h = silu(gate) * up in fp32.
+template <int MATS, int NT, int U>
 __global__ __launch_bounds__(64 * S_WAVES) void k_int8_few(Int8Params P) {
-  __shared__ int32_t red[S_WAVES][16 * NT][17];
+  __shared__ int32_t red[MATS][S_WAVES][16 * NT][17];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
@@ -133,45 +141,62 @@ __global__ __launch_bounds__(64 * S_WAVES) void k_int8_few(Int8Params P) {
   const int steps = (K + 63) / 64;
   const int spw = (steps + S_WAVES - 1) / S_WAVES;
   const int s0 = wave * spw, s1 = min(s0 + spw, steps);
-  const int8_t* wr = P.w + (size_t)min(r0 + n, P.rows - 1) * K;
+  const int8_t* wr[MATS];
+#pragma unroll
+  for (int m = 0; m < MATS; m++) wr[m] = (m ? P.w2 : P.w) + (size_t)min(r0 + n, P.rows - 1) * K;
   const int8_t* xr[NT];
 #pragma unroll
   for (int t = 0; t < NT; t++) xr[t] = P.xq + (size_t)min(t0 + 16 * t + n, P.T - 1) * K;
-  i32x4 acc[NT];
+  i32x4 acc[MATS][NT];
 #pragma unroll
-  for (int t = 0; t < NT; t++) acc[t] = i32x4{0, 0, 0, 0};
+  for (int m = 0; m < MATS; m++)
+#pragma unroll
+    for (int t = 0; t < NT; t++) acc[m][t] = i32x4{0, 0, 0, 0};
   for (int s = s0; s < s1; s += U) {
-    u32x4 wv[U], xv[U][NT];
+    u32x4 wv[U][MATS], xv[U][NT];
     // K steps past the end and the last step's bytes past K: the last 16 bytes again
     // (in bounds), with zeros in the weights' place
 #pragma unroll
-    for (int u = 0; u < U; u++) wv[u] = ld16(wr + min(64 * (s + u) + 16 * g, K - 16));
+    for (int u = 0; u < U; u++)
+#pragma unroll
+      for (int m = 0; m < MATS; m++) wv[u][m] = ld16(wr[m] + min(64 * (s + u) + 16 * g, K - 16));
 #pragma unroll
     for (int u = 0; u < U; u++)
 #pragma unroll
       for (int t = 0; t < NT; t++) xv[u][t] = ld16(xr[t] + min(64 * (s + u) + 16 * g, K - 16));
 #pragma unroll
     for (int u = 0; u < U; u++) {
-      if (s + u >= s1 || 64 * (s + u) + 16 * g >= K) wv[u] = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int t = 0; t < NT; t++)
-        acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, wv[u]),
-                                                        __builtin_bit_cast(i32x4, xv[u][t]), acc[t], 0, 0, 0);
+      for (int m = 0; m < MATS; m++) {
+        if (s + u >= s1 || 64 * (s + u) + 16 * g >= K) wv[u][m] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int t = 0; t < NT; t++)
+          acc[m][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, wv[u][m]),
+                                                             __builtin_bit_cast(i32x4, xv[u][t]), acc[m][t], 0, 0, 0);
+      }
     }
   }
 #pragma unroll
-  for (int t = 0; t < NT; t++)
+  for (int m = 0; m < MATS; m++)
 #pragma unroll
-    for (int r = 0; r < 4; r++) red[wave][16 * t + n][4 * g + r] = acc[t][r];
+    for (int t = 0; t < NT; t++)
+#pragma unroll
+      for (int r = 0; r < 4; r++) red[m][wave][16 * t + n][4 * g + r] = acc[m][t][r];
   __syncthreads();
   for (int i = threadIdx.x; i < 256 * NT; i += 64 * S_WAVES) {
     const int tk = i >> 4, c = i & 15;
     if (t0 + tk < P.T && r0 + c < P.rows) {
-      int v = 0;
+      int v[MATS];
 #pragma unroll
-      for (int w = 0; w < S_WAVES; w++) v += red[w][tk][c];
-      float f = (float)v * P.xs[t0 + tk] * P.ws[r0 + c];
-      if (P.bias) f += P.bias[r0 + c];
+      for (int m = 0; m < MATS; m++) {
+        v[m] = 0;
+#pragma unroll
+        for (int w = 0; w < S_WAVES; w++) v[m] += red[m][w][tk][c];
+      }
+      const float xs = P.xs[t0 + tk];
+      float f = (float)v[0] * xs * P.ws[r0 + c];
+      if constexpr (MATS == 2) f = silu_mul(f, (float)v[1] * xs * P.ws2[r0 + c]);
+      else f = finish(P, t0 + tk, r0 + c, f);
       store_out(P, t0 + tk, r0 + c, f);
     }
   }
@@ -270,9 +295,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_tiled(Int8Params P) {
 #pragma unroll
         for (int e = 0; e < 4; e++) {
           if (t < P.T && r + e < P.rows) {
-            float f = (float)acc[i][j][4 * q + e] * xs * P.ws[r + e];
-            if (P.bias) f += P.bias[r + e];
-            store_out(P, t, r + e, f);
+            store_out(P, t, r + e, finish(P, t, r + e, (float)acc[i][j][4 * q + e] * xs * P.ws[r + e]));
           }
         }
       }
@@ -293,10 +316,10 @@ hipError_t go_tiled(const Int8Params& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int NT, int U>
+template <int MATS, int NT, int U>
 hipError_t go_few(const Int8Params& p, hipStream_t s) {
   const dim3 g((unsigned)((p.rows + 15) / 16), (unsigned)((p.T + 16 * NT - 1) / (16 * NT)));
-  hipLaunchKernelGGL((k_int8_few<NT, U>), g, dim3(64 * S_WAVES), 0, s, p);
+  hipLaunchKernelGGL((k_int8_few<MATS, NT, U>), g, dim3(64 * S_WAVES), 0, s, p);
   return hipGetLastError();
 }
 
@@ -317,12 +340,38 @@ hipError_t launch_dequant_int8(const int8_t* w, const float* ws, int rows, int c
 
 hipError_t launch_linear_int8(const Int8Params& p, hipStream_t s) {
   if (p.T < 1 || p.rows < 1 || p.cols < 16 || p.cols % 16 || p.cols > INT8_MAX_COLS) return hipErrorInvalidValue;
-  if (p.T <= 16) return go_few<1, 8>(p, s);
-  if (p.T <= 64) return go_few<4, 4>(p, s);
-  if (p.T <= 128) return go_few<8, 2>(p, s);
+  if (p.T <= 16) return go_few<1, 1, 8>(p, s);
+  if (p.T <= 64) return go_few<1, 4, 4>(p, s);
+  if (p.T <= 128) return go_few<1, 8, 2>(p, s);
   const long tiles = (long)((p.rows + 255) / 256) * ((p.T + 255) / 256);
   if (tiles >= 200) return go_tiled<2, 4, 4, 2>(p, s);
   return go_tiled<2, 2, 2, 2>(p, s);
+}
+
+hipError_t launch_gate_up_int8(const Int8Params& p, hipStream_t s) {
+  if (p.T < 1 || p.rows < 1 || p.cols < 16 || p.cols % 16 || p.cols > INT8_MAX_COLS) return hipErrorInvalidValue;
+  // token tiles are grid rows
+  for (int t0 = 0; t0 < p.T; t0 += 1 << 20) {
+    Int8Params q = p;
+    q.T = p.T - t0 < (1 << 20) ? p.T - t0 : 1 << 20;
+    q.xq += (size_t)t0 * p.cols;
+    q.xs += t0;
+    q.y = (float*)p.y + (size_t)t0 * p.rows;
+    const hipError_t e = q.T <= 16 ? go_few<2, 1, 4>(q, s) : go_few<2, 4, 2>(q, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+__global__ __launch_bounds__(256) void k_to_bf16(const float* x, size_t n, uint16_t* y) {
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256)
+    y[i] = (uint16_t)f32_bf16_rne_nan(x[i]);
+}
+
+hipError_t launch_to_bf16(const float* x, size_t n, uint16_t* y, hipStream_t s) {
+  const size_t b = (n + 255) / 256;
+  hipLaunchKernelGGL(k_to_bf16, dim3((unsigned)(b < 4096 ? b : 4096)), dim3(256), 0, s, x, n, y);
+  return hipGetLastError();
 }
 
 }  // namespace moeq

@@ -112,8 +112,25 @@ struct Int8Params {
   const int8_t* xq;   // [T][cols], 16-byte aligned
   const float* xs;    // [T]
   const float* bias;  // [rows] or null
+  const float* add;   // fp32 [T][rows] added to the product, or null
   void* y;            // fp32 or bf16 [T][rows]
   int rows, cols, T, out_bf16;
+  // gate/up pair (launch_gate_up_int8): w, ws hold the gate, these the up matrix
+  const int8_t* w2;
+  const float* ws2;
+};
+
+// Scores of the router, in the order of MOEQ_SCORE_*.
+enum { SCORE_SOFTMAX = 0, SCORE_SIGMOID = 1, SCORE_SQRT_SOFTPLUS = 2 };
+struct RouterParams {
+  const uint16_t* x;  // bf16 [T][hidden]
+  const uint16_t* w;  // bf16 [n_experts][hidden]
+  const float* bias;  // [n_experts] or null
+  double* logits;     // [T][n_experts] workspace
+  int32_t* ids;       // [T][top_k]
+  float* rw;          // [T][top_k]
+  int hidden, n_experts, top_k, scoring, normalize, T;
+  float scale;
 };
 
 // Launchers (return hipError_t of the launch).
@@ -186,6 +203,11 @@ hipError_t launch_nv4_to_mx4(const uint8_t* nib, const uint8_t* e4m3, const floa
 // Per-token int8 codes and scales of bf16 (in_f32 = 0) or fp32 rows; K % 16 == 0.
 hipError_t launch_quant_int8(int in_f32, const void* x, int T, int K, int8_t* q, float* scale, hipStream_t s);
 hipError_t launch_linear_int8(const Int8Params& p, hipStream_t s);
+// h[T][rows] (fp32, p.y) = silu(gate) * up of an INT8 gate/up pair, as launch_linear_int8 for each.
+hipError_t launch_gate_up_int8(const Int8Params& p, hipStream_t s);
+hipError_t launch_router(const RouterParams& p, hipStream_t s);
+// y bf16 = x fp32, n values.
+hipError_t launch_to_bf16(const float* x, size_t n, uint16_t* y, hipStream_t s);
 hipError_t launch_dequant_int8(const int8_t* w, const float* ws, int rows, int cols, float* out, hipStream_t s);
 
 // Chunk geometry: weights per 16-byte chunk; lanes per row and chunks per lane.

@@ -354,6 +354,59 @@ size_t moeq_linear_int8_workspace_bytes(int T, int cols);
 int moeq_linear_int8_dynamic(const moeq_weight* w, int expert, const void* x, int T, const float* bias, int out_type,
                              void* y, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------ router, whole layer */
+
+/* Scores s of the logits z: softmax over the experts, 1 / (1 + e^-z), or
+ * sqrt(log(1 + e^z)). */
+#define MOEQ_SCORE_SOFTMAX 0
+#define MOEQ_SCORE_SIGMOID 1
+#define MOEQ_SCORE_SQRT_SOFTPLUS 2
+
+typedef struct moeq_router {
+  int hidden;         /* H, a multiple of 8, at most 65536 */
+  int n_experts;      /* E, 1..1024 */
+  int top_k;          /* K, 1..16, at most E */
+  int scoring;        /* MOEQ_SCORE_* */
+  int normalize;      /* != 0: the K chosen scores are divided by their sum */
+  float scale;        /* factor of the route weights */
+  const void* weight; /* bf16 [E][H], 16-byte aligned */
+  const float* bias;  /* fp32 [E], added to the scores for the choice only, or NULL */
+} moeq_router;
+
+/* The shared expert beside the routed ones: three MOEQ_FMT_INT8 tensors (expert 0 of
+ * each), gate and up [inter][hidden], down [hidden][inter]; inter a multiple of 16. */
+typedef struct moeq_shared {
+  int inter;
+  moeq_weight gate, up, down;
+} moeq_shared;
+
+/* The K experts with the largest s + bias of every token, in falling order (ties: the
+ * lower id first; a NaN counts below every number), and their weights s * scale, or
+ * s / (sum of the K) * scale. The logits W x are sums of exact products in fp64, and so
+ * are scores and sums: the choice does not depend on an order of summation beyond
+ * fp64's. x bf16 [T][H], 16-byte aligned; ids int32 [T][K] (always distinct and inside
+ * [0, E)) and rw fp32 [T][K] overwritten: what moeq_expert_forward takes. A sum of 0
+ * gives weights 0. ws: moeq_router_workspace_bytes(R, T) bytes, 256-byte aligned,
+ * zero-filled once before first use (or passed to moeq_workspace_init), not shared
+ * with an overlapping call. T == 0 is a no-op. */
+size_t moeq_router_workspace_bytes(const moeq_router* R, int T);
+int moeq_router_topk(const moeq_router* R, const void* x, int T, int32_t* ids, float* rw, void* ws, size_t ws_bytes,
+                     void* stream);
+
+/* The whole layer for x[T][H] (bf16): y = bf16(routed + shared), with the routed
+ * experts of moeq_router_topk as moeq_expert_forward computes them and the shared
+ * expert Ds (silu(Gs x) * (Us x)) on the INT8 linears: x and the intermediate h
+ * (fp32) quantised per token as by moeq_quantize_int8, sums in fp32, one rounding to
+ * bf16 at the end. S may be NULL (no shared expert). R and L agree on hidden,
+ * n_experts and top_k. ids and rw (int32 / fp32 [T][K]) receive the routing, or NULL.
+ * ws: moeq_moe_workspace_bytes bytes, 256-byte aligned, zero-filled once before first
+ * use (or passed to moeq_workspace_init), not shared with an overlapping call; its
+ * first 4 bytes hold the device error word. x, y 16-byte aligned. Any T; made for a
+ * few tokens. T == 0 is a no-op. */
+size_t moeq_moe_workspace_bytes(const moeq_layer* L, const moeq_router* R, const moeq_shared* S, int T);
+int moeq_moe_forward(const moeq_layer* L, const moeq_router* R, const moeq_shared* S, const void* x, int T, void* y,
+                     int32_t* ids, float* rw, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronise `stream`, then read (and with clear != 0, zero) the device error word. */
 int moeq_check_device_error(void* ws, void* stream, uint32_t* err_host, int clear);
 

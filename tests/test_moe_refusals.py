@@ -1,0 +1,98 @@
+"""Refusals of the router and of the whole layer, on the CPU."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+import bit_quantized_moe_dequant_amd as mq
+
+pytestmark = pytest.mark.skipif(not os.path.exists(mq.library_path()), reason="libmoeq.so not built")
+
+P = ctypes.c_void_p
+A = ctypes.addressof
+
+
+def router(H=1024, E=8, K=2, scoring=0, w=0x100000, bias=0):
+    return mq.MoeqRouter(H, E, K, scoring, 1, 1.0, w, bias)
+
+
+def layer(H=1024, I=512, E=8, K=2):
+    mx = lambda r, c: mq.MoeqWeight(1, r, c, E, 0x10000, 1 << 20, 0x20000, 1 << 20, 0, 0)
+    return mq.MoeqLayer(H, I, E, K, mx(I, H), mx(I, H), mx(H, I))
+
+
+def shared(H=1024, I=256, fmt=9):
+    w = lambda r, c: mq.MoeqWeight(fmt, r, c, 1, 0x10000, 1 << 20, 0x20000, 1 << 20, 0, 0)
+    return mq.MoeqShared(I, w(I, H), w(I, H), w(H, I))
+
+
+def topk(r, x=0x200000, T=3, ids=0x300000, rw=0x400000, ws=0x500000, n=1 << 20):
+    return mq._lib().moeq_router_topk(ctypes.byref(r), P(x), T, P(ids), P(rw), P(ws), n, None)
+
+
+def forward(L=None, R=None, S=None, x=0x200000, T=3, y=0x300000, ids=0, rw=0, ws=0x500000, n=1 << 30):
+    L, R, S = L or layer(), R or router(), S or shared()
+    return mq._lib().moeq_moe_forward(A(L), A(R), A(S), P(x), T, P(y), P(ids), P(rw), P(ws), n, None)
+
+
+def test_router_refusals():
+    assert topk(router(H=0)) == -1 and topk(router(E=0)) == -1 and topk(router(K=0)) == -1
+    assert topk(router(K=9)) == -1 and topk(router(E=64, K=17)) == -1
+    assert topk(router(scoring=3)) == -1 and topk(router(scoring=-1)) == -1
+    assert topk(router(H=1020)) == -4 and topk(router(E=1025)) == -4 and topk(router(H=65544)) == -4
+    assert topk(router(w=0)) == -1 and topk(router(w=0x100008)) == -3 and topk(router(bias=0x600002)) == -3
+    r = router()
+    assert topk(r, x=0) == -1 and topk(r, ids=0) == -1 and topk(r, rw=0) == -1 and topk(r, T=-1) == -1
+    assert topk(r, x=0x200008) == -3 and topk(r, ids=0x300002) == -3 and topk(r, rw=0x400002) == -3
+    assert topk(r, ws=0) == -5 and topk(r, n=16) == -5 and topk(r, ws=0x500010) == -3
+    assert topk(r, T=0) == 0
+    lib = mq._lib()
+    assert lib.moeq_router_workspace_bytes(ctypes.byref(r), 3) > 3 * 8 * 8
+    assert lib.moeq_router_workspace_bytes(ctypes.byref(router(H=4)), 3) == 0
+
+
+def test_layer_refusals():
+    assert forward(T=0) == 0
+    assert forward(R=router(H=512)) == -4 and forward(R=router(E=9)) == -4 and forward(R=router(K=3)) == -4
+    assert forward(R=router(w=0)) == -1
+    assert forward(S=shared(H=512)) == -4 and forward(S=shared(fmt=6)) == -2 and forward(S=shared(I=40)) == -4
+    bad = shared()
+    bad.down.rows = 512
+    assert forward(S=bad) == -4
+    bad = shared()
+    bad.inter = 128
+    assert forward(S=bad) == -4
+    bad = shared()
+    bad.up.data = 0
+    assert forward(S=bad) == -1
+    bad = layer()
+    bad.down.fmt = 9
+    assert forward(L=bad) == -2
+    assert forward(x=0) == -1 and forward(y=0) == -1 and forward(T=-1) == -1
+    assert forward(x=0x200008) == -3 and forward(y=0x300008) == -3 and forward(ids=0x600002) == -3
+    assert forward(ws=0) == -5 and forward(n=1000) == -5 and forward(ws=0x500010) == -3
+    lib = mq._lib()
+    L, R, S = layer(), router(), shared()
+    one = lib.moeq_moe_workspace_bytes(A(L), A(R), A(S), 1)
+    assert lib.moeq_workspace_bytes(ctypes.byref(L), 1) < one < lib.moeq_moe_workspace_bytes(A(L), A(R), A(S), 64)
+    assert lib.moeq_moe_workspace_bytes(A(L), A(R), None, 1) > 0
+    assert lib.moeq_moe_workspace_bytes(A(L), None, A(S), 1) == 0
+
+
+def test_binding_refusals():
+    w = torch.zeros((8, 64), dtype=torch.bfloat16)
+    for bad in (lambda: mq.Router(w.float(), 2), lambda: mq.Router(w[0], 2), lambda: mq.Router(w[:, ::2], 2),
+                lambda: mq.Router(w, 2, scoring="relu"), lambda: mq.Router(w, 2, bias=torch.zeros(7)),
+                lambda: mq.Router(w, 2, bias=torch.zeros(8, dtype=torch.float64))):
+        with pytest.raises(ValueError):
+            bad()
+    r = mq.Router(w, 2)
+    x = torch.zeros((3, 64), dtype=torch.bfloat16)
+    for bad in (lambda: mq.router_topk(r, x[:, :32]), lambda: mq.router_topk(r, x.float()),
+                lambda: mq.router_topk(r, x, ids=torch.zeros((3, 2), dtype=torch.int64)),
+                lambda: mq.router_topk(r, x, rw=torch.zeros((2, 2)))):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(ValueError, match="GPU"):
+        mq.router_topk(r, x)
