@@ -219,6 +219,7 @@ class Weight:
                  expert_stride=None, scale_expert_stride=None):
         self.fmt, self.rows, self.cols, self.n_experts = int(fmt), int(rows), int(cols), int(n_experts)
         self.data, self.scales, self.scale2, self.grid = data, scales, scale2, grid
+        self._made = None
         self.expert_stride = expert_stride if expert_stride is not None else _round16(plane_bytes(fmt, rows, cols, 0))
         self.scale_expert_stride = (scale_expert_stride if scale_expert_stride is not None
                                     else _round16(plane_bytes(fmt, rows, cols, 1)))
@@ -245,6 +246,16 @@ class Weight:
                           self.scales.data_ptr(), self.scale_expert_stride,
                           0 if self.scale2 is None else self.scale2.data_ptr(),
                           0 if self.grid is None else self.grid.data_ptr())
+
+    def _ref(self):
+        """byref of this weight's descriptor, made again when a field has changed."""
+        now = (self.fmt, self.rows, self.cols, self.n_experts, self.data.data_ptr(), self.expert_stride,
+               self.scales.data_ptr(), self.scale_expert_stride, self.scale2, self.grid)
+        if now != self._made:
+            self._struct = self.struct()
+            self._by = ctypes.byref(self._struct)
+            self._made = now
+        return self._by
 
     def algorithmic_bytes(self) -> int:
         """Bytes of one expert tensor at the format's bits per weight."""
@@ -489,13 +500,44 @@ def quantize_mxfp8(x, q=None, e=None):
     return q, e
 
 
+# The calls below are made once per layer and token, so their argument checks are written
+# for the well-formed case: attributes only, no temporaries; _want says what is wrong.
+
+def _need(name, t, dtypes, shape):
+    """_want, quick where nothing is wrong."""
+    try:
+        if t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _want(name, t, dtypes, shape)
+
+
+_GPU = None  # (current device, raw stream of a device, the dtypes of the checks)
+
+
+def _gpu():
+    global _GPU
+    if _GPU is None:
+        torch = _torch()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            raw = lambda dev: torch.cuda.current_stream(dev).cuda_stream  # noqa: E731
+        _GPU = (torch.cuda.current_device, raw, (torch.bfloat16,), (torch.int8,), (torch.float32,), (torch.int32,),
+                (torch.uint8,))
+    return _GPU
+
+
 def _on_device(*ts):
-    """The tensors are on the current GPU (the library launches there)."""
-    _require_cuda(*ts)
-    dev = _torch().cuda.current_device()
+    """The current GPU's index, if all tensors are on it (the library launches there)."""
     for t in ts:
-        if t is not None and t.device.index != dev:
+        if t is not None and not t.is_cuda:
+            raise ValueError("tensor must be on the GPU")
+    dev = _gpu()[0]()
+    for t in ts:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    return dev
 
 
 def quantize_int8(x, q=None, scale=None):
@@ -504,46 +546,52 @@ def quantize_int8(x, q=None, scale=None):
     if x is None or len(x.shape) != 2:
         raise ValueError("x: expected a [T, K] tensor")
     T, K = x.shape
-    _want("x", x, (torch.bfloat16, torch.float32), (T, K))
+    f32 = x.dtype == torch.float32
+    _need("x", x, (torch.bfloat16, torch.float32), (T, K))
     if q is None:
         q = torch.empty((T, K), dtype=torch.int8, device=x.device)
     if scale is None:
         scale = torch.empty((T,), dtype=torch.float32, device=x.device)
-    _want("q", q, (torch.int8,), (T, K))
-    _want("scale", scale, (torch.float32,), (T,))
-    _on_device(x, q, scale)
+    gpu = _gpu()
+    _need("q", q, gpu[3], (T, K))
+    _need("scale", scale, gpu[4], (T,))
+    dev = _on_device(x, q, scale)
     if T == 0:
         return q, scale
-    fn = _lib().moeq_quantize_int8_f32 if x.dtype == torch.float32 else _lib().moeq_quantize_int8
-    _check("moeq_quantize_int8", fn(x.data_ptr(), T, K, q.data_ptr(), scale.data_ptr(), _stream_ptr()))
+    lib = _LIB or _lib()
+    _check("moeq_quantize_int8", (lib.moeq_quantize_int8_f32 if f32 else lib.moeq_quantize_int8)(
+        x.data_ptr(), T, K, q.data_ptr(), scale.data_ptr(), gpu[1](dev)))
     return q, scale
 
 
 def _int8_out(w, T, bias, y, out_dtype, device):
     torch = _torch()
     if bias is not None:
-        _want("bias", bias, (torch.float32,), (w.rows,))
+        _need("bias", bias, (torch.float32,), (w.rows,))
     if y is None:
         y = torch.empty((T, w.rows), dtype=out_dtype or torch.bfloat16, device=device)
-    _want("y", y, (torch.float32, torch.bfloat16) if out_dtype is None else (out_dtype,), (T, w.rows))
-    return y, OUT_BF16 if y.dtype == torch.bfloat16 else OUT_F32
+    _need("y", y, (torch.float32, torch.bfloat16) if out_dtype is None else (out_dtype,), (T, w.rows))
+    if y.dtype == torch.bfloat16:
+        return y, OUT_BF16
+    if y.dtype == torch.float32:
+        return y, OUT_F32
+    raise ValueError(f"out_dtype: {y.dtype}, expected torch.float32 or torch.bfloat16")
 
 
 def linear_int8(w: Weight, xq, xs, expert: int = 0, bias=None, y=None, out_dtype=None):
     """y [T, rows] = xs * scale * (xq W^T) (+ bias) of int8 tokens (quantize_int8) and an
     INT8 weight; bf16 unless y or out_dtype says fp32."""
-    torch = _torch()
     T = _tokens("xq", xq, w.cols)
-    _want("xq", xq, (torch.int8,), (T, w.cols))
-    _want("xs", xs, (torch.float32,), (T,))
+    gpu = _gpu()
+    _need("xq", xq, gpu[3], (T, w.cols))
+    _need("xs", xs, gpu[4], (T,))
     y, out = _int8_out(w, T, bias, y, out_dtype, xq.device)
-    s = w.struct()
-    _on_device(xq, xs, bias, y, w.data, w.scales)
+    dev = _on_device(xq, xs, bias, y, w.data, w.scales)
     if T == 0:
         return y
-    _check("moeq_linear_int8", _lib().moeq_linear_int8(ctypes.byref(s), expert, xq.data_ptr(), xs.data_ptr(), T,
-                                                       None if bias is None else bias.data_ptr(), out, y.data_ptr(),
-                                                       _stream_ptr()))
+    _check("moeq_linear_int8", (_LIB or _lib()).moeq_linear_int8(
+        w._ref(), expert, xq.data_ptr(), xs.data_ptr(), T, None if bias is None else bias.data_ptr(), out,
+        y.data_ptr(), gpu[1](dev)))
     return y
 
 
@@ -555,28 +603,27 @@ def linear_int8_workspace(T: int, cols: int, device="cuda"):
         raise MoeqError("moeq_linear_int8_workspace_bytes", -4)
     ws = torch.empty(n + 256, dtype=torch.uint8, device=device)
     off = (-ws.data_ptr()) % 256
-    return ws[off:off + n]
+    return ws[off:off + n] if off else ws
 
 
 def linear_int8_dynamic(w: Weight, x, expert: int = 0, bias=None, y=None, out_dtype=None, ws=None):
     """linear_int8 from bf16 tokens x [T, cols], quantised within the call. Without ws the
     workspace is allocated for the call from torch's caching allocator (on the current
     stream, so calls on different streams never share one)."""
-    torch = _torch()
     T = _tokens("x", x, w.cols)
-    _want("x", x, (torch.bfloat16,), (T, w.cols))
+    gpu = _gpu()
+    _need("x", x, gpu[2], (T, w.cols))
     y, out = _int8_out(w, T, bias, y, out_dtype, x.device)
-    _on_device(x, bias, y, ws, w.data, w.scales)
+    dev = _on_device(x, bias, y, ws, w.data, w.scales)
     if T == 0:
         return y
     if ws is None:
         ws = linear_int8_workspace(T, w.cols, x.device)
-    _want("ws", ws, (torch.uint8,), (ws.numel(),))
-    s = w.struct()
-    _check("moeq_linear_int8_dynamic",
-           _lib().moeq_linear_int8_dynamic(ctypes.byref(s), expert, x.data_ptr(), T,
-                                           None if bias is None else bias.data_ptr(), out, y.data_ptr(),
-                                           ws.data_ptr(), ws.numel(), _stream_ptr()))
+    n = ws.numel()
+    _need("ws", ws, gpu[6], (n,))
+    _check("moeq_linear_int8_dynamic", (_LIB or _lib()).moeq_linear_int8_dynamic(
+        w._ref(), expert, x.data_ptr(), T, None if bias is None else bias.data_ptr(), out, y.data_ptr(),
+        ws.data_ptr(), n, gpu[1](dev)))
     return y
 
 
@@ -601,11 +648,12 @@ class Router:
         self._struct = MoeqRouter(self.hidden, self.n_experts, self.top_k, SCORE_BY_NAME[scoring],
                                   int(self.normalize), self.scale, weight.data_ptr(),
                                   0 if bias is None else bias.data_ptr())
-        self._ws = _Workspaces(lambda T: _lib().moeq_router_workspace_bytes(ctypes.byref(self._struct), T))
+        self._by = ctypes.byref(self._struct)
+        self._ws = _Workspaces(lambda T: _lib().moeq_router_workspace_bytes(self._by, T))
 
     def workspace(self, T: int):
         """An initialised workspace for T tokens; the current stream's own (kept per stream)."""
-        return self._ws.get(T, self.weight.device)
+        return self._ws.get(T, self.weight.device, _stream_ptr().value or 0)
 
 
 class SharedExpert:
@@ -633,7 +681,7 @@ class MoeLayer:
 
     def workspace(self, T: int):
         """An initialised workspace for T tokens; the current stream's own (kept per stream)."""
-        return self._ws.get(T, self.router.weight.device)
+        return self._ws.get(T, self.router.weight.device, _stream_ptr().value or 0)
 
 
 class _Workspaces:
@@ -645,11 +693,10 @@ class _Workspaces:
     def __init__(self, need):
         self.need, self.kept = need, {}
 
-    def get(self, T, device):
-        torch = _torch()
-        if torch.cuda.is_current_stream_capturing():
+    def get(self, T, device, stream):
+        if _torch().cuda.is_current_stream_capturing():
             return self._make(T, device)
-        key = (torch.cuda.current_stream().cuda_stream, T)
+        key = (stream, T)
         ws = self.kept.get(key)
         if ws is None:
             ws = self.kept[key] = self._make(T, device)
@@ -668,48 +715,52 @@ class _Workspaces:
 
 def router_topk(router: Router, x, ids=None, rw=None, ws=None):
     """(ids [T, K] int32, route weights [T, K] fp32) of bf16 tokens x [T, H]."""
-    torch = _torch()
     T = _tokens("x", x, router.hidden)
-    _want("x", x, (torch.bfloat16,), (T, router.hidden))
+    gpu = _gpu()
+    _need("x", x, gpu[2], (T, router.hidden))
     if ids is None:
-        ids = torch.empty((T, router.top_k), dtype=torch.int32, device=x.device)
+        ids = _torch().empty((T, router.top_k), dtype=gpu[5][0], device=x.device)
     if rw is None:
-        rw = torch.empty((T, router.top_k), dtype=torch.float32, device=x.device)
-    _want("ids", ids, (torch.int32,), (T, router.top_k))
-    _want("rw", rw, (torch.float32,), (T, router.top_k))
-    _on_device(x, ids, rw, ws, router.weight, router.bias)
+        rw = _torch().empty((T, router.top_k), dtype=gpu[4][0], device=x.device)
+    _need("ids", ids, gpu[5], (T, router.top_k))
+    _need("rw", rw, gpu[4], (T, router.top_k))
+    dev = _on_device(x, ids, rw, ws, router.weight, router.bias)
     if T == 0:
         return ids, rw
+    stream = gpu[1](dev)
     if ws is None:
-        ws = router.workspace(T)
-    _want("ws", ws, (torch.uint8,), (ws.numel(),))
-    _check("moeq_router_topk", _lib().moeq_router_topk(ctypes.byref(router._struct), x.data_ptr(), T, ids.data_ptr(),
-                                                       rw.data_ptr(), ws.data_ptr(), ws.numel(), _stream_ptr()))
+        ws = router._ws.get(T, x.device, stream)
+    n = ws.numel()
+    _need("ws", ws, gpu[6], (n,))
+    _check("moeq_router_topk", (_LIB or _lib()).moeq_router_topk(
+        router._by, x.data_ptr(), T, ids.data_ptr(), rw.data_ptr(), ws.data_ptr(), n, stream))
     return ids, rw
 
 
 def moe_forward(moe: MoeLayer, x, y=None, ids=None, rw=None, ws=None):
     """The whole layer on bf16 tokens x [T, H]: (y [T, H] bf16, ids [T, K], route weights [T, K])."""
-    torch = _torch()
     T = _tokens("x", x, moe.hidden)
-    _want("x", x, (torch.bfloat16,), (T, moe.hidden))
+    gpu = _gpu()
+    _need("x", x, gpu[2], (T, moe.hidden))
     if y is None:
-        y = torch.empty((T, moe.hidden), dtype=torch.bfloat16, device=x.device)
+        y = _torch().empty((T, moe.hidden), dtype=gpu[2][0], device=x.device)
     if ids is None:
-        ids = torch.empty((T, moe.top_k), dtype=torch.int32, device=x.device)
+        ids = _torch().empty((T, moe.top_k), dtype=gpu[5][0], device=x.device)
     if rw is None:
-        rw = torch.empty((T, moe.top_k), dtype=torch.float32, device=x.device)
-    _want("y", y, (torch.bfloat16,), (T, moe.hidden))
-    _want("ids", ids, (torch.int32,), (T, moe.top_k))
-    _want("rw", rw, (torch.float32,), (T, moe.top_k))
-    _on_device(x, y, ids, rw, ws, moe.router.weight)
+        rw = _torch().empty((T, moe.top_k), dtype=gpu[4][0], device=x.device)
+    _need("y", y, gpu[2], (T, moe.hidden))
+    _need("ids", ids, gpu[5], (T, moe.top_k))
+    _need("rw", rw, gpu[4], (T, moe.top_k))
+    dev = _on_device(x, y, ids, rw, ws, moe.router.weight)
     if T == 0:
         return y, ids, rw
+    stream = gpu[1](dev)
     if ws is None:
-        ws = moe.workspace(T)
-    _want("ws", ws, (torch.uint8,), (ws.numel(),))
-    _check("moeq_moe_forward", _lib().moeq_moe_forward(*moe._refs, x.data_ptr(), T, y.data_ptr(), ids.data_ptr(),
-                                                       rw.data_ptr(), ws.data_ptr(), ws.numel(), _stream_ptr()))
+        ws = moe._ws.get(T, x.device, stream)
+    n = ws.numel()
+    _need("ws", ws, gpu[6], (n,))
+    _check("moeq_moe_forward", (_LIB or _lib()).moeq_moe_forward(
+        *moe._refs, x.data_ptr(), T, y.data_ptr(), ids.data_ptr(), rw.data_ptr(), ws.data_ptr(), n, stream))
     return y, ids, rw
 
 

@@ -126,10 +126,8 @@ __global__ __launch_bounds__(Q_THREADS) void k_quant_int8(const void* x, int K, 
 // operand B 16 tokens, so a lane ends with four consecutive channels of one token.
 // A work-group takes 16 weight rows and NT tiles of 16 tokens; its waves take
 // contiguous runs of K steps and their int32 partials meet in LDS.
-constexpr int S_WAVES = 8;
-
 // MATS = 2: a gate/up pair, h = silu(gate) * up in fp32.
-template <int MATS, int NT, int U>
+template <int MATS, int NT, int U, int S_WAVES>
 __global__ __launch_bounds__(64 * S_WAVES) void k_int8_few(Int8Params P) {
   __shared__ int32_t red[MATS][S_WAVES][16 * NT][17];
   const int lane = threadIdx.x & 63;
@@ -202,54 +200,131 @@ __global__ __launch_bounds__(64 * S_WAVES) void k_int8_few(Int8Params P) {
   }
 }
 
+// Four consecutive channels r .. r + 3 of token t from their sums.
+__device__ __forceinline__ void store4(const Int8Params& P, int t, int r, float xs, int v0, int v1, int v2, int v3) {
+  if (t >= P.T || r >= P.rows) return;
+  const int v[4] = {v0, v1, v2, v3};
+  if (P.vec4) {  // rows a multiple of 4 and aligned outputs: all four exist, one store
+    float f[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++) f[e] = finish(P, t, r + e, (float)v[e] * xs * P.ws[r + e]);
+    if (P.out_bf16) {
+      const u32x2 o = {f32_bf16_rne_nan(f[0]) | (f32_bf16_rne_nan(f[1]) << 16),
+                       f32_bf16_rne_nan(f[2]) | (f32_bf16_rne_nan(f[3]) << 16)};
+      *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(P.y) + (size_t)t * P.rows + r) = o;
+    } else {
+      const u32x4 o = {f2u(f[0]), f2u(f[1]), f2u(f[2]), f2u(f[3])};
+      *reinterpret_cast<u32x4*>(reinterpret_cast<float*>(P.y) + (size_t)t * P.rows + r) = o;
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; e++)
+    if (r + e < P.rows) store_out(P, t, r + e, finish(P, t, r + e, (float)v[e] * xs * P.ws[r + e]));
+}
+
+// Tile of a work-group. Work-groups go to the eight XCDs in turn; each XCD is given a
+// contiguous run of tiles, eight channel tiles wide, so that the tiles it works on at a
+// time share operand rows in its L2.
+__device__ __forceinline__ void tile_of(int b, int nbm, int nbn, int& bm, int& bn) {
+  const int total = nbm * nbn, per = total / 8, rem = total % 8, xcd = b % 8;
+  const int l = xcd * per + min(xcd, rem) + b / 8;
+  constexpr int GM = 8;
+  const int group = l / (GM * nbn), first = group * GM, width = min(GM, nbm - first), in = l - group * GM * nbn;
+  bm = first + in % width;
+  bn = in / width;
+}
+
+// 16 bytes per lane from base + off + step into LDS at dst + 16 lane (dst the wave's own).
+__device__ __forceinline__ void copy16(const int8_t* base, int off, int step, uint8_t* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(base), (short)0, 0x7FFFFFFF, 0x00020000),
+      (__attribute__((address_space(3))) void*)dst, 16, off, step, 0, 0);
+}
+
+template <int N> struct Count {
+  static constexpr int value = N;
+};
+
+// Spread a batch's R operand reads among its M products instead of all before them.
+template <int R, int M>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < R && i < M; i++) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one matrix instruction
+    __builtin_amdgcn_sched_group_barrier(0x100, R > M ? (R + M - 1) / M : 1, 0);  // LDS reads
+  }
+  if (M > R) __builtin_amdgcn_sched_group_barrier(0x008, M - R, 0);
+}
+
 // ---------------------------------------------------------------- many tokens
 // A tiled product on v_mfma_i32_32x32x32_i8 (lane L: 16 bytes of row L % 32 at K =
 // 16 (L / 32); output register r: row (r % 4) + 8 (r / 4) + 4 (L / 32) of A, row
-// L % 32 of B). A work-group holds BM channels x BN tokens; per 128-byte step of K
-// both tiles are copied to LDS by the memory pipe itself (no registers), into one
-// of two buffers while the other is multiplied. A row's eight 16-byte chunks are
-// stored at chunk ^ (row & 7), so eight lanes reading the same chunk of eight rows
-// touch all banks once.
-constexpr int G_BK = 128;
-
-template <int WM, int WN, int TM, int TN>
+// L % 32 of B). A work-group holds BM channels x BN tokens. Both tiles' next 128 bytes
+// of K are copied to LDS by the memory pipe itself (no registers), into a ring of
+// STAGES buffers. A row's 16-byte chunks are stored at chunk ^ key(row): sixteen lanes
+// that read the same chunk of sixteen rows touch all 64 banks once (with the row's low
+// three bits as the key, half of the LDS cycles were bank conflicts: two 128-byte rows
+// share the banks, and a row's parity and its key went together).
+//
+// One barrier per step: before the last batch of a step's operands is multiplied, all of
+// them already in registers, every wave waits for its copies of the next step and for its
+// own reads; past the barrier the buffer just read is free for the copy STAGES steps on
+// and the next step's first operands are read, both under the last batch's products.
+template <int WM, int WN, int TM, int TN, int STAGES, int G_BK, int Q>
 __global__ __launch_bounds__(64 * WM * WN) void k_int8_tiled(Int8Params P) {
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32, WAVES = WM * WN;
   constexpr int ROWS = BM + BN;                 // rows of one buffer: channels, then tokens
-  constexpr int LOADS = ROWS / 8 / WAVES;       // copies per wave and step, eight rows each
-  static_assert(ROWS % (8 * WAVES) == 0 && BM % 8 == 0, "whole copies");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * ROWS * G_BK];
+  constexpr int CPR = G_BK / 16, RPC = 64 / CPR;  // chunks of a row, rows of a copy
+  constexpr int WL = BM / RPC / WAVES, XL = BN / RPC / WAVES;  // a wave's copies per step
+  constexpr int LOADS = WL + XL;
+  constexpr int NB = G_BK / 32 / Q;             // operand batches of a step, Q matrix-instruction depths each
+  static_assert(BM % (RPC * WAVES) == 0 && BN % (RPC * WAVES) == 0 && (G_BK == 128 || G_BK == 256), "whole copies");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[STAGES * ROWS * G_BK];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int K = P.cols;
-  const int nbm = (P.rows + BM - 1) / BM;
-  const int bm = blockIdx.x % nbm, bn = blockIdx.x / nbm;
+  const int nbm = (P.rows + BM - 1) / BM, nbn = (P.T + BN - 1) / BN;
+  int bm, bn;
+  tile_of(blockIdx.x, nbm, nbn, bm, bn);
   const int r0 = bm * BM, t0 = bn * BN;
 
-  // copy j of this wave: buffer rows 8 (wave LOADS + j) + lane / 8, chunk lane % 8
-  const int8_t* src[LOADS];
+  // a copy: RPC rows of one operand, lane l the 16 bytes that are stored at row l / CPR, position l % CPR
+  const int8_t* wbase = P.w + (size_t)r0 * K;
+  const int8_t* xbase = P.xq + (size_t)t0 * K;
+  const int wrow = RPC * WL * wave, xrow = RPC * XL * wave;  // this wave's first rows of the tiles
+  int off[LOADS];  // rows past the operand's end read its last row
+  auto key = [](int row) { return G_BK == 128 ? (row >> 1) & 7 : row & 15; };
+  auto c16 = [&](int row) { return 16 * ((lane & (CPR - 1)) ^ key(row)); };  // chunk at this lane's position
 #pragma unroll
-  for (int j = 0; j < LOADS; j++) {
-    const int row = 8 * (wave * LOADS + j) + (lane >> 3);
-    const int c = (lane & 7) ^ (row & 7);
-    src[j] = (row < BM ? P.w + (size_t)min(r0 + row, P.rows - 1) * K : P.xq + (size_t)min(t0 + row - BM, P.T - 1) * K) + 16 * c;
+  for (int j = 0; j < WL; j++) {
+    const int row = wrow + RPC * j + lane / CPR;
+    off[j] = min(row, P.rows - 1 - r0) * K + c16(row);
+  }
+#pragma unroll
+  for (int j = 0; j < XL; j++) {
+    const int row = xrow + RPC * j + lane / CPR;
+    off[WL + j] = min(row, P.T - 1 - t0) * K + c16(row);
   }
   const int full = K / G_BK, steps = (K + G_BK - 1) / G_BK;
-  auto copy = [&](int s, int buf) {
-    uint8_t* dst = lds + buf * ROWS * G_BK;
-    if (s < full) {
+  constexpr int BUF = ROWS * G_BK;
+  // step s, wholly inside K, into the buffer at byte `at` of the ring
+  auto copy = [&](int s, int at) {
 #pragma unroll
-      for (int j = 0; j < LOADS; j++)
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src[j] + (size_t)s * G_BK),
-                                         (__attribute__((address_space(3))) void*)(dst + 8 * (wave * LOADS + j) * G_BK), 16, 0, 0);
-    } else {  // the last, partial step: chunks past K are zeros
+    for (int j = 0; j < LOADS; j++)
+      copy16(j < WL ? wbase : xbase, off[j], s * G_BK, lds + at + (j < WL ? wrow + RPC * j : BM + xrow + RPC * (j - WL)) * G_BK);
+  };
+  // any step, none past the end; in the last, partial one chunks past K are zeros
+  auto copy_any = [&](int s, int at) {
+    if (s < full) {
+      copy(s, at);
+    } else if (s < steps) {
 #pragma unroll
       for (int j = 0; j < LOADS; j++) {
-        const int row = 8 * (wave * LOADS + j) + (lane >> 3);
-        const int c = (lane & 7) ^ (row & 7);
+        const int row = j < WL ? wrow + RPC * j : xrow + RPC * (j - WL);
         u32x4 v = u32x4{0u, 0u, 0u, 0u};
-        if (s * G_BK + 16 * c < K) v = ld16(src[j] + (size_t)s * G_BK);
-        *reinterpret_cast<u32x4*>(dst + row * G_BK + 16 * (lane & 7)) = v;
+        if (s * G_BK + c16(row + lane / CPR) < K) v = ld16((j < WL ? wbase : xbase) + off[j] + (size_t)s * G_BK);
+        *reinterpret_cast<u32x4*>(lds + at + (j < WL ? row : BM + row) * G_BK + 16 * lane) = v;
       }
     }
   };
@@ -261,26 +336,75 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_tiled(Int8Params P) {
   for (int i = 0; i < TM; i++)
 #pragma unroll
     for (int j = 0; j < TN; j++) acc[i][j] = i32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-
-  copy(0, 0);
-  for (int s = 0; s < steps; s++) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's copies of step s have landed
-    __syncthreads();                                  // everybody's have, and step s - 1 has been read
-    if (s + 1 < steps) copy(s + 1, (s + 1) & 1);
-    const uint8_t* b = lds + (s & 1) * ROWS * G_BK;
+  i32x4 a[2][Q][TM], x[2][Q][TN];
+  const uint8_t* la = lds + (wm * TM * 32 + n) * G_BK;
+  const uint8_t* lx = lds + (BM + wn * TN * 32 + n) * G_BK;
+  auto read = [&](int ring, int b, int to) {  // operands of batch b of the step in the buffer at `ring`
 #pragma unroll
-    for (int k = 0; k < G_BK / 32; k++) {
-      const int pos = 16 * ((2 * k + g) ^ (n & 7));  // tile rows start at multiples of 32: row & 7 = n & 7
-      i32x4 a[TM], x[TN];
+    for (int q = 0; q < Q; q++) {
+      // operand tiles start at multiples of 32 rows
+      const int at = ring + 16 * ((2 * (b * Q + q) + g) ^ key(n));
 #pragma unroll
-      for (int i = 0; i < TM; i++) a[i] = *reinterpret_cast<const i32x4*>(b + ((wm * TM + i) * 32 + n) * G_BK + pos);
+      for (int i = 0; i < TM; i++) a[to][q][i] = *reinterpret_cast<const i32x4*>(la + at + i * 32 * G_BK);
 #pragma unroll
-      for (int j = 0; j < TN; j++) x[j] = *reinterpret_cast<const i32x4*>(b + (BM + (wn * TN + j) * 32 + n) * G_BK + pos);
-#pragma unroll
-      for (int i = 0; i < TM; i++)
-#pragma unroll
-        for (int j = 0; j < TN; j++) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], x[j], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < TN; j++) x[to][q][j] = *reinterpret_cast<const i32x4*>(lx + at + j * 32 * G_BK);
     }
+  };
+  auto multiply = [&](int from) {
+#pragma unroll
+    for (int q = 0; q < Q; q++)
+#pragma unroll
+      for (int j = 0; j < TN; j++)
+#pragma unroll
+        for (int i = 0; i < TM; i++)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[from][q][i], x[from][q][j], acc[i][j], 0, 0, 0);
+  };
+  // The compiler does not see that copies write LDS: a wave waits for its own by count.
+  // `flying`: the steps whose copies may still be on their way.
+  auto landed = [&](auto flying) {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(decltype(flying)::value * LOADS) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  auto next = [](int ring) { return ring + BUF == STAGES * BUF ? 0 : ring + BUF; };
+
+#pragma unroll
+  for (int s = 0; s < STAGES; s++) copy_any(s, s * BUF);
+  if (STAGES <= full) landed(Count<STAGES - 1>{});
+  else landed(Count<0>{});
+  read(0, 0, 0);
+  int ring = 0;  // step s's buffer
+  // FULL: every copy made so far and the one made here is of a whole step
+  auto step = [&](int s, int at, auto FULL) {  // at: the register set that holds batch 0
+#pragma unroll
+    for (int b = 0; b < NB; b++) {
+      const int cur = (at + b) & 1;
+      if (b + 1 < NB) {
+        read(ring, b + 1, cur ^ 1);
+      } else {
+        if constexpr (decltype(FULL)::value) {
+          landed(Count<STAGES - 2>{});  // steps s + 2 .. s + STAGES - 1 may be on their way
+          copy(s + STAGES, ring);
+        } else {
+          landed(Count<0>{});
+          copy_any(s + STAGES, ring);
+        }
+        ring = next(ring);
+        read(ring, 0, cur ^ 1);  // past the end: a buffer's old bytes, not used
+      }
+      multiply(cur);
+      if constexpr (Q == 1) interleave<TM + TN, TM * TN>();
+    }
+  };
+  constexpr int SWAP = NB % 2;  // one batch per step: the register sets swap roles every step
+  int s = 0;
+  for (; s + STAGES + 1 < full; s += 2) {
+    step(s, 0, Count<1>{});
+    step(s + 1, SWAP, Count<1>{});
+  }
+  for (; s < steps; s += 2) {
+    step(s, 0, Count<0>{});
+    if (s + 1 < steps) step(s + 1, SWAP, Count<0>{});
   }
 
 #pragma unroll
@@ -290,15 +414,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_tiled(Int8Params P) {
 #pragma unroll
     for (int i = 0; i < TM; i++)
 #pragma unroll
-      for (int q = 0; q < 4; q++) {  // four consecutive channels
-        const int r = r0 + (wm * TM + i) * 32 + 8 * q + 4 * g;
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-          if (t < P.T && r + e < P.rows) {
-            store_out(P, t, r + e, finish(P, t, r + e, (float)acc[i][j][4 * q + e] * xs * P.ws[r + e]));
-          }
-        }
-      }
+      for (int q = 0; q < 4; q++)  // four consecutive channels
+        store4(P, t, r0 + (wm * TM + i) * 32 + 8 * q + 4 * g, xs, acc[i][j][4 * q], acc[i][j][4 * q + 1],
+               acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
   }
 }
 
@@ -308,18 +426,19 @@ __global__ __launch_bounds__(256) void k_dequant_int8(const int8_t* w, const flo
     out[i] = (float)w[i] * ws[i / cols];
 }
 
-template <int WM, int WN, int TM, int TN>
+template <int WM, int WN, int TM, int TN, int STAGES, int BK, int Q>
 hipError_t go_tiled(const Int8Params& p, hipStream_t s) {
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
-  const int blocks = ((p.rows + BM - 1) / BM) * ((p.T + BN - 1) / BN);
-  hipLaunchKernelGGL((k_int8_tiled<WM, WN, TM, TN>), dim3((unsigned)blocks), dim3(64 * WM * WN), 0, s, p);
+  const long blocks = (long)((p.rows + BM - 1) / BM) * ((p.T + BN - 1) / BN);
+  if (blocks > 0x7FFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((k_int8_tiled<WM, WN, TM, TN, STAGES, BK, Q>), dim3((unsigned)blocks), dim3(64 * WM * WN), 0, s, p);
   return hipGetLastError();
 }
 
-template <int MATS, int NT, int U>
+template <int MATS, int NT, int U, int S_WAVES = 8>
 hipError_t go_few(const Int8Params& p, hipStream_t s) {
   const dim3 g((unsigned)((p.rows + 15) / 16), (unsigned)((p.T + 16 * NT - 1) / (16 * NT)));
-  hipLaunchKernelGGL((k_int8_few<MATS, NT, U>), g, dim3(64 * S_WAVES), 0, s, p);
+  hipLaunchKernelGGL((k_int8_few<MATS, NT, U, S_WAVES>), g, dim3(64 * S_WAVES), 0, s, p);
   return hipGetLastError();
 }
 
@@ -338,14 +457,16 @@ hipError_t launch_dequant_int8(const int8_t* w, const float* ws, int rows, int c
   return hipGetLastError();
 }
 
-hipError_t launch_linear_int8(const Int8Params& p, hipStream_t s) {
+hipError_t launch_linear_int8(const Int8Params& p0, hipStream_t s) {
+  Int8Params p = p0;
+  p.vec4 = p.rows % 4 == 0 && (uintptr_t)p.y % (p.out_bf16 ? 8 : 16) == 0;
   if (p.T < 1 || p.rows < 1 || p.cols < 16 || p.cols % 16 || p.cols > INT8_MAX_COLS) return hipErrorInvalidValue;
   if (p.T <= 16) return go_few<1, 1, 8>(p, s);
   if (p.T <= 64) return go_few<1, 4, 4>(p, s);
   if (p.T <= 128) return go_few<1, 8, 2>(p, s);
   const long tiles = (long)((p.rows + 255) / 256) * ((p.T + 255) / 256);
-  if (tiles >= 200) return go_tiled<2, 4, 4, 2>(p, s);
-  return go_tiled<2, 2, 2, 2>(p, s);
+  if (tiles >= 200) return go_tiled<2, 4, 4, 2, 2, 128, 1>(p, s);
+  return go_tiled<2, 2, 2, 2, 2, 128, 1>(p, s);
 }
 
 hipError_t launch_gate_up_int8(const Int8Params& p, hipStream_t s) {

@@ -115,6 +115,7 @@ struct Int8Params {
   const float* add;   // fp32 [T][rows] added to the product, or null
   void* y;            // fp32 or bf16 [T][rows]
   int rows, cols, T, out_bf16;
+  int vec4;           // set by the launch: outputs can be stored four channels at a time
   // gate/up pair (launch_gate_up_int8): w, ws hold the gate, these the up matrix
   const int8_t* w2;
   const float* ws2;
