@@ -607,9 +607,9 @@ def linear_int8_workspace(T: int, cols: int, device="cuda"):
 
 
 def linear_int8_dynamic(w: Weight, x, expert: int = 0, bias=None, y=None, out_dtype=None, ws=None):
-    """linear_int8 from bf16 tokens x [T, cols], quantised within the call. Without ws the
-    workspace is allocated for the call from torch's caching allocator (on the current
-    stream, so calls on different streams never share one)."""
+    """linear_int8 from bf16 tokens x [T, cols], quantised within the call. More than a few
+    tokens need a workspace: without ws it is allocated for the call from torch's caching
+    allocator (on the current stream, so calls on different streams never share one)."""
     T = _tokens("x", x, w.cols)
     gpu = _gpu()
     _need("x", x, gpu[2], (T, w.cols))
@@ -617,13 +617,16 @@ def linear_int8_dynamic(w: Weight, x, expert: int = 0, bias=None, y=None, out_dt
     dev = _on_device(x, bias, y, ws, w.data, w.scales)
     if T == 0:
         return y
-    if ws is None:
-        ws = linear_int8_workspace(T, w.cols, x.device)
-    n = ws.numel()
-    _need("ws", ws, gpu[6], (n,))
+    at, n = None, 0
+    if T > 16 or w.cols << (T - 1).bit_length() > 65536:  # the codes are stored
+        if ws is None:
+            ws = linear_int8_workspace(T, w.cols, x.device)
+        n = ws.numel()
+        _need("ws", ws, gpu[6], (n,))
+        at = ws.data_ptr()
     _check("moeq_linear_int8_dynamic", (_LIB or _lib()).moeq_linear_int8_dynamic(
-        w._ref(), expert, x.data_ptr(), T, None if bias is None else bias.data_ptr(), out, y.data_ptr(),
-        ws.data_ptr(), n, gpu[1](dev)))
+        w._ref(), expert, x.data_ptr(), T, None if bias is None else bias.data_ptr(), out, y.data_ptr(), at, n,
+        gpu[1](dev)))
     return y
 
 

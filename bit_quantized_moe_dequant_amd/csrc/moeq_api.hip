@@ -987,6 +987,7 @@ int moeq_linear_int8(const moeq_weight* w, int expert, const int8_t* xq, const f
 
 size_t moeq_linear_int8_workspace_bytes(int T, int cols) {
   if (T < 0 || cols <= 0 || cols % 16 || cols > INT8_MAX_COLS) return 0;
+  if (few_bf16_fits(T, cols)) return 256;  // quantised where they are used: nothing is stored
   return align_up((size_t)T * 4, 256) + align_up((size_t)T * cols, 256) + 256;
 }
 
@@ -996,19 +997,24 @@ int moeq_linear_int8_dynamic(const moeq_weight* w, int expert, const void* x, in
   if (rc) return rc;
   if (!x) return MOEQ_E_INVAL;
   if (!aligned(x, 16)) return MOEQ_E_ALIGN;
-  if (!ws || ws_bytes < moeq_linear_int8_workspace_bytes(T, w->cols)) return MOEQ_E_WORKSPACE;
+  const bool few = few_bf16_fits(T, w->cols);
+  if (!few && (!ws || ws_bytes < moeq_linear_int8_workspace_bytes(T, w->cols))) return MOEQ_E_WORKSPACE;
   if (!aligned(ws, 256)) return MOEQ_E_ALIGN;
   if (T == 0) return MOEQ_OK;
-  float* xs = (float*)ws;
-  int8_t* xq = (int8_t*)ws + align_up((size_t)T * 4, 256);
-  if ((rc = hip_rc(launch_quant_int8(0, x, T, w->cols, xq, xs, S(stream))))) return rc;
   Int8Params p = int8_params(*w, expert);
-  p.xq = xq;
-  p.xs = xs;
   p.T = T;
   p.bias = bias;
   p.out_bf16 = out_type == MOEQ_OUT_BF16;
   p.y = y;
+  if (few) {
+    p.x = (const uint16_t*)x;
+    return hip_rc(launch_linear_int8_bf16(p, false, S(stream)));
+  }
+  float* xs = (float*)ws;
+  int8_t* xq = (int8_t*)ws + align_up((size_t)T * 4, 256);
+  if ((rc = hip_rc(launch_quant_int8(0, x, T, w->cols, xq, xs, S(stream))))) return rc;
+  p.xq = xq;
+  p.xs = xs;
   return hip_rc(launch_linear_int8(p, S(stream)));
 }
 

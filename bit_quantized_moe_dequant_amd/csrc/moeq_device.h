@@ -80,6 +80,34 @@ __device__ __forceinline__ int int8_code(float v, float s) {
   const float q = __builtin_fminf(__builtin_fmaxf(__builtin_rintf(v / s), -127.0f), 127.0f);
   return s > 0.f ? (int)q : 0;
 }
+// N codes at a time, four to a word, r = 1 / s. The product v r is within 127.5 * 2^-23 of
+// fl(v / s), so its nearest integer is the code unless it lies that near a half: then (and
+// where r is not finite: s zero, NaN or tiny) the divisions are made. Adding 1.5 * 2^23
+// rounds to the nearest integer, ties to even, and leaves it in the low bits.
+template <int N>
+__device__ __forceinline__ void int8_codes(const float (&v)[N], float s, float r, uint32_t (&out)[N / 4]) {
+  constexpr float MAGIC = 12582912.0f;
+  float far = 0.f;
+#pragma unroll
+  for (int j = 0; j < N / 4; j++) {
+    uint32_t t[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const float m = __builtin_fmaf(v[4 * j + k], r, MAGIC);
+      far = __builtin_fmaxf(far, __builtin_fabsf(__builtin_fmaf(v[4 * j + k], r, MAGIC - m)));
+      t[k] = f2u(m);
+    }
+    out[j] = __builtin_amdgcn_perm(t[1], t[0], 0x0C0C0400u) | __builtin_amdgcn_perm(t[3], t[2], 0x04000C0Cu);
+  }
+  if (!(far < 0.499976f) || !(r <= 3.402823466e38f)) {
+#pragma unroll
+    for (int j = 0; j < N / 4; j++) {
+      out[j] = 0;
+#pragma unroll
+      for (int k = 0; k < 4; k++) out[j] |= ((uint32_t)int8_code(v[4 * j + k], s) & 255u) << (8 * k);
+    }
+  }
+}
 
 // Split two fp32 values into hi and lo bf16 pairs with a + b ~ value to 16 bits.
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint32_t& lo) {

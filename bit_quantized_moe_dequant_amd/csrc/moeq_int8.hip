@@ -67,16 +67,13 @@ template <int IN_F32> struct QVals {
     const uint32_t w = v[i / 8][(i % 8) / 2];
     return u2f((i & 1) ? (w & 0xFFFF0000u) : (w << 16));
   }
-  __device__ __forceinline__ u32x4 codes(float s) const {
-    u32x4 q;
+  __device__ __forceinline__ u32x4 codes(float s, float r) const {
+    float f[16];
+    uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      uint32_t w = 0;
-#pragma unroll
-      for (int k = 0; k < 4; k++) w |= ((uint32_t)int8_code(at(4 * j + k), s) & 255u) << (8 * k);
-      q[j] = w;
-    }
-    return q;
+    for (int i = 0; i < 16; i++) f[i] = at(i);
+    int8_codes(f, s, r, w);
+    return u32x4{w[0], w[1], w[2], w[3]};
   }
 };
 
@@ -105,17 +102,17 @@ __global__ __launch_bounds__(Q_THREADS) void k_quant_int8(const void* x, int K, 
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < Q_THREADS / 64; w++) m = max(m, red[w]);
-  const float s = int8_scale(m);
+  const float s = int8_scale(m), r = 1.0f / s;
   if (tid == 0) scale[blockIdx.x] = s;
 #pragma unroll
   for (int j = 0; j < Q_HOLD; j++) {
     const int c = tid + j * Q_THREADS;
-    if (c < n) *reinterpret_cast<u32x4*>(q + row + 16 * (size_t)c) = held[j].codes(s);
+    if (c < n) *reinterpret_cast<u32x4*>(q + row + 16 * (size_t)c) = held[j].codes(s, r);
   }
   for (int c = tid + Q_HOLD * Q_THREADS; c < n; c += Q_THREADS) {
     QVals<IN_F32> v;
     v.load(x, row + 16 * (size_t)c);
-    *reinterpret_cast<u32x4*>(q + row + 16 * (size_t)c) = v.codes(s);
+    *reinterpret_cast<u32x4*>(q + row + 16 * (size_t)c) = v.codes(s, r);
   }
 }
 
@@ -200,6 +197,131 @@ __global__ __launch_bounds__(64 * S_WAVES) void k_int8_few(Int8Params P) {
   }
 }
 
+// The same product from bf16 tokens (dynamic quantisation): every work-group makes the codes
+// of its up to 16 tokens itself, in LDS, while its weight loads are on their way; a second
+// launch and a round trip of the codes through memory cost more at these sizes than the
+// repeated conversion. Wave w works on tokens w / WPT + (8 / WPT) j (WPT waves to a token,
+// TPW tokens to a wave), lane l on chunks of 8 values l, l + 64 WPT, ... (CPL of them).
+constexpr int F_LDS = 65536;  // codes of all tokens
+
+template <int MATS, int TPW, int CPL>
+__global__ __launch_bounds__(512) void k_int8_few_bf16(Int8Params P) {
+  constexpr int W = 8, U = 8;
+  __shared__ __attribute__((aligned(16))) uint8_t code[F_LDS + 17 * 16 + 64];  // rows K + 16 apart
+  __shared__ int32_t red[MATS][W][16][17];
+  __shared__ uint32_t top[W][2];
+  __shared__ float sc[16];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, g = lane >> 4;
+  const int r0 = blockIdx.x * 16;
+  const int K = P.cols, pitch = K + 16;
+  const int wpt = P.wpt, per = W / wpt;  // waves to a token, tokens at a time
+  const int sub = wave % wpt;
+
+  // tokens first, then the weights: the conversion waits for the former only
+  u32x4 v[TPW][CPL];
+#pragma unroll
+  for (int j = 0; j < TPW; j++) {
+    const int t = min(wave / wpt + per * j, P.T - 1);
+#pragma unroll
+    for (int c = 0; c < CPL; c++)
+      v[j][c] = ld16(P.x + (size_t)t * K + 8 * min(lane + 64 * (sub + wpt * c), K / 8 - 1));
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  const int steps = (K + 63) / 64;
+  const int spw = (steps + W - 1) / W;
+  const int s0 = wave * spw, s1 = min(s0 + spw, steps);
+  const int8_t* wr[MATS];
+#pragma unroll
+  for (int m = 0; m < MATS; m++) wr[m] = (m ? P.w2 : P.w) + (size_t)min(r0 + n, P.rows - 1) * K;
+  u32x4 wv[U][MATS];
+  auto load = [&](int s) {
+#pragma unroll
+    for (int u = 0; u < U; u++)
+#pragma unroll
+      for (int m = 0; m < MATS; m++) wv[u][m] = ld16(wr[m] + min(64 * (s + u) + 16 * g, K - 16));
+  };
+  load(s0);
+  __builtin_amdgcn_sched_barrier(0);
+
+  uint32_t m[TPW];
+#pragma unroll
+  for (int j = 0; j < TPW; j++) {
+    m[j] = 0;
+#pragma unroll
+    for (int c = 0; c < CPL; c++)  // chunks past the row's end repeat its last one
+#pragma unroll
+      for (int k = 0; k < 4; k++) m[j] = max(max(m[j], (v[j][c][k] << 16) & 0x7FFF0000u), v[j][c][k] & 0x7FFF0000u);
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) m[j] = max(m[j], (uint32_t)__shfl_xor((int)m[j], o, 64));
+    if (lane == 0) top[wave][j] = m[j];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < TPW; j++) {
+    const int t = wave / wpt + per * j;
+    for (int w = 0; w < wpt; w++) m[j] = max(m[j], top[wave - sub + w][j]);
+    const float s = int8_scale(m[j]), r = 1.0f / s;
+    if (t < P.T) {  // uniform
+      if (sub == 0 && lane == 0) sc[t] = s;
+#pragma unroll
+      for (int c = 0; c < CPL; c++) {
+        const int ch = lane + 64 * (sub + wpt * c);
+        float f[8];
+        uint32_t q[2];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          f[2 * k] = u2f(v[j][c][k] << 16);
+          f[2 * k + 1] = u2f(v[j][c][k] & 0xFFFF0000u);
+        }
+        int8_codes(f, s, r, q);
+        if (ch < K / 8) *reinterpret_cast<u32x2*>(&code[t * pitch + 8 * ch]) = u32x2{q[0], q[1]};
+      }
+    }
+  }
+  __syncthreads();
+
+  const uint8_t* xr = code + min(n, P.T - 1) * pitch + 16 * g;
+  i32x4 acc[MATS];
+#pragma unroll
+  for (int mt = 0; mt < MATS; mt++) acc[mt] = i32x4{0, 0, 0, 0};
+  for (int s = s0; s < s1; s += U) {
+    if (s > s0) load(s);
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      if (s + u < s1) {  // uniform; in the last step weights past K are zeros (and the codes there old bytes)
+        const i32x4 xv = *reinterpret_cast<const i32x4*>(xr + 64 * (s + u));
+#pragma unroll
+        for (int mt = 0; mt < MATS; mt++) {
+          if (64 * (s + u) + 16 * g >= K) wv[u][mt] = u32x4{0u, 0u, 0u, 0u};
+          acc[mt] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, wv[u][mt]), xv, acc[mt], 0, 0, 0);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int mt = 0; mt < MATS; mt++)
+#pragma unroll
+    for (int r = 0; r < 4; r++) red[mt][wave][n][4 * g + r] = acc[mt][r];
+  __syncthreads();
+  const int i = threadIdx.x, tk = i >> 4, c = i & 15;
+  if (i < 256 && tk < P.T && r0 + c < P.rows) {
+    int sum[MATS];
+#pragma unroll
+    for (int mt = 0; mt < MATS; mt++) {
+      sum[mt] = 0;
+#pragma unroll
+      for (int w = 0; w < W; w++) sum[mt] += red[mt][w][tk][c];
+    }
+    const float xs = sc[tk];
+    float f = (float)sum[0] * xs * P.ws[r0 + c];
+    if constexpr (MATS == 2) f = silu_mul(f, (float)sum[1] * xs * P.ws2[r0 + c]);
+    else f = finish(P, tk, r0 + c, f);
+    store_out(P, tk, r0 + c, f);
+  }
+}
+
 // Four consecutive channels r .. r + 3 of token t from their sums.
 __device__ __forceinline__ void store4(const Int8Params& P, int t, int r, float xs, int v0, int v1, int v2, int v3) {
   if (t >= P.T || r >= P.rows) return;
@@ -246,15 +368,17 @@ template <int N> struct Count {
   static constexpr int value = N;
 };
 
-// Spread a batch's R operand reads among its M products instead of all before them.
-template <int R, int M>
+// Spread a batch's R operand reads and V copies among its M products instead of all before
+// them: a copy waits for its turn at the memory pipe, and what follows it waits with it.
+template <int R, int V, int M, int I = 0>
 __device__ __forceinline__ void interleave() {
-#pragma unroll
-  for (int i = 0; i < R && i < M; i++) {
+  if constexpr (I < M) {
+    constexpr int reads = (I + 1) * R / M - I * R / M, copies = (I + 1) * V / M - I * V / M;
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one matrix instruction
-    __builtin_amdgcn_sched_group_barrier(0x100, R > M ? (R + M - 1) / M : 1, 0);  // LDS reads
+    if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
+    if constexpr (copies > 0) __builtin_amdgcn_sched_group_barrier(0x020, copies, 0);
+    interleave<R, V, M, I + 1>();
   }
-  if (M > R) __builtin_amdgcn_sched_group_barrier(0x008, M - R, 0);
 }
 
 // ---------------------------------------------------------------- many tokens
@@ -271,7 +395,7 @@ __device__ __forceinline__ void interleave() {
 // them already in registers, every wave waits for its copies of the next step and for its
 // own reads; past the barrier the buffer just read is free for the copy STAGES steps on
 // and the next step's first operands are read, both under the last batch's products.
-template <int WM, int WN, int TM, int TN, int STAGES, int G_BK, int Q>
+template <int WM, int WN, int TM, int TN, int STAGES, int G_BK, int Q, int SPREAD>
 __global__ __launch_bounds__(64 * WM * WN) void k_int8_tiled(Int8Params P) {
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32, WAVES = WM * WN;
   constexpr int ROWS = BM + BN;                 // rows of one buffer: channels, then tokens
@@ -308,19 +432,19 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_tiled(Int8Params P) {
   }
   const int full = K / G_BK, steps = (K + G_BK - 1) / G_BK;
   constexpr int BUF = ROWS * G_BK;
-  // step s, wholly inside K, into the buffer at byte `at` of the ring
-  auto copy = [&](int s, int at) {
+  // part `part` of step s, wholly inside K, into the buffer at byte `at` of the ring
+  auto copy = [&](int s, int at, int part) {
 #pragma unroll
-    for (int j = 0; j < LOADS; j++)
+    for (int j = part * LOADS / SPREAD; j < (part + 1) * LOADS / SPREAD; j++)
       copy16(j < WL ? wbase : xbase, off[j], s * G_BK, lds + at + (j < WL ? wrow + RPC * j : BM + xrow + RPC * (j - WL)) * G_BK);
   };
   // any step, none past the end; in the last, partial one chunks past K are zeros
-  auto copy_any = [&](int s, int at) {
+  auto copy_any = [&](int s, int at, int part) {
     if (s < full) {
-      copy(s, at);
+      copy(s, at, part);
     } else if (s < steps) {
 #pragma unroll
-      for (int j = 0; j < LOADS; j++) {
+      for (int j = part * LOADS / SPREAD; j < (part + 1) * LOADS / SPREAD; j++) {
         const int row = j < WL ? wrow + RPC * j : xrow + RPC * (j - WL);
         u32x4 v = u32x4{0u, 0u, 0u, 0u};
         if (s * G_BK + c16(row + lane / CPR) < K) v = ld16((j < WL ? wbase : xbase) + off[j] + (size_t)s * G_BK);
@@ -362,40 +486,44 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_tiled(Int8Params P) {
   // The compiler does not see that copies write LDS: a wave waits for its own by count.
   // `flying`: the steps whose copies may still be on their way.
   auto landed = [&](auto flying) {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(decltype(flying)::value * LOADS) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(decltype(flying)::value) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
   auto next = [](int ring) { return ring + BUF == STAGES * BUF ? 0 : ring + BUF; };
 
 #pragma unroll
-  for (int s = 0; s < STAGES; s++) copy_any(s, s * BUF);
-  if (STAGES <= full) landed(Count<STAGES - 1>{});
+  for (int s = 0; s < STAGES; s++)
+#pragma unroll
+    for (int part = 0; part < (s + 1 < STAGES ? SPREAD : 1); part++) copy_any(s, s * BUF, part);
+  if (STAGES <= full) landed(Count<(STAGES - 2) * LOADS + LOADS / SPREAD>{});
   else landed(Count<0>{});
   read(0, 0, 0);
-  int ring = 0;  // step s's buffer
-  // FULL: every copy made so far and the one made here is of a whole step
+  int ring = 0, last = (STAGES - 1) * BUF;  // step s's buffer, and the one before
+  // FULL: every copy made so far and the ones made here are of whole steps
   auto step = [&](int s, int at, auto FULL) {  // at: the register set that holds batch 0
 #pragma unroll
     for (int b = 0; b < NB; b++) {
       const int cur = (at + b) & 1;
+      const int part = b + 1 == NB ? 0 : b + 1;  // of step s - 1 + STAGES until the barrier, then of the next one
       if (b + 1 < NB) {
         read(ring, b + 1, cur ^ 1);
       } else {
-        if constexpr (decltype(FULL)::value) {
-          landed(Count<STAGES - 2>{});  // steps s + 2 .. s + STAGES - 1 may be on their way
-          copy(s + STAGES, ring);
-        } else {
-          landed(Count<0>{});
-          copy_any(s + STAGES, ring);
-        }
+        if constexpr (decltype(FULL)::value) landed(Count<(STAGES - 2) * LOADS>{});  // steps s + 2 .. s + STAGES - 1
+        else landed(Count<0>{});
+        last = ring;
         ring = next(ring);
         read(ring, 0, cur ^ 1);  // past the end: a buffer's old bytes, not used
       }
+      if (part < SPREAD) {
+        if constexpr (decltype(FULL)::value) copy(s + STAGES - (part ? 1 : 0), last, part);
+        else copy_any(s + STAGES - (part ? 1 : 0), last, part);
+      }
       multiply(cur);
-      if constexpr (Q == 1) interleave<TM + TN, TM * TN>();
+      if constexpr (Q == 1) interleave<TM + TN, LOADS / SPREAD, TM * TN>();
     }
   };
+  static_assert(SPREAD <= NB && LOADS % SPREAD == 0, "a step's copies are made within a step");
   constexpr int SWAP = NB % 2;  // one batch per step: the register sets swap roles every step
   int s = 0;
   for (; s + STAGES + 1 < full; s += 2) {
@@ -426,12 +554,12 @@ __global__ __launch_bounds__(256) void k_dequant_int8(const int8_t* w, const flo
     out[i] = (float)w[i] * ws[i / cols];
 }
 
-template <int WM, int WN, int TM, int TN, int STAGES, int BK, int Q>
+template <int WM, int WN, int TM, int TN, int STAGES, int BK, int Q, int SPREAD>
 hipError_t go_tiled(const Int8Params& p, hipStream_t s) {
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
   const long blocks = (long)((p.rows + BM - 1) / BM) * ((p.T + BN - 1) / BN);
   if (blocks > 0x7FFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((k_int8_tiled<WM, WN, TM, TN, STAGES, BK, Q>), dim3((unsigned)blocks), dim3(64 * WM * WN), 0, s, p);
+  hipLaunchKernelGGL((k_int8_tiled<WM, WN, TM, TN, STAGES, BK, Q, SPREAD>), dim3((unsigned)blocks), dim3(64 * WM * WN), 0, s, p);
   return hipGetLastError();
 }
 
@@ -457,16 +585,54 @@ hipError_t launch_dequant_int8(const int8_t* w, const float* ws, int rows, int c
   return hipGetLastError();
 }
 
+// T up to 16, rounded up to a power of two times cols within the staged codes (and so at
+// most 16 chunks to a lane).
+bool few_bf16_fits(int T, int cols) {
+  int t = 1;
+  while (t < T) t *= 2;
+  return T >= 1 && T <= 16 && (long)t * cols <= F_LDS;
+}
+
+// P.x in place of the codes (few_bf16_fits).
+hipError_t launch_linear_int8_bf16(const Int8Params& p0, bool gate_up, hipStream_t s) {
+  Int8Params p = p0;
+  if (!few_bf16_fits(p.T, p.cols) || p.rows < 1 || p.cols < 16 || p.cols % 16) return hipErrorInvalidValue;
+  p.wpt = p.T <= 1 ? 8 : p.T <= 2 ? 4 : p.T <= 4 ? 2 : 1;
+  const int cpl = (p.cols / 8 + 64 * p.wpt - 1) / (64 * p.wpt);  // chunks per lane and token
+  const dim3 g((unsigned)((p.rows + 15) / 16)), b(512);
+#define MOEQ_FEW(TPW, CPL)                                                                \
+  do {                                                                                    \
+    if (gate_up) hipLaunchKernelGGL((k_int8_few_bf16<2, TPW, CPL>), g, b, 0, s, p);       \
+    else hipLaunchKernelGGL((k_int8_few_bf16<1, TPW, CPL>), g, b, 0, s, p);               \
+    return hipGetLastError();                                                             \
+  } while (0)
+  if (p.T <= 8) {  // one token at most to a wave
+    if (cpl <= 1) MOEQ_FEW(1, 1);
+    if (cpl <= 4) MOEQ_FEW(1, 4);
+    if (cpl <= 16) MOEQ_FEW(1, 16);
+  } else {
+    if (cpl <= 2) MOEQ_FEW(2, 2);
+    if (cpl <= 8) MOEQ_FEW(2, 8);
+  }
+#undef MOEQ_FEW
+  return hipErrorInvalidValue;
+}
+
 hipError_t launch_linear_int8(const Int8Params& p0, hipStream_t s) {
   Int8Params p = p0;
   p.vec4 = p.rows % 4 == 0 && (uintptr_t)p.y % (p.out_bf16 ? 8 : 16) == 0;
   if (p.T < 1 || p.rows < 1 || p.cols < 16 || p.cols % 16 || p.cols > INT8_MAX_COLS) return hipErrorInvalidValue;
   if (p.T <= 16) return go_few<1, 1, 8>(p, s);
-  if (p.T <= 64) return go_few<1, 4, 4>(p, s);
-  if (p.T <= 128) return go_few<1, 8, 2>(p, s);
-  const long tiles = (long)((p.rows + 255) / 256) * ((p.T + 255) / 256);
-  if (tiles >= 200) return go_tiled<2, 4, 4, 2, 2, 128, 1>(p, s);
-  return go_tiled<2, 2, 2, 2, 2, 128, 1>(p, s);
+  if (p.T <= 32) return go_few<1, 2, 8>(p, s);
+  // The largest tile that still gives most of the 256 CUs one (us at T = 64 / 256 / 512 /
+  // 2048 x 4096 x 4096): 256 x 256 - / - / - / 60; 256 x 128 - / - / - / 44; 128 x 64
+  // - / 17.2 / 17.0 / 52; 64 x 64 11.7 / 12.2 / 17.7 / -; 32 x 64 10.0 / 12.9 / - / -.
+  auto tiles = [&](int bm, int bn) { return (long)((p.rows + bm - 1) / bm) * ((p.T + bn - 1) / bn); };
+  if (tiles(256, 256) >= 224) return go_tiled<2, 4, 4, 2, 2, 128, 1, 2>(p, s);
+  if (tiles(256, 128) >= 160) return go_tiled<4, 2, 2, 2, 3, 128, 1, 2>(p, s);
+  if (tiles(128, 64) >= 160) return go_tiled<4, 2, 1, 1, 3, 128, 4, 1>(p, s);
+  if (tiles(64, 64) >= 160) return go_tiled<2, 2, 1, 1, 4, 128, 4, 1>(p, s);
+  return go_tiled<1, 2, 1, 1, 4, 128, 4, 1>(p, s);
 }
 
 hipError_t launch_gate_up_int8(const Int8Params& p, hipStream_t s) {

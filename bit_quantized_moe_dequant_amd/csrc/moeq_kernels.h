@@ -119,6 +119,9 @@ struct Int8Params {
   // gate/up pair (launch_gate_up_int8): w, ws hold the gate, these the up matrix
   const int8_t* w2;
   const float* ws2;
+  // launch_linear_int8_bf16: the tokens in place of xq, xs
+  const uint16_t* x;  // bf16 [T][cols], 16-byte aligned
+  int wpt;            // set by the launch: waves to a token
 };
 
 // Scores of the router, in the order of MOEQ_SCORE_*.
@@ -204,6 +207,9 @@ hipError_t launch_nv4_to_mx4(const uint8_t* nib, const uint8_t* e4m3, const floa
 // Per-token int8 codes and scales of bf16 (in_f32 = 0) or fp32 rows; K % 16 == 0.
 hipError_t launch_quant_int8(int in_f32, const void* x, int T, int K, int8_t* q, float* scale, hipStream_t s);
 hipError_t launch_linear_int8(const Int8Params& p, hipStream_t s);
+// The product (or the gate/up pair) from bf16 tokens p.x in one launch, for a few of them.
+bool few_bf16_fits(int T, int cols);
+hipError_t launch_linear_int8_bf16(const Int8Params& p, bool gate_up, hipStream_t s);
 // h[T][rows] (fp32, p.y) = silu(gate) * up of an INT8 gate/up pair, as launch_linear_int8 for each.
 hipError_t launch_gate_up_int8(const Int8Params& p, hipStream_t s);
 hipError_t launch_router(const RouterParams& p, hipStream_t s);

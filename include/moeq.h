@@ -349,7 +349,9 @@ int moeq_linear_int8(const moeq_weight* w, int expert, const int8_t* xq, const f
 /* The same product from bf16 tokens x [T][cols] (16-byte aligned), quantised as by
  * moeq_quantize_int8 within the call. ws: at least
  * moeq_linear_int8_workspace_bytes(T, cols) bytes, 256-byte aligned, contents
- * arbitrary, not shared with an overlapping call. */
+ * arbitrary, not shared with an overlapping call. For a few tokens (T <= 16, and T
+ * rounded up to a power of two times cols <= 65536) it is one launch that stores no
+ * codes: ws may then be NULL. */
 size_t moeq_linear_int8_workspace_bytes(int T, int cols);
 int moeq_linear_int8_dynamic(const moeq_weight* w, int expert, const void* x, int T, const float* bias, int out_type,
                              void* y, void* ws, size_t ws_bytes, void* stream);

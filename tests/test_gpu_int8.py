@@ -85,6 +85,21 @@ def test_quantize(T, K, f32):
     assert np.array_equal(s.cpu().numpy(), rs, equal_nan=True)
 
 
+def test_quantize_every_scale_and_value():
+    """bf16 values of all magnitudes under scales of all exponents: the codes are the fp32 rule's."""
+    say("quantize all")
+    v = torch.arange(0, 0x7F80, 7, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)  # finite, non-negative
+    v = torch.cat([v, -v])[: 9344].reshape(-1)
+    n = v.numel() // 16 * 16
+    rows = torch.stack([v[:n] * f for f in (1.0, 0.37, 2.0 ** -60, 2.0 ** -120)])
+    order = torch.argsort(rows[0].float().abs())
+    x = rows[:, order].reshape(4 * (n // 16), 16).contiguous().cuda()  # sixteen neighbours to a row: every scale
+    q, s = mq.quantize_int8(x)
+    rq, rs = quant_ref(x.float().cpu().numpy())
+    assert np.array_equal(s.cpu().numpy(), rs)
+    assert np.array_equal(q.cpu().numpy(), rq)
+
+
 def test_quantize_ties_and_borders():
     """Values on and next to half codes: the rule is the fp32 quotient's, rounded to even."""
     say("quantize ties")
@@ -192,6 +207,24 @@ def test_streams_and_graph():
         q, s = quant_ref(x.float().cpu().numpy())
         check(y, q, s, wq[0], ws[0], None, False)
         del graph
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 8, 9, 13, 16])
+@pytest.mark.parametrize("cols", [16, 48, 528, 1040, 2064, 4096, 7168, 8192, 16384])
+def test_few_tokens_from_bf16(T, cols):
+    """The one-launch form (T <= 16, and T as a power of two times cols <= 65536) and the two beyond it."""
+    say("few", T, cols)
+    w, wq, ws = weight(37, cols, cols)
+    x = tokens(T, cols, T)
+    x[T - 1, cols - 1] = 300.0  # the maximum in the row's last place
+    if T > 2:
+        x[1] = 0
+        x[2, 3] = float("nan")
+    q, s = quant_ref(x.float().cpu().numpy())
+    y = mq.linear_int8_dynamic(w, x, out_dtype=torch.float32)
+    check(y, q, s, wq[0], ws[0], None, False)
+    two = mq.linear_int8(w, *mq.quantize_int8(x), out_dtype=torch.float32)
+    assert torch.equal(y.nan_to_num(123.0), two.nan_to_num(123.0))
 
 
 def test_no_tokens():

@@ -21,7 +21,7 @@ def linear(w, expert=0, xq=0x100000, xs=0x200000, T=4, bias=0, out=0, y=0x300000
     return mq._lib().moeq_linear_int8(ctypes.byref(w), expert, P(xq), P(xs), T, P(bias), out, P(y), None)
 
 
-def dynamic(w, expert=0, x=0x100000, T=4, out=0, y=0x300000, ws=0x400000, n=None):
+def dynamic(w, expert=0, x=0x100000, T=40, out=0, y=0x300000, ws=0x400000, n=None):
     n = mq._lib().moeq_linear_int8_workspace_bytes(max(T, 0), 512) if n is None else n
     return mq._lib().moeq_linear_int8_dynamic(ctypes.byref(w), expert, P(x), T, None, out, P(y), P(ws), n, None)
 
@@ -30,7 +30,8 @@ def test_sizes():
     assert mq.plane_bytes(9, 7, 48, 0) == 7 * 48 and mq.plane_bytes(9, 7, 48, 1) == 28
     assert mq.plane_bytes(9, 7, 40, 0) == 0 and mq.packed_bytes(9, 4096, 4096) == 4096 * 4096 + 4 * 4096
     lib = mq._lib()
-    assert lib.moeq_linear_int8_workspace_bytes(1, 512) >= 516
+    assert lib.moeq_linear_int8_workspace_bytes(40, 512) >= 40 * 516
+    assert lib.moeq_linear_int8_workspace_bytes(1, 512) > 0
     assert lib.moeq_linear_int8_workspace_bytes(4, 40) == 0 == lib.moeq_linear_int8_workspace_bytes(-1, 64)
 
 
