@@ -515,13 +515,18 @@ int check_moe(const moeq_layer* L, const moeq_router* R, const moeq_shared* S) {
 
 size_t router_bytes(const moeq_router* R, int T) { return 256 + align_up((size_t)T * R->n_experts * 8, 256); }
 
-RouterParams router_params(const moeq_router* R, const void* x, int T, int32_t* ids, float* rw, double* logits) {
+// The counters of the one-launch router lie in the workspace's header, which the caller
+// has zeroed once; every launch leaves them at zero.
+static_assert(64 + 4 * (ROUTER_FEW_T / 8) <= 256, "the counters fit the header");
+RouterParams router_params(const moeq_router* R, const void* x, int T, int32_t* ids, float* rw, void* ws,
+                           double* logits) {
   RouterParams p;
   memset(&p, 0, sizeof(p));
   p.x = (const uint16_t*)x;
   p.w = (const uint16_t*)R->weight;
   p.bias = R->bias;
   p.logits = logits;
+  p.count = (uint32_t*)((uint8_t*)ws + 64);
   p.ids = ids;
   p.rw = rw;
   p.hidden = R->hidden;
@@ -570,7 +575,7 @@ int moe_forward(const moeq_layer* L, const moeq_router* R, const moeq_shared* Sh
   if (!ids) ids = (int32_t*)(base + m.ids);
   if (!rw) rw = (float*)(base + m.rw);
   float* y32 = (float*)(base + m.y);
-  int rc = hip_rc(launch_router(router_params(R, x, T, ids, rw, (double*)(base + m.logits)), s));
+  int rc = hip_rc(launch_router(router_params(R, x, T, ids, rw, ws, (double*)(base + m.logits)), s));
   if (rc) return rc;
   if ((rc = forward(L, x, ids, rw, T, y32, ws, m.routed, s))) return rc;
   if (!Sh) return hip_rc(launch_to_bf16(y32, (size_t)T * L->hidden, (uint16_t*)y, s));
@@ -1032,7 +1037,7 @@ int moeq_router_topk(const moeq_router* R, const void* x, int T, int32_t* ids, f
   if (!ws || ws_bytes < router_bytes(R, T)) return MOEQ_E_WORKSPACE;
   if (!aligned(ws, 256)) return MOEQ_E_ALIGN;
   if (T == 0) return MOEQ_OK;
-  return hip_rc(launch_router(router_params(R, x, T, ids, rw, (double*)((uint8_t*)ws + 256)), S(stream)));
+  return hip_rc(launch_router(router_params(R, x, T, ids, rw, ws, (double*)((uint8_t*)ws + 256)), S(stream)));
 }
 
 size_t moeq_moe_workspace_bytes(const moeq_layer* L, const moeq_router* R, const moeq_shared* Sh, int T) {

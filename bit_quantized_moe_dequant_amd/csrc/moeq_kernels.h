@@ -124,6 +124,7 @@ struct Int8Params {
   int wpt;            // set by the launch: waves to a token
 };
 
+constexpr int ROUTER_FEW_T = 64;  // tokens of the one-launch router
 // Scores of the router, in the order of MOEQ_SCORE_*.
 enum { SCORE_SOFTMAX = 0, SCORE_SIGMOID = 1, SCORE_SQRT_SOFTPLUS = 2 };
 struct RouterParams {
@@ -131,6 +132,7 @@ struct RouterParams {
   const uint16_t* w;  // bf16 [n_experts][hidden]
   const float* bias;  // [n_experts] or null
   double* logits;     // [T][n_experts] workspace
+  uint32_t* count;    // ROUTER_FEW_T / 8 counters, zero between launches
   int32_t* ids;       // [T][top_k]
   float* rw;          // [T][top_k]
   int hidden, n_experts, top_k, scoring, normalize, T;
@@ -212,6 +214,7 @@ bool few_bf16_fits(int T, int cols);
 hipError_t launch_linear_int8_bf16(const Int8Params& p, bool gate_up, hipStream_t s);
 // h[T][rows] (fp32, p.y) = silu(gate) * up of an INT8 gate/up pair, as launch_linear_int8 for each.
 hipError_t launch_gate_up_int8(const Int8Params& p, hipStream_t s);
+bool router_few_fits(int T);
 hipError_t launch_router(const RouterParams& p, hipStream_t s);
 // y bf16 = x fp32, n values.
 hipError_t launch_to_bf16(const float* x, size_t n, uint16_t* y, hipStream_t s);

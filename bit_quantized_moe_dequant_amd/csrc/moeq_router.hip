@@ -10,21 +10,16 @@
 // two correct fp32 routers disagree on a near tie and a token's output jumps. A product
 // of two bf16 values is exact in fp64 and the vector unit issues fp64 FMAs at the fp32
 // rate here, so the exactness costs the conversions only.
-#include "moeq_device.h"
-#include "moeq_kernels.h"
+#include "moeq_router.h"
 
 namespace moeq {
 
 namespace {
 
+__global__ __launch_bounds__(512) void k_router_few(RouterParams P) { router_few(P, blockIdx.x, blockIdx.y); }
+
 constexpr int R_WAVES = 4;  // experts per work-group, one per wave
 constexpr int R_TOK = 8;    // tokens per work-group
-
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
 
 // Lane l takes the 16-byte chunks l, l + 64, ... of the expert's row.
 __global__ __launch_bounds__(64 * R_WAVES) void k_router_logits(RouterParams P) {
@@ -65,101 +60,27 @@ __global__ __launch_bounds__(64 * R_WAVES) void k_router_logits(RouterParams P) 
     }
 }
 
-// One wave per token; lane l holds experts l, l + 64, ...
-template <int N>
-__device__ void choose(const RouterParams& P, int t, int lane) {
-  const double* z = P.logits + (size_t)t * P.n_experts;
-  double s[N], key[N];
-#pragma unroll
-  for (int i = 0; i < N; i++) s[i] = lane + 64 * i < P.n_experts ? z[lane + 64 * i] : -__builtin_inf();
-  if (P.scoring == SCORE_SOFTMAX) {
-    double m = -__builtin_inf();
-#pragma unroll
-    for (int i = 0; i < N; i++) m = s[i] > m ? s[i] : m;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const double v = __shfl_xor(m, o, 64);
-      m = v > m ? v : m;
-    }
-    double sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < N; i++) {
-      s[i] = lane + 64 * i < P.n_experts ? exp(s[i] - m) : 0.0;
-      sum += s[i];
-    }
-    sum = wave_sum(sum);
-#pragma unroll
-    for (int i = 0; i < N; i++) s[i] /= sum;
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i++) {
-      const double v = s[i];
-      if (P.scoring == SCORE_SIGMOID) s[i] = 1.0 / (1.0 + exp(-v));
-      else s[i] = sqrt((v > 0.0 ? v : v < 0.0 ? 0.0 : v) + log1p(exp(-__builtin_fabs(v))));
-    }
-  }
-  // A key that is NaN counts below every number, an expert past the end below that.
-#pragma unroll
-  for (int i = 0; i < N; i++) {
-    const int e = lane + 64 * i;
-    const double k = e < P.n_experts && P.bias ? s[i] + (double)P.bias[e] : s[i];
-    key[i] = k == k ? k : -__builtin_inf();
-  }
-  uint32_t taken = 0;  // of this lane's experts
-  double ws = 0.0, sum = 0.0;
-  for (int k = 0; k < P.top_k; k++) {
-    double best = 0.0;
-    int id = 1 << 30;  // none
-#pragma unroll
-    for (int i = 0; i < N; i++)
-      if (lane + 64 * i < P.n_experts && !((taken >> i) & 1) && (id == (1 << 30) || key[i] > best)) {
-        best = key[i];
-        id = lane + 64 * i;
-      }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const double ob = __shfl_xor(best, o, 64);
-      const int oi = __shfl_xor(id, o, 64);
-      if (oi != (1 << 30) && (id == (1 << 30) || ob > best || (ob == best && oi < id))) {
-        best = ob;
-        id = oi;
-      }
-    }
-    double sc = 0.0;
-#pragma unroll
-    for (int i = 0; i < N; i++)
-      if (lane + 64 * i == id) {
-        taken |= 1u << i;
-        sc = s[i];
-      }
-    sc = __shfl(sc, id & 63, 64);
-    sum += sc;
-    if (lane == k) {
-      ws = sc;
-      P.ids[(size_t)t * P.top_k + k] = id;
-    }
-  }
-  if (lane < P.top_k) {
-    double w = ws;
-    if (P.normalize) w = sum == 0.0 ? 0.0 : w / sum;
-    P.rw[(size_t)t * P.top_k + lane] = (float)(w * (double)P.scale);
-  }
-}
-
 __global__ __launch_bounds__(256) void k_router_choose(RouterParams P) {
   const int lane = threadIdx.x & 63;
   const int t = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (t >= P.T) return;
-  if (P.n_experts <= 256) choose<4>(P, t, lane);
-  else choose<16>(P, t, lane);
+  if (P.n_experts <= 256) choose<4, false>(P, t, lane);
+  else choose<16, false>(P, t, lane);
 }
 
 }  // namespace
+
+bool router_few_fits(int T) { return T <= ROUTER_FEW_T; }
 
 hipError_t launch_router(const RouterParams& p, hipStream_t s) {
   if (p.T < 1 || p.n_experts < 1 || p.n_experts > 1024 || p.top_k < 1 || p.top_k > 16 || p.top_k > p.n_experts ||
       p.hidden < 8 || p.hidden % 8)
     return hipErrorInvalidValue;
+  if (router_few_fits(p.T)) {
+    const dim3 g((unsigned)((p.n_experts + RF_EXPERTS - 1) / RF_EXPERTS), (unsigned)((p.T + RF_TOK - 1) / RF_TOK));
+    hipLaunchKernelGGL(k_router_few, g, dim3(512), 0, s, p);
+    return hipGetLastError();
+  }
   for (int t0 = 0; t0 < p.T; t0 += 65535 * R_TOK) {  // grid rows
     RouterParams q = p;
     q.T = p.T - t0 < 65535 * R_TOK ? p.T - t0 : 65535 * R_TOK;
