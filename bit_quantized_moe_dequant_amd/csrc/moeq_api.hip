@@ -328,23 +328,29 @@ int run_gate_up(const moeq_layer* L, const void* x, const int32_t* ids, int T, f
   return hip_rc(launch_gemv(L->gate.fmt, EPI_SWIGLU, p, slots, grouped_wide(L, T) ? 4 : 1, s, ev));
 }
 
+Down1Params down1_params(const moeq_layer* L, const float* h, const int32_t* ids, const float* rw, int T,
+                         uint32_t* err) {
+  Down1Params d;
+  memset(&d, 0, sizeof(d));
+  d.T = T;
+  d.w = ref_of(L->down);
+  d.grid = L->down.grid;
+  d.rows = L->down.rows;
+  d.cols = L->down.cols;
+  d.n_experts = L->n_experts;
+  d.top_k = L->top_k;
+  d.h = h;
+  d.ids = ids;
+  d.rw = rw;
+  d.err = err;
+  return d;
+}
+
 int run_down(const moeq_layer* L, const float* h, const int32_t* ids, const float* rw, int T, float* y, void* ws,
              const WsLayout& lay, hipStream_t s) {
   if (dn_direct(L, T, h)) {
-    Down1Params d;
-    memset(&d, 0, sizeof(d));
-    d.T = T;
-    d.w = ref_of(L->down);
-    d.grid = L->down.grid;
-    d.rows = L->down.rows;
-    d.cols = L->down.cols;
-    d.n_experts = L->n_experts;
-    d.top_k = L->top_k;
-    d.h = h;
-    d.ids = ids;
-    d.rw = rw;
+    Down1Params d = down1_params(L, h, ids, rw, T, err_of(ws, lay));
     d.y = y;
-    d.err = err_of(ws, lay);
     return hip_rc(launch_down1(L->down.fmt, d, s));
   }
   GemvParams p = gemv_params(L, L->down, nullptr, ws, lay);
@@ -575,34 +581,74 @@ int moe_forward(const moeq_layer* L, const moeq_router* R, const moeq_shared* Sh
   if (!ids) ids = (int32_t*)(base + m.ids);
   if (!rw) rw = (float*)(base + m.rw);
   float* y32 = (float*)(base + m.y);
-  int rc = hip_rc(launch_router(router_params(R, x, T, ids, rw, ws, (double*)(base + m.logits)), s));
-  if (rc) return rc;
-  if ((rc = forward(L, x, ids, rw, T, y32, ws, m.routed, s))) return rc;
-  if (!Sh) return hip_rc(launch_to_bf16(y32, (size_t)T * L->hidden, (uint16_t*)y, s));
   int8_t* xq = (int8_t*)(base + m.xq);
   int8_t* hq = (int8_t*)(base + m.hq);
   float* xs = (float*)(base + m.xs);
   float* hs = (float*)(base + m.hs);
-  float* h = (float*)(base + m.h);
-  if ((rc = hip_rc(launch_quant_int8(0, x, T, L->hidden, xq, xs, s)))) return rc;
-  Int8Params p = int8_params(Sh->gate, 0);
-  const Int8Params up = int8_params(Sh->up, 0);
-  p.w2 = up.w;
-  p.ws2 = up.ws;
-  p.xq = xq;
-  p.xs = xs;
-  p.T = T;
-  p.y = h;
-  if ((rc = hip_rc(launch_gate_up_int8(p, s)))) return rc;
-  if ((rc = hip_rc(launch_quant_int8(1, h, T, Sh->inter, hq, hs, s)))) return rc;
-  p = int8_params(Sh->down, 0);
-  p.xq = hq;
-  p.xs = hs;
-  p.T = T;
-  p.add = y32;
-  p.out_bf16 = 1;
-  p.y = y;
-  return hip_rc(launch_linear_int8(p, s));
+  float* hsh = (float*)(base + m.h);  // the shared expert's h
+  const RouterParams rp = router_params(R, x, T, ids, rw, ws, (double*)(base + m.logits));
+  Int8Params gu, dn;
+  memset(&gu, 0, sizeof(gu));
+  memset(&dn, 0, sizeof(dn));
+  if (Sh) {
+    gu = int8_params(Sh->gate, 0);
+    const Int8Params up = int8_params(Sh->up, 0);
+    gu.w2 = up.w;
+    gu.ws2 = up.ws;
+    gu.x = x;
+    gu.y = hsh;
+    dn = int8_params(Sh->down, 0);
+    dn.x = hsh;
+  }
+  gu.T = dn.T = T;
+  int rc;
+
+  // 1. the router, with the shared gate/up beside it for a few tokens
+  if (Sh && moe_front_fits(T, L->hidden)) {
+    rc = hip_rc(launch_moe_front(rp, gu, s));
+  } else {
+    if ((rc = hip_rc(launch_router(rp, s)))) return rc;
+    if (Sh) {
+      if ((rc = hip_rc(launch_quant_int8(0, x, T, L->hidden, xq, xs, s)))) return rc;
+      gu.xq = xq;
+      gu.xs = xs;
+      rc = hip_rc(launch_gate_up_int8(gu, s));
+    }
+  }
+  if (rc) return rc;
+
+  // 2, 3. the FP4 gate/up over every pair with the shared down beside it, then the down
+  // that adds everything up
+  float* h = (float*)(base + m.routed.h);
+  Down1Params d = down1_params(L, h, ids, rw, T, err_of(ws, m.routed));
+  const bool fp4 = L->gate.fmt == MOEQ_FMT_MXFP4 || L->gate.fmt == MOEQ_FMT_NVFP4;
+  if (fp4 && gu_direct(L, T) && gu1_mx4_fits(L->inter, L->hidden) && scales16(L->gate) && scales16(L->up) &&
+      dn_direct(L, T, h) && down1_final_fits(L->down.fmt, d) && (!Sh || moe_shared_down_fits(T, Sh->inter))) {
+    GemvParams p = gemv_params(L, L->gate, &L->up, ws, m.routed);
+    p.act = x;
+    p.ids = ids;
+    p.T = T;
+    p.out = h;
+    p.mode = MODE_DIRECT;
+    dn.y = y32;
+    if ((rc = hip_rc(launch_gu1_fp4_shared(L->gate.fmt, p, T * L->top_k, dn, s)))) return rc;
+    d.add = Sh ? y32 : nullptr;
+    d.y16 = (uint16_t*)y;
+    return hip_rc(launch_down1_final(L->down.fmt, d, s));
+  }
+
+  // other formats and more tokens: the routed layer by its own path, then the shared down,
+  // which adds it
+  if ((rc = forward(L, x, ids, rw, T, y32, ws, m.routed, s))) return rc;
+  if (!Sh) return hip_rc(launch_to_bf16(y32, (size_t)T * L->hidden, (uint16_t*)y, s));
+  dn.add = y32;
+  dn.out_bf16 = 1;
+  dn.y = y;
+  if (few_bf16_fits(T, Sh->inter)) return hip_rc(launch_linear_int8_few(dn, true, s));
+  if ((rc = hip_rc(launch_quant_int8(1, hsh, T, Sh->inter, hq, hs, s)))) return rc;
+  dn.xq = hq;
+  dn.xs = hs;
+  return hip_rc(launch_linear_int8(dn, s));
 }
 
 // ---------------------------------------------------------------- allocation-free scratch
@@ -1012,8 +1058,8 @@ int moeq_linear_int8_dynamic(const moeq_weight* w, int expert, const void* x, in
   p.out_bf16 = out_type == MOEQ_OUT_BF16;
   p.y = y;
   if (few) {
-    p.x = (const uint16_t*)x;
-    return hip_rc(launch_linear_int8_bf16(p, false, S(stream)));
+    p.x = x;
+    return hip_rc(launch_linear_int8_few(p, false, S(stream)));
   }
   float* xs = (float*)ws;
   int8_t* xq = (int8_t*)ws + align_up((size_t)T * 4, 256);

@@ -128,6 +128,8 @@ struct QdStage {
 #else
 #define QD_ATTR
 #endif
+// FINAL: the layer's output, bf16(P.add + y), instead of y.
+template <bool FINAL>
 __global__ __launch_bounds__(64 * QD_KPARTS * QD_SLOTS) QD_ATTR void k_down1_q2k(Down1Params P) {
   __shared__ QdStage st;
   __shared__ float red[QD_SLOTS * QD_KPARTS][16];
@@ -260,7 +262,12 @@ __global__ __launch_bounds__(64 * QD_KPARTS * QD_SLOTS) QD_ATTR void k_down1_q2k
       y += pk * u2f(__builtin_amdgcn_readlane(f2u(rwv), k));
     }
     const int r = n0 + (int)threadIdx.x;
-    if (r < P.rows) yt[r] = y;
+    if constexpr (FINAL) {
+      const size_t at = (size_t)blockIdx.y * P.rows + r;
+      if (r < P.rows) P.y16[at] = (uint16_t)f32_bf16_rne_nan(P.add ? y + P.add[at] : y);
+    } else if (r < P.rows) {
+      yt[r] = y;
+    }
   }
   if (!ok && blockIdx.x == 0 && lane == 0 && part == 0) atomicOr(P.err, 1u);
 }
@@ -565,7 +572,14 @@ bool down1_q2k_fits(int rows, int cols, int top_k) {
 hipError_t launch_down1_q2k(const Down1Params& p, hipStream_t s) {
   if (!down1_q2k_fits(p.rows, p.cols, p.top_k)) return hipErrorInvalidValue;
   dim3 g((unsigned)((p.rows + 15) / 16), (unsigned)(p.T > 1 ? p.T : 1)), b((unsigned)(64 * QD_KPARTS * p.top_k));
-  hipLaunchKernelGGL(k_down1_q2k, g, b, 0, s, p);
+  hipLaunchKernelGGL(k_down1_q2k<false>, g, b, 0, s, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_down1_q2k_final(const Down1Params& p, hipStream_t s) {
+  if (!down1_q2k_fits(p.rows, p.cols, p.top_k)) return hipErrorInvalidValue;
+  dim3 g((unsigned)((p.rows + 15) / 16), (unsigned)(p.T > 1 ? p.T : 1)), b((unsigned)(64 * QD_KPARTS * p.top_k));
+  hipLaunchKernelGGL(k_down1_q2k<true>, g, b, 0, s, p);
   return hipGetLastError();
 }
 

@@ -34,8 +34,7 @@
 // in wave order.
 #include <hip/hip_ext.h>
 
-#include "moeq_device.h"
-#include "moeq_kernels.h"
+#include "moeq_int8.h"
 
 namespace moeq {
 
@@ -106,7 +105,7 @@ struct MxStage {
 // the terms.)
 
 template <int FMT, int DEPTH>  // DEPTH: K steps in flight per wave
-__global__ __launch_bounds__(64 * MX_WAVES) void k_gu1_fp4(GemvParams P) {
+__device__ __forceinline__ void gu1_fp4(const GemvParams& P, const int tile, const int slot) {
   constexpr bool NV = FMT == FMT_NVFP4;
   __shared__ MxStage st;
   __shared__ float red[MX_WAVES][2][16];
@@ -115,8 +114,7 @@ __global__ __launch_bounds__(64 * MX_WAVES) void k_gu1_fp4(GemvParams P) {
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int slot = blockIdx.y;
-  const int n0 = blockIdx.x * 16;
+  const int n0 = tile * 16;
   const int K = P.cols;
   const int nsteps = K / 128;
   const int e = P.ids[slot];
@@ -334,7 +332,27 @@ __global__ __launch_bounds__(64 * MX_WAVES) void k_gu1_fp4(GemvParams P) {
     us *= s2u;
     const int r = n0 + (int)threadIdx.x;
     if (r < P.rows) P.out[(size_t)slot * P.rows + r] = ok ? silu_mul(gs, us) : 0.f;
-    if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(P.err, 1u);
+    if (!ok && tile == 0 && threadIdx.x == 0) atomicOr(P.err, 1u);
+  }
+}
+
+template <int FMT, int DEPTH>
+__global__ __launch_bounds__(64 * MX_WAVES) void k_gu1_fp4(GemvParams P) {
+  gu1_fp4<FMT, DEPTH>(P, blockIdx.x, blockIdx.y);
+}
+
+// The whole layer's second launch: the shared expert's down projection (whose h the first
+// launch left) in the first D.rows / 16 work-groups, the routed gate/up in the others. The
+// two need nothing of each other; alone the shared one has too few work-groups to draw the
+// memory's bandwidth.
+template <int FMT, int DEPTH, int TPW, int CPL>
+__global__ __launch_bounds__(64 * MX_WAVES) void k_gu1_fp4_shared(GemvParams P, Int8Params D) {
+  const int nd = (D.rows + 15) / 16, b = (int)blockIdx.x - nd;
+  if (b < 0) {
+    int8_few<1, TPW, CPL, MX_WAVES, 1>(D, blockIdx.x);
+  } else {
+    const int tiles = (P.rows + 15) / 16;
+    gu1_fp4<FMT, DEPTH>(P, b % tiles, b / tiles);
   }
 }
 
@@ -356,6 +374,8 @@ struct DmStage {
   uint8_t sc[DM_TERMS][DM_SLOTS * DM_KMAX / 32];
 };
 
+// FINAL: the layer's output, bf16(P.add + y), instead of y.
+template <bool FINAL>
 __global__ __launch_bounds__(64 * DM_KPARTS * DM_SLOTS) void k_down1_mx4(Down1Params P) {
   __shared__ DmStage st;
   __shared__ float red[DM_SLOTS * DM_KPARTS][16];
@@ -483,7 +503,12 @@ __global__ __launch_bounds__(64 * DM_KPARTS * DM_SLOTS) void k_down1_mx4(Down1Pa
       y += pk * u2f(__builtin_amdgcn_readlane(f2u(rwv), k));
     }
     const int r = n0 + (int)threadIdx.x;
-    if (r < P.rows) yt[r] = y;
+    if constexpr (FINAL) {
+      const size_t at = (size_t)blockIdx.y * P.rows + r;
+      if (r < P.rows) P.y16[at] = (uint16_t)f32_bf16_rne_nan(P.add ? y + P.add[at] : y);
+    } else if (r < P.rows) {
+      yt[r] = y;
+    }
   }
   if (!ok && blockIdx.x == 0 && lane == 0 && part == 0) atomicOr(P.err, 1u);
 }
@@ -501,7 +526,14 @@ bool down1_mx4_fits(int rows, int cols, int top_k) {
 hipError_t launch_down1_mx4(const Down1Params& p, hipStream_t s) {
   if (!down1_mx4_fits(p.rows, p.cols, p.top_k)) return hipErrorInvalidValue;
   dim3 g((unsigned)((p.rows + 15) / 16), (unsigned)(p.T > 1 ? p.T : 1)), b((unsigned)(64 * DM_KPARTS * p.top_k));
-  hipLaunchKernelGGL(k_down1_mx4, g, b, 0, s, p);
+  hipLaunchKernelGGL(k_down1_mx4<false>, g, b, 0, s, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_down1_mx4_final(const Down1Params& p, hipStream_t s) {
+  if (!down1_mx4_fits(p.rows, p.cols, p.top_k)) return hipErrorInvalidValue;
+  dim3 g((unsigned)((p.rows + 15) / 16), (unsigned)(p.T > 1 ? p.T : 1)), b((unsigned)(64 * DM_KPARTS * p.top_k));
+  hipLaunchKernelGGL(k_down1_mx4<true>, g, b, 0, s, p);
   return hipGetLastError();
 }
 
@@ -513,6 +545,36 @@ hipError_t launch_gu1_fp4(int fmt, const GemvParams& p, int n_slots, hipStream_t
                              : k_gu1_fp4<FMT_NVFP4, MX_DEPTH>;
   if (ev) hipExtLaunchKernelGGL(k, g, b, 0, s, ev->start, ev->stop, 0, p);
   else hipLaunchKernelGGL(k, g, b, 0, s, p);
+  return hipGetLastError();
+}
+
+// Up to eight tokens of fp32 h: at most eight chunks of 8 values to a lane of four waves.
+bool moe_shared_down_fits(int T, int inter) {
+  if (T < 1 || T > 8) return false;
+  const FewPlan f = few_plan(T, inter, MX_WAVES);
+  return f.cpl <= 4;
+}
+
+hipError_t launch_gu1_fp4_shared(int fmt, const GemvParams& p, int n_slots, const Int8Params& d0, hipStream_t s) {
+  if (!gu1_mx4_fits(p.rows, p.cols) || (fmt != FMT_MXFP4 && fmt != FMT_NVFP4)) return hipErrorInvalidValue;
+  Int8Params d = d0;
+  FewPlan f{MX_WAVES, 1, 1};
+  if (d.rows > 0) {
+    if (!moe_shared_down_fits(d.T, d.cols)) return hipErrorInvalidValue;
+    f = few_plan(d.T, d.cols, MX_WAVES);
+  }
+  d.wpt = f.wpt;
+  const dim3 g((unsigned)((d.rows + 15) / 16 + (p.rows + 15) / 16 * n_slots)), b(64 * MX_WAVES);
+#define MOEQ_GUS(FMT, DEPTH)                                                                              \
+  do {                                                                                                    \
+    if (f.tpw == 2) hipLaunchKernelGGL((k_gu1_fp4_shared<FMT, DEPTH, 2, 4>), g, b, 0, s, p, d);           \
+    else if (f.cpl <= 1) hipLaunchKernelGGL((k_gu1_fp4_shared<FMT, DEPTH, 1, 1>), g, b, 0, s, p, d);      \
+    else hipLaunchKernelGGL((k_gu1_fp4_shared<FMT, DEPTH, 1, 4>), g, b, 0, s, p, d);                      \
+  } while (0)
+  if (fmt == FMT_MXFP4) MOEQ_GUS(FMT_MXFP4, MX_DEPTH);
+  else if (n_slots <= 8) MOEQ_GUS(FMT_NVFP4, MOEQ_NV_DEPTH);
+  else MOEQ_GUS(FMT_NVFP4, MX_DEPTH);
+#undef MOEQ_GUS
   return hipGetLastError();
 }
 

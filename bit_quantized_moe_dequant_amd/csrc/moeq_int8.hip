@@ -10,28 +10,11 @@
 // 2^31 in any order, so every split of K below gives the same bits. The scales
 // multiply the sum once, in fp32: int32 -> fp32 is the first rounding, two products
 // and the bias follow, and bf16 outputs are rounded once more at the store.
-#include "moeq_device.h"
-#include "moeq_kernels.h"
+#include "moeq_int8.h"
 
 namespace moeq {
 
 namespace {
-
-typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
-typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-
-// The bias and the added term of one output.
-__device__ __forceinline__ float finish(const Int8Params& P, size_t t, int r, float v) {
-  if (P.bias) v += P.bias[r];
-  if (P.add) v += P.add[t * P.rows + r];
-  return v;
-}
-
-__device__ __forceinline__ void store_out(const Int8Params& P, size_t t, int r, float v) {
-  if (P.out_bf16) reinterpret_cast<uint16_t*>(P.y)[t * P.rows + r] = (uint16_t)f32_bf16_rne_nan(v);
-  else reinterpret_cast<float*>(P.y)[t * P.rows + r] = v;
-}
 
 // ---------------------------------------------------------------- quantisation
 // One work-group per token, 16 values per thread and step (two 16-byte loads for
@@ -194,131 +177,6 @@ __global__ __launch_bounds__(64 * S_WAVES) void k_int8_few(Int8Params P) {
       else f = finish(P, t0 + tk, r0 + c, f);
       store_out(P, t0 + tk, r0 + c, f);
     }
-  }
-}
-
-// The same product from bf16 tokens (dynamic quantisation): every work-group makes the codes
-// of its up to 16 tokens itself, in LDS, while its weight loads are on their way; a second
-// launch and a round trip of the codes through memory cost more at these sizes than the
-// repeated conversion. Wave w works on tokens w / WPT + (8 / WPT) j (WPT waves to a token,
-// TPW tokens to a wave), lane l on chunks of 8 values l, l + 64 WPT, ... (CPL of them).
-constexpr int F_LDS = 65536;  // codes of all tokens
-
-template <int MATS, int TPW, int CPL>
-__global__ __launch_bounds__(512) void k_int8_few_bf16(Int8Params P) {
-  constexpr int W = 8, U = 8;
-  __shared__ __attribute__((aligned(16))) uint8_t code[F_LDS + 17 * 16 + 64];  // rows K + 16 apart
-  __shared__ int32_t red[MATS][W][16][17];
-  __shared__ uint32_t top[W][2];
-  __shared__ float sc[16];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n = lane & 15, g = lane >> 4;
-  const int r0 = blockIdx.x * 16;
-  const int K = P.cols, pitch = K + 16;
-  const int wpt = P.wpt, per = W / wpt;  // waves to a token, tokens at a time
-  const int sub = wave % wpt;
-
-  // tokens first, then the weights: the conversion waits for the former only
-  u32x4 v[TPW][CPL];
-#pragma unroll
-  for (int j = 0; j < TPW; j++) {
-    const int t = min(wave / wpt + per * j, P.T - 1);
-#pragma unroll
-    for (int c = 0; c < CPL; c++)
-      v[j][c] = ld16(P.x + (size_t)t * K + 8 * min(lane + 64 * (sub + wpt * c), K / 8 - 1));
-  }
-  __builtin_amdgcn_sched_barrier(0);
-  const int steps = (K + 63) / 64;
-  const int spw = (steps + W - 1) / W;
-  const int s0 = wave * spw, s1 = min(s0 + spw, steps);
-  const int8_t* wr[MATS];
-#pragma unroll
-  for (int m = 0; m < MATS; m++) wr[m] = (m ? P.w2 : P.w) + (size_t)min(r0 + n, P.rows - 1) * K;
-  u32x4 wv[U][MATS];
-  auto load = [&](int s) {
-#pragma unroll
-    for (int u = 0; u < U; u++)
-#pragma unroll
-      for (int m = 0; m < MATS; m++) wv[u][m] = ld16(wr[m] + min(64 * (s + u) + 16 * g, K - 16));
-  };
-  load(s0);
-  __builtin_amdgcn_sched_barrier(0);
-
-  uint32_t m[TPW];
-#pragma unroll
-  for (int j = 0; j < TPW; j++) {
-    m[j] = 0;
-#pragma unroll
-    for (int c = 0; c < CPL; c++)  // chunks past the row's end repeat its last one
-#pragma unroll
-      for (int k = 0; k < 4; k++) m[j] = max(max(m[j], (v[j][c][k] << 16) & 0x7FFF0000u), v[j][c][k] & 0x7FFF0000u);
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) m[j] = max(m[j], (uint32_t)__shfl_xor((int)m[j], o, 64));
-    if (lane == 0) top[wave][j] = m[j];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < TPW; j++) {
-    const int t = wave / wpt + per * j;
-    for (int w = 0; w < wpt; w++) m[j] = max(m[j], top[wave - sub + w][j]);
-    const float s = int8_scale(m[j]), r = 1.0f / s;
-    if (t < P.T) {  // uniform
-      if (sub == 0 && lane == 0) sc[t] = s;
-#pragma unroll
-      for (int c = 0; c < CPL; c++) {
-        const int ch = lane + 64 * (sub + wpt * c);
-        float f[8];
-        uint32_t q[2];
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-          f[2 * k] = u2f(v[j][c][k] << 16);
-          f[2 * k + 1] = u2f(v[j][c][k] & 0xFFFF0000u);
-        }
-        int8_codes(f, s, r, q);
-        if (ch < K / 8) *reinterpret_cast<u32x2*>(&code[t * pitch + 8 * ch]) = u32x2{q[0], q[1]};
-      }
-    }
-  }
-  __syncthreads();
-
-  const uint8_t* xr = code + min(n, P.T - 1) * pitch + 16 * g;
-  i32x4 acc[MATS];
-#pragma unroll
-  for (int mt = 0; mt < MATS; mt++) acc[mt] = i32x4{0, 0, 0, 0};
-  for (int s = s0; s < s1; s += U) {
-    if (s > s0) load(s);
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-      if (s + u < s1) {  // uniform; in the last step weights past K are zeros (and the codes there old bytes)
-        const i32x4 xv = *reinterpret_cast<const i32x4*>(xr + 64 * (s + u));
-#pragma unroll
-        for (int mt = 0; mt < MATS; mt++) {
-          if (64 * (s + u) + 16 * g >= K) wv[u][mt] = u32x4{0u, 0u, 0u, 0u};
-          acc[mt] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, wv[u][mt]), xv, acc[mt], 0, 0, 0);
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int mt = 0; mt < MATS; mt++)
-#pragma unroll
-    for (int r = 0; r < 4; r++) red[mt][wave][n][4 * g + r] = acc[mt][r];
-  __syncthreads();
-  const int i = threadIdx.x, tk = i >> 4, c = i & 15;
-  if (i < 256 && tk < P.T && r0 + c < P.rows) {
-    int sum[MATS];
-#pragma unroll
-    for (int mt = 0; mt < MATS; mt++) {
-      sum[mt] = 0;
-#pragma unroll
-      for (int w = 0; w < W; w++) sum[mt] += red[mt][w][tk][c];
-    }
-    const float xs = sc[tk];
-    float f = (float)sum[0] * xs * P.ws[r0 + c];
-    if constexpr (MATS == 2) f = silu_mul(f, (float)sum[1] * xs * P.ws2[r0 + c]);
-    else f = finish(P, tk, r0 + c, f);
-    store_out(P, tk, r0 + c, f);
   }
 }
 
@@ -585,37 +443,35 @@ hipError_t launch_dequant_int8(const int8_t* w, const float* ws, int rows, int c
   return hipGetLastError();
 }
 
-// T up to 16, rounded up to a power of two times cols within the staged codes (and so at
-// most 16 chunks to a lane).
+// T up to 16, rounded up to a power of two times cols at most 65536 (16 chunks to a lane).
 bool few_bf16_fits(int T, int cols) {
-  int t = 1;
-  while (t < T) t *= 2;
-  return T >= 1 && T <= 16 && (long)t * cols <= F_LDS;
+  if (T < 1 || T > 16) return false;
+  const FewPlan f = few_plan(T, cols, 8);
+  return f.tpw * f.cpl <= 16;
 }
 
-// P.x in place of the codes (few_bf16_fits).
-hipError_t launch_linear_int8_bf16(const Int8Params& p0, bool gate_up, hipStream_t s) {
+namespace {
+template <int MATS, int TPW, int CPL, int IN_F32>
+__global__ __launch_bounds__(512) void k_int8_few_x(Int8Params P) { int8_few<MATS, TPW, CPL, 8, IN_F32>(P, blockIdx.x); }
+
+template <int MATS, int IN_F32>
+hipError_t few_x(const Int8Params& p0, hipStream_t s) {
   Int8Params p = p0;
-  if (!few_bf16_fits(p.T, p.cols) || p.rows < 1 || p.cols < 16 || p.cols % 16) return hipErrorInvalidValue;
-  p.wpt = p.T <= 1 ? 8 : p.T <= 2 ? 4 : p.T <= 4 ? 2 : 1;
-  const int cpl = (p.cols / 8 + 64 * p.wpt - 1) / (64 * p.wpt);  // chunks per lane and token
+  const FewPlan f = few_plan(p.T, p.cols, 8);
+  p.wpt = f.wpt;
   const dim3 g((unsigned)((p.rows + 15) / 16)), b(512);
-#define MOEQ_FEW(TPW, CPL)                                                                \
-  do {                                                                                    \
-    if (gate_up) hipLaunchKernelGGL((k_int8_few_bf16<2, TPW, CPL>), g, b, 0, s, p);       \
-    else hipLaunchKernelGGL((k_int8_few_bf16<1, TPW, CPL>), g, b, 0, s, p);               \
-    return hipGetLastError();                                                             \
-  } while (0)
-  if (p.T <= 8) {  // one token at most to a wave
-    if (cpl <= 1) MOEQ_FEW(1, 1);
-    if (cpl <= 4) MOEQ_FEW(1, 4);
-    if (cpl <= 16) MOEQ_FEW(1, 16);
-  } else {
-    if (cpl <= 2) MOEQ_FEW(2, 2);
-    if (cpl <= 8) MOEQ_FEW(2, 8);
-  }
-#undef MOEQ_FEW
-  return hipErrorInvalidValue;
+  if (f.tpw == 1 && f.cpl <= 1) hipLaunchKernelGGL((k_int8_few_x<MATS, 1, 1, IN_F32>), g, b, 0, s, p);
+  else if (f.tpw == 1 && f.cpl <= 4) hipLaunchKernelGGL((k_int8_few_x<MATS, 1, 4, IN_F32>), g, b, 0, s, p);
+  else if (f.tpw == 1) hipLaunchKernelGGL((k_int8_few_x<MATS, 1, 16, IN_F32>), g, b, 0, s, p);
+  else if (f.cpl <= 2) hipLaunchKernelGGL((k_int8_few_x<MATS, 2, 2, IN_F32>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((k_int8_few_x<MATS, 2, 8, IN_F32>), g, b, 0, s, p);
+  return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_linear_int8_few(const Int8Params& p, bool in_f32, hipStream_t s) {
+  if (!few_bf16_fits(p.T, p.cols) || p.rows < 1 || p.cols < 16 || p.cols % 16) return hipErrorInvalidValue;
+  return in_f32 ? few_x<1, 1>(p, s) : few_x<1, 0>(p, s);
 }
 
 hipError_t launch_linear_int8(const Int8Params& p0, hipStream_t s) {

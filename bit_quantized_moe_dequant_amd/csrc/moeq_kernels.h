@@ -68,6 +68,9 @@ struct Down1Params {
   float* y;
   uint32_t* err;
   int rows_per_wg, U;
+  // the whole layer's last launch (launch_down1_final): y16 = bf16(add + the sum)
+  const float* add;  // fp32 [T][rows] or null
+  uint16_t* y16;     // bf16 [T][rows]
 };
 
 
@@ -119,8 +122,8 @@ struct Int8Params {
   // gate/up pair (launch_gate_up_int8): w, ws hold the gate, these the up matrix
   const int8_t* w2;
   const float* ws2;
-  // launch_linear_int8_bf16: the tokens in place of xq, xs
-  const uint16_t* x;  // bf16 [T][cols], 16-byte aligned
+  // launch_linear_int8_few: the tokens in place of xq, xs
+  const void* x;      // bf16 or fp32 [T][cols], 16-byte aligned
   int wpt;            // set by the launch: waves to a token
 };
 
@@ -209,12 +212,23 @@ hipError_t launch_nv4_to_mx4(const uint8_t* nib, const uint8_t* e4m3, const floa
 // Per-token int8 codes and scales of bf16 (in_f32 = 0) or fp32 rows; K % 16 == 0.
 hipError_t launch_quant_int8(int in_f32, const void* x, int T, int K, int8_t* q, float* scale, hipStream_t s);
 hipError_t launch_linear_int8(const Int8Params& p, hipStream_t s);
-// The product (or the gate/up pair) from bf16 tokens p.x in one launch, for a few of them.
+// The product from tokens p.x (bf16 or fp32) in one launch, for a few of them.
 bool few_bf16_fits(int T, int cols);
-hipError_t launch_linear_int8_bf16(const Int8Params& p, bool gate_up, hipStream_t s);
+hipError_t launch_linear_int8_few(const Int8Params& p, bool in_f32, hipStream_t s);
 // h[T][rows] (fp32, p.y) = silu(gate) * up of an INT8 gate/up pair, as launch_linear_int8 for each.
 hipError_t launch_gate_up_int8(const Int8Params& p, hipStream_t s);
 bool router_few_fits(int T);
+// The whole layer for a few tokens in three launches (see moeq_moe.hip): the router beside
+// the shared gate/up pair (g.y = h fp32); the routed gate/up beside the shared down (d.x =
+// h, d.y fp32); the routed down with the sum of both, as bf16. No shared expert: rows = 0.
+bool moe_front_fits(int T, int hidden);
+bool moe_shared_down_fits(int T, int inter);
+hipError_t launch_moe_front(const RouterParams& r, const Int8Params& g, hipStream_t s);
+hipError_t launch_gu1_fp4_shared(int fmt, const GemvParams& p, int n_slots, const Int8Params& d, hipStream_t s);
+bool down1_final_fits(int fmt, const Down1Params& p);
+hipError_t launch_down1_final(int fmt, const Down1Params& p, hipStream_t s);
+hipError_t launch_down1_mx4_final(const Down1Params& p, hipStream_t s);
+hipError_t launch_down1_q2k_final(const Down1Params& p, hipStream_t s);
 hipError_t launch_router(const RouterParams& p, hipStream_t s);
 // y bf16 = x fp32, n values.
 hipError_t launch_to_bf16(const float* x, size_t n, uint16_t* y, hipStream_t s);
