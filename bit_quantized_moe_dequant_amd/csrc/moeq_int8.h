@@ -7,7 +7,6 @@
 namespace moeq {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 
 // The bias and the added term of one output.
 __device__ __forceinline__ float finish(const Int8Params& P, size_t t, int r, float v) {
