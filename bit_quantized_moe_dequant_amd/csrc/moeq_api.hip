@@ -519,19 +519,26 @@ int check_moe(const moeq_layer* L, const moeq_router* R, const moeq_shared* S) {
   return check_shared(L, S);
 }
 
-size_t router_bytes(const moeq_router* R, int T) { return 256 + align_up((size_t)T * R->n_experts * 8, 256); }
+// The router's scratch: the experts' norms, then logits (fp64) or parts of them (fp32).
+size_t router_scratch(int E, int T) {
+  const size_t per = router_few_fits(T) ? 8 : 4 * ROUTER_MM_Z;
+  return align_up((size_t)E * 8, 256) + align_up((size_t)T * E * per, 256);
+}
+size_t router_bytes(const moeq_router* R, int T) { return 256 + router_scratch(R->n_experts, T); }
 
 // The counters of the one-launch router lie in the workspace's header, which the caller
 // has zeroed once; every launch leaves them at zero.
 static_assert(64 + 4 * (ROUTER_FEW_T / 8) <= 256, "the counters fit the header");
 RouterParams router_params(const moeq_router* R, const void* x, int T, int32_t* ids, float* rw, void* ws,
-                           double* logits) {
+                           uint8_t* scratch) {
   RouterParams p;
   memset(&p, 0, sizeof(p));
   p.x = (const uint16_t*)x;
   p.w = (const uint16_t*)R->weight;
   p.bias = R->bias;
-  p.logits = logits;
+  p.norms = (double*)scratch;
+  p.logits = (double*)(scratch + align_up((size_t)R->n_experts * 8, 256));
+  p.approx = (float*)p.logits;
   p.count = (uint32_t*)((uint8_t*)ws + 64);
   p.ids = ids;
   p.rw = rw;
@@ -560,7 +567,7 @@ MoeLayout moe_layout(const moeq_layer* L, const moeq_shared* S, int T) {
     off += align_up(bytes, 256);
     return at;
   };
-  m.logits = take((size_t)T * L->n_experts * 8);
+  m.logits = take(router_scratch(L->n_experts, T));
   m.ids = take((size_t)T * L->top_k * 4);
   m.rw = take((size_t)T * L->top_k * 4);
   m.y = take((size_t)T * L->hidden * 4);
@@ -586,7 +593,7 @@ int moe_forward(const moeq_layer* L, const moeq_router* R, const moeq_shared* Sh
   float* xs = (float*)(base + m.xs);
   float* hs = (float*)(base + m.hs);
   float* hsh = (float*)(base + m.h);  // the shared expert's h
-  const RouterParams rp = router_params(R, x, T, ids, rw, ws, (double*)(base + m.logits));
+  const RouterParams rp = router_params(R, x, T, ids, rw, ws, base + m.logits);
   Int8Params gu, dn;
   memset(&gu, 0, sizeof(gu));
   memset(&dn, 0, sizeof(dn));
@@ -1083,7 +1090,7 @@ int moeq_router_topk(const moeq_router* R, const void* x, int T, int32_t* ids, f
   if (!ws || ws_bytes < router_bytes(R, T)) return MOEQ_E_WORKSPACE;
   if (!aligned(ws, 256)) return MOEQ_E_ALIGN;
   if (T == 0) return MOEQ_OK;
-  return hip_rc(launch_router(router_params(R, x, T, ids, rw, ws, (double*)((uint8_t*)ws + 256)), S(stream)));
+  return hip_rc(launch_router(router_params(R, x, T, ids, rw, ws, (uint8_t*)ws + 256), S(stream)));
 }
 
 size_t moeq_moe_workspace_bytes(const moeq_layer* L, const moeq_router* R, const moeq_shared* Sh, int T) {

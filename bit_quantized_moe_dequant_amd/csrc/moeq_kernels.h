@@ -128,6 +128,7 @@ struct Int8Params {
 };
 
 constexpr int ROUTER_FEW_T = 64;  // tokens of the one-launch router
+constexpr int ROUTER_MM_Z = 4;    // parts of the hidden size whose sums are kept apart
 // Scores of the router, in the order of MOEQ_SCORE_*.
 enum { SCORE_SOFTMAX = 0, SCORE_SIGMOID = 1, SCORE_SQRT_SOFTPLUS = 2 };
 struct RouterParams {
@@ -135,6 +136,8 @@ struct RouterParams {
   const uint16_t* w;  // bf16 [n_experts][hidden]
   const float* bias;  // [n_experts] or null
   double* logits;     // [T][n_experts] workspace
+  float* approx;      // [up to ROUTER_MM_Z][T][n_experts] workspace (the same memory)
+  double* norms;      // [n_experts] workspace
   uint32_t* count;    // ROUTER_FEW_T / 8 counters, zero between launches
   int32_t* ids;       // [T][top_k]
   float* rw;          // [T][top_k]

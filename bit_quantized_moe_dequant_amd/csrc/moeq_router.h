@@ -6,10 +6,29 @@
 
 namespace moeq {
 
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v) {  // v + the lane that CTRL names (0 outside the rows)
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, false);
+  return v + __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+}
+
+__device__ __forceinline__ double read_lane(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane) |
+                                        ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane) << 32));
+}
+
+// The sum over the wave (all lanes active), as wave_max gathers its maximum.
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-  return v;
+  v = dpp_add<0x111, 0xF>(v);
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);
+  v = dpp_add<0x143, 0xC>(v);
+  return read_lane(v, 63);
 }
 
 // Scores that need no other expert's logit.
@@ -38,7 +57,26 @@ __device__ __forceinline__ void choose(const RouterParams& P, int t, int lane) {
     s[i] = -__builtin_inf();
     if (lane + 64 * i < P.n_experts) s[i] = SCORED ? get_agent(z + lane + 64 * i) : z[lane + 64 * i];
   }
+  // Keys as integers in the order of the numbers: a NaN counts as -inf, -0 as 0, and an
+  // expert that is taken or past the end is 0, below every number. A softmax without a bias
+  // orders by the logits.
+  uint32_t hi[N], lo[N];
+  auto keys = [&](const double (&v)[N], bool biased) {
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      const int e = lane + 64 * i;
+      double k = v[i];
+      if (biased && e < P.n_experts) k += (double)P.bias[e];
+      k = k == k ? k + 0.0 : -__builtin_inf();
+      uint64_t b = __builtin_bit_cast(uint64_t, k);
+      b ^= (uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull;
+      if (e >= P.n_experts) b = 0;
+      hi[i] = (uint32_t)(b >> 32);
+      lo[i] = (uint32_t)b;
+    }
+  };
   if (P.scoring == SCORE_SOFTMAX) {
+    if (!P.bias) keys(s, false);
     double m = -__builtin_inf();
 #pragma unroll
     for (int i = 0; i < N; i++) m = s[i] > m ? s[i] : m;
@@ -56,24 +94,13 @@ __device__ __forceinline__ void choose(const RouterParams& P, int t, int lane) {
     sum = wave_sum(sum);
 #pragma unroll
     for (int i = 0; i < N; i++) s[i] /= sum;
-  } else if (!SCORED) {
+    if (P.bias) keys(s, true);
+  } else {
+    if (!SCORED) {
 #pragma unroll
-    for (int i = 0; i < N; i++) s[i] = score_of(P.scoring, s[i]);
-  }
-  // Keys as integers in the order of the numbers: a NaN counts as -inf, -0 as 0, and an
-  // expert that is taken or past the end is 0, below every number.
-  uint32_t hi[N], lo[N];
-#pragma unroll
-  for (int i = 0; i < N; i++) {
-    const int e = lane + 64 * i;
-    double k = s[i];
-    if (P.bias && e < P.n_experts) k += (double)P.bias[e];
-    k = k == k ? k + 0.0 : -__builtin_inf();
-    uint64_t b = __builtin_bit_cast(uint64_t, k);
-    b ^= (uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull;
-    if (e >= P.n_experts) b = 0;
-    hi[i] = (uint32_t)(b >> 32);
-    lo[i] = (uint32_t)b;
+      for (int i = 0; i < N; i++) s[i] = score_of(P.scoring, s[i]);
+    }
+    keys(s, P.bias != nullptr);
   }
   double mine = 0.0, sum = 0.0;
   for (int k = 0; k < P.top_k; k++) {
@@ -109,9 +136,7 @@ __device__ __forceinline__ void choose(const RouterParams& P, int t, int lane) {
         sc = s[i];
         if (lane == src) hi[i] = lo[i] = 0;
       }
-    const uint64_t sb = __builtin_bit_cast(uint64_t, sc);
-    sc = __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)sb, src) |
-                                        ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(sb >> 32), src) << 32));
+    sc = read_lane(sc, src);
     sum += sc;
     if (lane == k) {
       mine = sc;
@@ -181,14 +206,16 @@ __device__ __forceinline__ void router_few(const RouterParams& P, int block, int
     put_agent(P.logits + (size_t)(t0 + t) * P.n_experts + block * RF_EXPERTS + j,
               P.scoring == SCORE_SOFTMAX ? z : score_of(P.scoring, z));
   }
-  // The stores above are acknowledged from where every XCD reads them before the count.
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const int blocks = (P.n_experts + RF_EXPERTS - 1) / RF_EXPERTS;
-    const uint32_t before = __hip_atomic_fetch_add(P.count + group, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    is_last = before == (uint32_t)blocks - 1;
-    if (is_last) __hip_atomic_store(P.count + group, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next launch
+  static_assert(RF_EXPERTS * RF_TOK <= 64, "the scores are the first wave's");
+  if (wave == 0) {
+    // The stores above are acknowledged from where every XCD reads them before the count.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if (lane == 0) {
+      const int blocks = (P.n_experts + RF_EXPERTS - 1) / RF_EXPERTS;
+      const uint32_t before = __hip_atomic_fetch_add(P.count + group, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      is_last = before == (uint32_t)blocks - 1;
+      if (is_last) __hip_atomic_store(P.count + group, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next launch
+    }
   }
   __syncthreads();
   if (is_last && wave < tn) {

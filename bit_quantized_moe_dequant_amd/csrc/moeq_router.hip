@@ -11,6 +11,7 @@
 // of two bf16 values is exact in fp64 and the vector unit issues fp64 FMAs at the fp32
 // rate here, so the exactness costs the conversions only.
 #include "moeq_router.h"
+#include "moeq_tiled.h"
 
 namespace moeq {
 
@@ -68,6 +69,333 @@ __global__ __launch_bounds__(256) void k_router_choose(RouterParams P) {
   else choose<16, false>(P, t, lane);
 }
 
+// ---------------------------------------------------------------- many tokens
+// All E logits of a token in fp64 cost the vector unit 2 E H conversions and FMAs, of which
+// the choice needs only a few exactly. So:
+//
+//   1. approximate logits on the bf16 matrix instruction, whose fp32 sums are added up in
+//      fp64 every RM_FLUSH steps (k_router_mm);
+//   2. one wave per token (k_router_pick): with |approximate - exact| <= d_e, the key at
+//      z_e + d_e is an upper bound of the expert's exact key. The K experts with the
+//      largest bounds get exact logits; then, while some other expert's bound reaches the
+//      K-th exact key, the one with the largest bound does too. What is left cannot be
+//      chosen.
+//
+// The bound: an fp32 sum of products p_1 .. p_n in any order errs by at most (additions a
+// term passes through) u sum |p_i|, and sum |p_i| <= |W_e| |x_t| (Cauchy-Schwarz). Between
+// two flushes a sum passes RM_FLUSH * 4 instructions, each adding 16 products in an order
+// that is not documented: at most 16 + 4 RM_FLUSH additions with u <= 2^-23 (truncation
+// included); twice that is taken, with the rounding of the ROUTER_MM_Z stored parts, and
+// 2^-100 for products that underflow.
+//
+// Measured at 2048 tokens, 4096 x 256: 262 us with all logits in fp64.
+constexpr int RM_FLUSH = 4;          // steps of 64 products
+constexpr int RM_E = 64, RM_T = 64;  // experts and tokens of a tile
+
+__global__ __launch_bounds__(256) void k_router_mm(RouterParams P, int z_count, int z_bytes, int tiles) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if ((int)blockIdx.x >= tiles * z_count) {  // |W_e|, one expert to a wave
+    const int e = ((int)blockIdx.x - tiles * z_count) * 4 + wave;
+    if (e >= P.n_experts) return;
+    double q = 0.0;
+    for (int c = lane; c < P.hidden / 8; c += 64) {
+      const u32x4 v = ld16(P.w + (size_t)e * P.hidden + 8 * (size_t)c);
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const double lo = (double)u2f(v[j] << 16), hi = (double)u2f(v[j] & 0xFFFF0000u);
+        q = __builtin_fma(lo, lo, __builtin_fma(hi, hi, q));
+      }
+    }
+    q = wave_sum(q);
+    if (lane == 0) P.norms[e] = sqrt(q);
+    return;
+  }
+  __shared__ __attribute__((aligned(16))) uint8_t lds[tiled_lds<2, 2, 1, 1, 4, 128>()];
+  const int z = blockIdx.x / tiles;
+  int be, bt;
+  tile_of(blockIdx.x % tiles, (P.n_experts + RM_E - 1) / RM_E, (P.T + RM_T - 1) / RM_T, be, bt);
+  const int e0 = be * RM_E, t0 = bt * RM_T, pitch = 2 * P.hidden;
+  f32x16 acc[1][1];
+  double sum[16];
+#pragma unroll
+  for (int r = 0; r < 16; r++) sum[r] = 0.0;
+  auto flush = [&](int s) {
+    if (s % RM_FLUSH == RM_FLUSH - 1) {
+#pragma unroll
+      for (int r = 0; r < 16; r++) {
+        sum[r] += (double)acc[0][0][r];
+        acc[0][0][r] = 0.f;
+      }
+    }
+  };
+  tiled_product<MmaBf16, 2, 2, 1, 1, 4, 128, 4, 1>(
+      reinterpret_cast<const int8_t*>(P.w) + (size_t)e0 * pitch + z * z_bytes, P.n_experts - e0,
+      reinterpret_cast<const int8_t*>(P.x) + (size_t)t0 * pitch + z * z_bytes, P.T - t0, pitch,
+      min(z_bytes, pitch - z * z_bytes), lds, acc, flush);
+  flush(RM_FLUSH - 1);
+  const int wm = wave & 1, wn = wave >> 1, n = lane & 31, g = lane >> 5;
+  const int t = t0 + 32 * wn + n;
+  if (t < P.T) {
+    float* out = P.approx + ((size_t)z * P.T + t) * P.n_experts;
+#pragma unroll
+    for (int r = 0; r < 16; r++) {
+      const int e = e0 + 32 * wm + (r & 3) + 8 * (r >> 2) + 4 * g;
+      if (e < P.n_experts) out[e] = (float)sum[r];
+    }
+  }
+}
+
+// A number as an unsigned integer of the same order; a NaN counts as -inf, -0 as 0.
+__device__ __forceinline__ uint64_t order_of(double k) {
+  k = k == k ? k + 0.0 : -__builtin_inf();
+  const uint64_t b = __builtin_bit_cast(uint64_t, k);
+  return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+}
+
+// A number not below the score of any logit that is not above v, from the fast fp32
+// functions: 2^-17 and |v| 2^-22 of it cover their errors (an ulp each, and the scaling of
+// the exponential's argument), 1e-18 what underflows.
+__device__ __forceinline__ float score_above(int scoring, float v) {
+  v = v + __builtin_fabsf(v) * 0x1p-23f;  // the rounding of v itself
+  const float slack = 0x1p-17f + __builtin_fminf(__builtin_fabsf(v), 1e6f) * 0x1p-22f;
+  if (scoring == SCORE_SIGMOID) {
+    const float p = __fdividef(1.0f, 1.0f + __expf(-v));
+    return __builtin_fminf(p + p * slack + 1e-18f, 1.0f);
+  }
+  const float e = __expf(-__builtin_fabsf(v));
+  // log(1 + e) <= e - e^2 / 2 + e^3 / 3, close where e is small and the logarithm of 1 + e is not
+  const float l = e < 0.015625f ? e * (1.0f - e * (0.5f - e * 0.33333334f)) : __logf(1.0f + e);
+  const float p = __builtin_fmaxf(v, 0.f) + l;
+  return __builtin_sqrtf(p + 2.0f * p * slack) + 1e-18f;
+}
+
+// The lane that holds the largest (value, then lowest id) and that value; by every lane.
+__device__ __forceinline__ int lane_of_max(uint64_t v, uint32_t id, uint64_t& top) {
+  const uint32_t mh = wave_max((uint32_t)(v >> 32));
+  bool in = (uint32_t)(v >> 32) == mh;
+  const uint32_t ml = wave_max(in ? (uint32_t)v : 0u);
+  in = in && (uint32_t)v == ml;
+  uint64_t who = __ballot(in);
+  if (__popcll(who) > 1) {
+    const uint32_t mi = wave_max(in ? ~id : 0u);
+    in = in && ~id == mi;
+    who = __ballot(in);
+  }
+  top = ((uint64_t)mh << 32) | ml;
+  return __ffsll((long long)who) - 1;
+}
+
+constexpr int RP_SEG = 4096;  // values of a token held at a time (64 to a lane)
+
+// Two waves to a SIMD at least: left free, the compiler hoists conversions and constants
+// until a SIMD holds one.
+template <int N>
+__global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_count, double unit) {
+  const int lane = threadIdx.x & 63;
+  const int t = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (t >= P.T) return;
+  const uint16_t* x = P.x + (size_t)t * P.hidden;
+  const int chunks = P.hidden / 8, E = P.n_experts, K = P.top_k;
+  const int segs = (chunks + RP_SEG / 8 - 1) / (RP_SEG / 8);
+
+  u32x4 xv[RP_SEG / 512];
+  auto load = [&](const uint16_t* row, int seg, u32x4 (&v)[RP_SEG / 512]) {  // chunks past the end are zeros
+#pragma unroll
+    for (int i = 0; i < RP_SEG / 512; i++) {
+      const int c = seg * (RP_SEG / 8) + lane + 64 * i;
+      v[i] = ld16(row + 8 * (size_t)min(c, chunks - 1));
+      if (c >= chunks) v[i] = u32x4{0u, 0u, 0u, 0u};
+    }
+  };
+  auto dot = [&](const u32x4 (&p)[RP_SEG / 512], const u32x4 (&q)[RP_SEG / 512]) {  // this lane's part
+    double a[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+    for (int i = 0; i < RP_SEG / 512; i++) {
+      u32x4 u = q[i];
+      // the compiler would convert the token's values once for all rows and hold 128 registers of them
+      asm volatile("" : "+v"(u));
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        a[j] = __builtin_fma((double)u2f(p[i][j] << 16), (double)u2f(u[j] << 16), a[j]);
+        a[j] = __builtin_fma((double)u2f(p[i][j] & 0xFFFF0000u), (double)u2f(u[j] & 0xFFFF0000u), a[j]);
+      }
+    }
+    return (a[0] + a[1]) + (a[2] + a[3]);
+  };
+  auto logit = [&](int e) {  // exact, by every lane
+    double a = 0.0;
+    for (int s = 0; s < segs; s++) {
+      u32x4 wv[RP_SEG / 512];
+      load(P.w + (size_t)e * P.hidden, s, wv);
+      if (segs > 1) load(x, s, xv);
+      a += dot(wv, xv);
+    }
+    return wave_sum(a);
+  };
+
+  double z[N];
+  uint64_t bound[N];  // upper bounds; 0: chosen or past the end
+  const bool soft = P.scoring == SCORE_SOFTMAX;  // (without a bias here) ordered by the logit
+  auto next = [&](int& e, uint64_t& top) {  // the largest bound left, without taking it
+    uint64_t b = bound[0];
+    uint32_t at = 0;
+#pragma unroll
+    for (int i = 1; i < N; i++)
+      if (bound[i] > b) {
+        b = bound[i];
+        at = i;
+      }
+    const int src = lane_of_max(b, lane + 64 * at, top);
+    e = src + 64 * __builtin_amdgcn_readlane((int)at, src);
+  };
+  auto take = [&](int e) {
+#pragma unroll
+    for (int i = 0; i < N; i++)
+      if (lane + 64 * i == e) bound[i] = 0;
+  };
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    const int e = lane + 64 * i;
+    z[i] = -__builtin_inf();
+    if (e < E) {
+      double v = 0.0;
+      for (int k = 0; k < z_count; k++) v += (double)P.approx[((size_t)k * P.T + t) * E + e];
+      z[i] = v;
+    }
+  }
+  // |x|, rounded up: in fp32 where its squares neither overflow nor vanish there
+  float q = 0.f;
+  for (int s = segs - 1; s >= 0; s--) {
+    load(x, s, xv);
+#pragma unroll
+    for (int i = 0; i < RP_SEG / 512; i++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const float lo = u2f(xv[i][j] << 16), hi = u2f(xv[i][j] & 0xFFFF0000u);
+        q = __builtin_fmaf(lo, lo, __builtin_fmaf(hi, hi, q));
+      }
+  }
+  double nx = wave_sum((double)q) * 1.001;  // at most 2 H / 64 + 1 roundings of 2^-24
+  if (!(nx > 1e-30 && nx < 1e38)) {
+    nx = 0.0;
+    for (int s = segs - 1; s >= 0; s--) {
+      load(x, s, xv);
+      nx += dot(xv, xv);
+    }
+    nx = wave_sum(nx);
+  }
+  nx = sqrt(nx);
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    const int e = lane + 64 * i;
+    bound[i] = 0;
+    if (e < E) {
+      double k = z[i] + (unit * P.norms[e] * nx + 0x1p-100);
+      if (!soft) k = (double)score_above(P.scoring, (float)k);
+      if (P.bias) k += (double)P.bias[e];
+      // nothing is known of a sum that left fp32's range: its exact logit is needed
+      bound[i] = __builtin_fabs(z[i]) < __builtin_inf() && k == k ? order_of(k) : ~0ull;
+      if (P.bias && P.bias[e] != P.bias[e]) bound[i] = order_of(-__builtin_inf());
+    }
+  }
+  const bool mine = lane < K;  // lane k < K: an expert of the best K so far, its exact logit and key
+  int id = 0;
+  double zk = 0.0;
+  for (int k = 0; k < K; k++) {
+    int e;
+    uint64_t top;
+    next(e, top);
+    take(e);
+    if (lane == k) id = e;
+  }
+  if (segs == 1) {  // the next expert's row is on its way while one is multiplied
+    u32x4 wv[2][RP_SEG / 512];
+    load(P.w + (size_t)__builtin_amdgcn_readlane(id, 0) * P.hidden, 0, wv[0]);
+    for (int k = 0; k < K; k += 2) {
+      load(P.w + (size_t)__builtin_amdgcn_readlane(id, min(k + 1, K - 1)) * P.hidden, 0, wv[1]);
+      const double v0 = wave_sum(dot(wv[0], xv));
+      if (lane == k) zk = v0;
+      load(P.w + (size_t)__builtin_amdgcn_readlane(id, min(k + 2, K - 1)) * P.hidden, 0, wv[0]);
+      const double v1 = wave_sum(dot(wv[1], xv));
+      if (lane == k + 1) zk = v1;
+    }
+  } else {
+    for (int k = 0; k < K; k++) {
+      const double v = logit(__builtin_amdgcn_readlane(id, k));
+      if (lane == k) zk = v;
+    }
+  }
+  auto score = [&](double v) { return soft ? v : score_of(P.scoring, v); };
+  double sk = score(zk);
+  uint64_t key = 0;
+  if (mine) key = order_of(P.bias ? sk + (double)P.bias[id] : sk);
+  for (;;) {
+    int e;
+    uint64_t top, low;
+    // the lowest of the K: the smallest key, of equal ones the highest id
+    const int worst = lane_of_max(mine ? ~key : 0ull, mine ? ~(uint32_t)id : 0xFFFFFFFFu, low);
+    low = ~low;
+    next(e, top);
+    if (top == 0 || top < low) break;
+    take(e);
+    const double v = logit(e);
+    const double s = score(v);
+    const uint64_t kv = order_of(P.bias ? s + (double)P.bias[e] : s);
+    if (kv > low || (kv == low && e < __builtin_amdgcn_readlane(id, worst))) {
+      if (lane == worst) {
+        id = e;
+        zk = v;
+        sk = s;
+        key = kv;
+      }
+    }
+  }
+
+  if (soft) {  // the normaliser over all experts: the chosen ones' logits exact, the others' not
+    double top = mine ? zk : -__builtin_inf(), sum = mine ? 1.0 : 0.0;
+#pragma unroll
+    for (int i = 0; i < N; i++) top = z[i] > top ? z[i] : top;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const double v = __shfl_xor(top, o, 64);
+      top = v > top ? v : top;
+    }
+    sk = exp(zk - top);
+    if (mine) sum = sk;
+    for (int k = 0; k < K; k++) {
+      const int e = __builtin_amdgcn_readlane(id, k);
+#pragma unroll
+      for (int i = 0; i < N; i++)
+        if (lane + 64 * i == e) z[i] = -__builtin_inf();
+    }
+#pragma unroll
+    for (int i = 0; i < N; i++) sum += lane + 64 * i < E ? exp(z[i] - top) : 0.0;
+    sk /= wave_sum(sum);
+  }
+  int rank = 0;
+  for (int k = 0; k < K; k++) {
+    const uint64_t ok = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)key, k) |
+                        ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(key >> 32), k) << 32);
+    rank += ok > key || (ok == key && __builtin_amdgcn_readlane(id, k) < id);
+  }
+  double sum = 0.0;
+  for (int r = 0; r < K; r++) sum += read_lane(sk, __ffsll((long long)__ballot(mine && rank == r)) - 1);
+  if (mine) {
+    P.ids[(size_t)t * K + rank] = id;
+    double w = sk;
+    if (P.normalize) w = sum == 0.0 ? 0.0 : w / sum;
+    P.rw[(size_t)t * K + rank] = (float)(w * (double)P.scale);
+  }
+}
+
+// Parts of K: enough work-groups for every CU, no part under 512 bytes.
+int mm_split(const RouterParams& p, long tiles) {
+  int z = 1;
+  while (z < ROUTER_MM_Z && tiles * z < 256 && p.hidden / (2 * z) >= 256) z *= 2;
+  return z;
+}
+
 }  // namespace
 
 bool router_few_fits(int T) { return T <= ROUTER_FEW_T; }
@@ -79,6 +407,20 @@ hipError_t launch_router(const RouterParams& p, hipStream_t s) {
   if (router_few_fits(p.T)) {
     const dim3 g((unsigned)((p.n_experts + RF_EXPERTS - 1) / RF_EXPERTS), (unsigned)((p.T + RF_TOK - 1) / RF_TOK));
     hipLaunchKernelGGL(k_router_few, g, dim3(512), 0, s, p);
+    return hipGetLastError();
+  }
+  // A softmax with a bias orders the experts by the normaliser too: all logits in fp64.
+  if (!(p.scoring == SCORE_SOFTMAX && p.bias)) {
+    const long tiles = (long)((p.n_experts + RM_E - 1) / RM_E) * ((p.T + RM_T - 1) / RM_T);
+    const int z = mm_split(p, tiles);
+    const int z_bytes = (2 * p.hidden / z + 127) / 128 * 128;
+    if (tiles * z > 0x7FFFFF || p.T > 0x7FFFFF) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(k_router_mm, dim3((unsigned)(tiles * z + (p.n_experts + 3) / 4)), dim3(256), 0, s, p, z, z_bytes,
+                       (int)tiles);
+    const double unit = (2.0 * (16 + 4 * RM_FLUSH) + ROUTER_MM_Z) * 0x1p-23;
+    const dim3 g((unsigned)((p.T + 3) / 4)), b(256);
+    if (p.n_experts <= 256) hipLaunchKernelGGL(k_router_pick<4>, g, b, 0, s, p, z, unit);
+    else hipLaunchKernelGGL(k_router_pick<16>, g, b, 0, s, p, z, unit);
     return hipGetLastError();
   }
   for (int t0 = 0; t0 < p.T; t0 += 65535 * R_TOK) {  // grid rows

@@ -82,9 +82,13 @@ constexpr int tiled_lds() {
   return STAGES * 32 * (WM * TM + WN * TN) * G_BK;
 }
 
-template <class M, int WM, int WN, int TM, int TN, int STAGES, int G_BK, int Q, int SPREAD>
+// after(s) is called behind step s's products and may change acc.
+struct Nothing {
+  __device__ __forceinline__ void operator()(int) const {}
+};
+template <class M, int WM, int WN, int TM, int TN, int STAGES, int G_BK, int Q, int SPREAD, class After = Nothing>
 __device__ __forceinline__ void tiled_product(const int8_t* wbase, int wrows, const int8_t* xbase, int xrows, int pitch,
-                                              int K, uint8_t* lds, typename M::Acc (&acc)[TM][TN]) {
+                                              int K, uint8_t* lds, typename M::Acc (&acc)[TM][TN], After after = {}) {
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32, WAVES = WM * WN;
   constexpr int ROWS = BM + BN;                 // rows of one buffer: channels, then tokens
   constexpr int CPR = G_BK / 16, RPC = 64 / CPR;  // chunks of a row, rows of a copy
@@ -206,11 +210,17 @@ __device__ __forceinline__ void tiled_product(const int8_t* wbase, int wrows, co
   int s = 0;
   for (; s + STAGES + 1 < full; s += 2) {
     step(s, 0, Count<1>{});
+    after(s);
     step(s + 1, SWAP, Count<1>{});
+    after(s + 1);
   }
   for (; s < steps; s += 2) {
     step(s, 0, Count<0>{});
-    if (s + 1 < steps) step(s + 1, SWAP, Count<0>{});
+    after(s);
+    if (s + 1 < steps) {
+      step(s + 1, SWAP, Count<0>{});
+      after(s + 1);
+    }
   }
 
 }

@@ -383,7 +383,8 @@ typedef struct moeq_shared {
 } moeq_shared;
 
 /* The K experts with the largest s + bias of every token, in falling order (ties: the
- * lower id first; a NaN counts below every number), and their weights s * scale, or
+ * lower id first; a NaN counts below every number; softmax without a bias: in the
+ * order of the logits), and their weights s * scale, or
  * s / (sum of the K) * scale. The logits W x are sums of exact products in fp64, and so
  * are scores and sums: the choice does not depend on an order of summation beyond
  * fp64's. x bf16 [T][H], 16-byte aligned; ids int32 [T][K] (always distinct and inside
