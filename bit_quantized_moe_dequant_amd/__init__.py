@@ -250,7 +250,8 @@ class Weight:
     def _ref(self):
         """byref of this weight's descriptor, made again when a field has changed."""
         now = (self.fmt, self.rows, self.cols, self.n_experts, self.data.data_ptr(), self.expert_stride,
-               self.scales.data_ptr(), self.scale_expert_stride, self.scale2, self.grid)
+               self.scales.data_ptr(), self.scale_expert_stride, 0 if self.scale2 is None else self.scale2.data_ptr(),
+               0 if self.grid is None else self.grid.data_ptr())
         if now != self._made:
             self._struct = self.struct()
             self._by = ctypes.byref(self._struct)
@@ -633,8 +634,9 @@ def linear_int8_dynamic(w: Weight, x, expert: int = 0, bias=None, y=None, out_dt
 class Router:
     """Router weights (bf16 [E, H]), an optional fp32 [E] bias for the choice, and the
     rule: scoring "softmax", "sigmoid" or "sqrtsoftplus"; normalize divides the chosen
-    scores by their sum; scale multiplies the route weights. The tensors are kept, their
-    contents are read by every call."""
+    scores by their sum; scale multiplies the route weights. The descriptor is taken when
+    it is made (the tensors' contents are read by every call); make a new one after
+    replacing a tensor."""
 
     def __init__(self, weight, top_k: int, scoring="softmax", normalize=False, scale=1.0, bias=None):
         torch = _torch()
@@ -647,6 +649,7 @@ class Router:
         if scoring not in SCORE_BY_NAME:
             raise ValueError(f"scoring: {scoring!r}, expected one of {', '.join(SCORE_BY_NAME)}")
         self.weight, self.bias, self.top_k = weight, bias, int(top_k)
+        self._keep = (weight, bias)  # what the descriptor points to
         self.scoring, self.normalize, self.scale = scoring, bool(normalize), float(scale)
         self._struct = MoeqRouter(self.hidden, self.n_experts, self.top_k, SCORE_BY_NAME[scoring],
                                   int(self.normalize), self.scale, weight.data_ptr(),
@@ -656,7 +659,7 @@ class Router:
 
     def workspace(self, T: int):
         """An initialised workspace for T tokens; the current stream's own (kept per stream)."""
-        return self._ws.get(T, self.weight.device, _stream_ptr().value or 0)
+        return self._ws.get(T, self._keep[0].device, _stream_ptr().value or 0)
 
 
 class SharedExpert:
@@ -679,12 +682,18 @@ class MoeLayer:
         self.hidden, self.top_k = layer.hidden, layer.top_k
         self._structs = (layer.struct(), router._struct, None if shared is None else shared.struct())
         self._refs = tuple(None if s is None else ctypes.addressof(s) for s in self._structs)
-        self._weights = [w for p in (layer, shared) if p is not None for w in (p.gate, p.up, p.down)]
+        weights = [w for p in (layer, shared) if p is not None for w in (p.gate, p.up, p.down)]
+        # what the descriptors point to
+        self._keep = router._keep + tuple(t for w in weights for t in (w.data, w.scales, w.scale2, w.grid))
+        self._device = router._keep[0].device
+        for t in self._keep:
+            if t is not None and t.device != self._device:
+                raise ValueError(f"tensor on {t.device}, but the router's weight on {self._device}")
         self._ws = _Workspaces(lambda T: _lib().moeq_moe_workspace_bytes(*self._refs, T))
 
     def workspace(self, T: int):
         """An initialised workspace for T tokens; the current stream's own (kept per stream)."""
-        return self._ws.get(T, self.router.weight.device, _stream_ptr().value or 0)
+        return self._ws.get(T, self._device, _stream_ptr().value or 0)
 
 
 class _Workspaces:
@@ -727,7 +736,7 @@ def router_topk(router: Router, x, ids=None, rw=None, ws=None):
         rw = _torch().empty((T, router.top_k), dtype=gpu[4][0], device=x.device)
     _need("ids", ids, gpu[5], (T, router.top_k))
     _need("rw", rw, gpu[4], (T, router.top_k))
-    dev = _on_device(x, ids, rw, ws, router.weight, router.bias)
+    dev = _on_device(x, ids, rw, ws, *router._keep)
     if T == 0:
         return ids, rw
     stream = gpu[1](dev)
@@ -754,7 +763,7 @@ def moe_forward(moe: MoeLayer, x, y=None, ids=None, rw=None, ws=None):
     _need("y", y, gpu[2], (T, moe.hidden))
     _need("ids", ids, gpu[5], (T, moe.top_k))
     _need("rw", rw, gpu[4], (T, moe.top_k))
-    dev = _on_device(x, y, ids, rw, ws, moe.router.weight)
+    dev = _on_device(x, y, ids, rw, ws, moe._keep[0])
     if T == 0:
         return y, ids, rw
     stream = gpu[1](dev)

@@ -259,8 +259,12 @@ hipError_t go_few(const Int8Params& p, hipStream_t s) {
 
 hipError_t launch_quant_int8(int in_f32, const void* x, int T, int K, int8_t* q, float* scale, hipStream_t s) {
   if (T < 1 || K < 16 || K % 16) return hipErrorInvalidValue;
-  if (in_f32) hipLaunchKernelGGL(k_quant_int8<1>, dim3((unsigned)T), dim3(Q_THREADS), 0, s, x, K, q, scale);
-  else hipLaunchKernelGGL(k_quant_int8<0>, dim3((unsigned)T), dim3(Q_THREADS), 0, s, x, K, q, scale);
+  for (int t = 0; t < T; t += 1 << 22) {  // a grid holds below 2^32 threads
+    const dim3 g((unsigned)(T - t < (1 << 22) ? T - t : 1 << 22));
+    const uint8_t* xt = (const uint8_t*)x + (size_t)t * K * (in_f32 ? 4 : 2);
+    if (in_f32) hipLaunchKernelGGL(k_quant_int8<1>, g, dim3(Q_THREADS), 0, s, xt, K, q + (size_t)t * K, scale + t);
+    else hipLaunchKernelGGL(k_quant_int8<0>, g, dim3(Q_THREADS), 0, s, xt, K, q + (size_t)t * K, scale + t);
+  }
   return hipGetLastError();
 }
 
@@ -307,15 +311,28 @@ hipError_t launch_linear_int8(const Int8Params& p0, hipStream_t s) {
   if (p.T < 1 || p.rows < 1 || p.cols < 16 || p.cols % 16 || p.cols > INT8_MAX_COLS) return hipErrorInvalidValue;
   if (p.T <= 16) return go_few<1, 1, 8>(p, s);
   if (p.T <= 32) return go_few<1, 2, 8>(p, s);
-  // The largest tile that still gives most of the 256 CUs one (us at T = 64 / 256 / 512 /
-  // 2048 x 4096 x 4096): 256 x 256 - / - / - / 60; 256 x 128 - / - / - / 44; 128 x 64
-  // - / 17.2 / 17.0 / 52; 64 x 64 11.7 / 12.2 / 17.7 / -; 32 x 64 10.0 / 12.9 / - / -.
-  auto tiles = [&](int bm, int bn) { return (long)((p.rows + bm - 1) / bm) * ((p.T + bn - 1) / bn); };
-  if (tiles(256, 256) >= 224) return go_tiled<2, 4, 4, 2, 2, 128, 1, 2>(p, s);
-  if (tiles(256, 128) >= 160) return go_tiled<4, 2, 2, 2, 3, 128, 1, 2>(p, s);
-  if (tiles(128, 64) >= 160) return go_tiled<4, 2, 1, 1, 3, 128, 4, 1>(p, s);
-  if (tiles(64, 64) >= 160) return go_tiled<2, 2, 1, 1, 4, 128, 4, 1>(p, s);
-  return go_tiled<1, 2, 1, 1, 4, 128, 4, 1>(p, s);
+  // The tile with the smallest estimate. A step of 128 bytes of K takes a CU, by how many
+  // work-groups it holds (measured, us): 32 x 64 0.21, 0.29, 0.39, then 0.13 each; 64 x 64
+  // 0.25, 0.44, then 0.22 each; 128 x 64 0.41, 0.72, then 0.36 each; 256 x 128 1.25 each and
+  // 256 x 256 2.2 each, one at a time. At 4096 x 4096 (us): T = 64 10.0 with 32 x 64 and 11.7
+  // with 64 x 64; T = 256 12.9, 12.2 and 17.2 with 128 x 64; T = 1000 -, 31.2, 26.7 and 34.9
+  // with 256 x 128; T = 2048 44 with 256 x 128, 60 with 256 x 256; T = 4096 86 and 79.6.
+  auto per_cu = [&](int bm, int bn) {
+    return (double)(((long)((p.rows + bm - 1) / bm) * ((p.T + bn - 1) / bn) + 255) / 256);
+  };
+  const double n0 = per_cu(32, 64), n1 = per_cu(64, 64), n2 = per_cu(128, 64);
+  const double c[5] = {n0 <= 1 ? 0.21 : n0 <= 2 ? 0.29 : 0.13 * n0, n1 <= 1 ? 0.25 : 0.22 * n1,
+                       n2 <= 1 ? 0.41 : 0.36 * n2, 1.25 * per_cu(256, 128), 2.2 * per_cu(256, 256)};
+  int best = 0;
+  for (int i = 1; i < 5; i++)
+    if (c[i] < c[best]) best = i;
+  switch (best) {
+    case 0: return go_tiled<1, 2, 1, 1, 4, 128, 4, 1>(p, s);
+    case 1: return go_tiled<2, 2, 1, 1, 4, 128, 4, 1>(p, s);
+    case 2: return go_tiled<4, 2, 1, 1, 3, 128, 4, 1>(p, s);
+    case 3: return go_tiled<4, 2, 2, 2, 3, 128, 1, 2>(p, s);
+  }
+  return go_tiled<2, 4, 4, 2, 2, 128, 1, 2>(p, s);
 }
 
 hipError_t launch_gate_up_int8(const Int8Params& p, hipStream_t s) {
