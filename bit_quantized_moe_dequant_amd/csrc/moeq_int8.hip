@@ -205,7 +205,8 @@ __device__ __forceinline__ void store4(const Int8Params& P, int t, int r, float 
 }
 
 // ---------------------------------------------------------------- many tokens
-template <int WM, int WN, int TM, int TN, int STAGES, int G_BK, int Q, int SPREAD>
+// RUNS: bf16 outputs without bias or added term, rows a multiple of 8, 16-byte aligned.
+template <int WM, int WN, int TM, int TN, int STAGES, int G_BK, int Q, int SPREAD, bool RUNS>
 __global__ __launch_bounds__(64 * WM * WN) void k_int8_tiled(Int8Params P) {
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
   __shared__ __attribute__((aligned(16))) uint8_t lds[tiled_lds<WM, WN, TM, TN, STAGES, G_BK>()];
@@ -220,16 +221,56 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_tiled(Int8Params P) {
                                                                P.T - t0, K, K, lds, acc);
   const int wm = wave % WM, wn = wave / WM;
   const int n = lane & 31, g = lane >> 5;
+  if constexpr (RUNS) {
+    // Through LDS, 32 tokens at a time and each wave for itself (past the last barrier nobody
+    // reads operands any more), so that a store writes whole runs of channels: stored from
+    // the registers, 8 bytes to a lane, a wave's store touches 32 rows (2048 x 4096 x 4096:
+    // 44.6 against 38.3 us).
+    constexpr int CH = TM * 32, PITCH = 2 * CH + 16;
+    static_assert(WM * WN * 32 * PITCH <= sizeof(lds), "the outputs of 32 tokens fit");
+    uint8_t* mine = lds + wave * 32 * PITCH;
+    const int rb = r0 + wm * CH;
 #pragma unroll
-  for (int j = 0; j < TN; j++) {
-    const int t = t0 + (wn * TN + j) * 32 + n;
-    const float xs = t < P.T ? P.xs[t] : 0.f;
+    for (int j = 0; j < TN; j++) {
+      const int tb = t0 + (wn * TN + j) * 32, t = min(tb + n, P.T - 1);
+      const float xs = P.xs[t];
 #pragma unroll
-    for (int i = 0; i < TM; i++)
+      for (int i = 0; i < TM; i++)
 #pragma unroll
-      for (int q = 0; q < 4; q++)  // four consecutive channels
-        store4(P, t, r0 + (wm * TM + i) * 32 + 8 * q + 4 * g, xs, acc[i][j][4 * q], acc[i][j][4 * q + 1],
-               acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+        for (int q = 0; q < 4; q++) {
+          const int c = i * 32 + 8 * q + 4 * g;
+          float f[4];
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            const int r = min(rb + c + e, P.rows - 1);
+            f[e] = (float)acc[i][j][4 * q + e] * xs * P.ws[r];
+          }
+          *reinterpret_cast<u32x2*>(mine + n * PITCH + 2 * c) =
+              u32x2{f32_bf16_rne_nan(f[0]) | (f32_bf16_rne_nan(f[1]) << 16),
+                    f32_bf16_rne_nan(f[2]) | (f32_bf16_rne_nan(f[3]) << 16)};
+          __builtin_amdgcn_sched_barrier(0);  // the scales of all channels at once would spill
+        }
+      constexpr int LPR = CH / 8;  // lanes to a row
+#pragma unroll
+      for (int k = 0; k < 32 * LPR / 64; k++) {
+        const int row = k * (64 / LPR) + lane / LPR, c = 8 * (lane % LPR);
+        const u32x4 v = *reinterpret_cast<const u32x4*>(mine + row * PITCH + 2 * c);
+        if (tb + row < P.T && rb + c < P.rows)
+          *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(P.y) + (size_t)(tb + row) * P.rows + rb + c) = v;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < TN; j++) {
+      const int t = t0 + (wn * TN + j) * 32 + n;
+      const float xs = t < P.T ? P.xs[t] : 0.f;
+#pragma unroll
+      for (int i = 0; i < TM; i++)
+#pragma unroll
+        for (int q = 0; q < 4; q++)  // four consecutive channels
+          store4(P, t, r0 + (wm * TM + i) * 32 + 8 * q + 4 * g, xs, acc[i][j][4 * q], acc[i][j][4 * q + 1],
+                 acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+    }
   }
 }
 
@@ -244,7 +285,11 @@ hipError_t go_tiled(const Int8Params& p, hipStream_t s) {
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
   const long blocks = (long)((p.rows + BM - 1) / BM) * ((p.T + BN - 1) / BN);
   if (blocks > 0x7FFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((k_int8_tiled<WM, WN, TM, TN, STAGES, BK, Q, SPREAD>), dim3((unsigned)blocks), dim3(64 * WM * WN), 0, s, p);
+  const dim3 g((unsigned)blocks), b(64 * WM * WN);
+  if (p.out_bf16 && p.rows % 8 == 0 && (uintptr_t)p.y % 16 == 0 && !p.bias && !p.add)
+    hipLaunchKernelGGL((k_int8_tiled<WM, WN, TM, TN, STAGES, BK, Q, SPREAD, true>), g, b, 0, s, p);
+  else
+    hipLaunchKernelGGL((k_int8_tiled<WM, WN, TM, TN, STAGES, BK, Q, SPREAD, false>), g, b, 0, s, p);
   return hipGetLastError();
 }
 
@@ -259,7 +304,7 @@ hipError_t go_few(const Int8Params& p, hipStream_t s) {
 
 hipError_t launch_quant_int8(int in_f32, const void* x, int T, int K, int8_t* q, float* scale, hipStream_t s) {
   if (T < 1 || K < 16 || K % 16) return hipErrorInvalidValue;
-  for (int t = 0; t < T; t += 1 << 22) {  // a grid holds below 2^32 threads
+  for (long t = 0; t < T; t += 1 << 22) {  // a grid holds below 2^32 threads
     const dim3 g((unsigned)(T - t < (1 << 22) ? T - t : 1 << 22));
     const uint8_t* xt = (const uint8_t*)x + (size_t)t * K * (in_f32 ? 4 : 2);
     if (in_f32) hipLaunchKernelGGL(k_quant_int8<1>, g, dim3(Q_THREADS), 0, s, xt, K, q + (size_t)t * K, scale + t);
@@ -313,16 +358,17 @@ hipError_t launch_linear_int8(const Int8Params& p0, hipStream_t s) {
   if (p.T <= 32) return go_few<1, 2, 8>(p, s);
   // The tile with the smallest estimate. A step of 128 bytes of K takes a CU, by how many
   // work-groups it holds (measured, us): 32 x 64 0.21, 0.29, 0.39, then 0.13 each; 64 x 64
-  // 0.25, 0.44, then 0.22 each; 128 x 64 0.41, 0.72, then 0.36 each; 256 x 128 1.25 each and
-  // 256 x 256 2.2 each, one at a time. At 4096 x 4096 (us): T = 64 10.0 with 32 x 64 and 11.7
-  // with 64 x 64; T = 256 12.9, 12.2 and 17.2 with 128 x 64; T = 1000 -, 31.2, 26.7 and 34.9
-  // with 256 x 128; T = 2048 44 with 256 x 128, 60 with 256 x 256; T = 4096 86 and 79.6.
+  // 0.25, 0.44, then 0.22 each; 128 x 64 0.41, 0.72, then 0.36 each; 256 x 128 1.1 each and
+  // 256 x 256 2.0 each, one at a time. At 4096 x 4096 (us): T = 64 10.0 with 32 x 64 and 11.7
+  // with 64 x 64; T = 256 12.9, 12.2 and 17.2 with 128 x 64; T = 1000 -, 30.7, 26.2 and 30.5
+  // with 256 x 128; T = 2048 48 with 128 x 64, 38.4 with 256 x 128, 54 with 256 x 256; T =
+  // 4096 75 and 67.
   auto per_cu = [&](int bm, int bn) {
     return (double)(((long)((p.rows + bm - 1) / bm) * ((p.T + bn - 1) / bn) + 255) / 256);
   };
   const double n0 = per_cu(32, 64), n1 = per_cu(64, 64), n2 = per_cu(128, 64);
   const double c[5] = {n0 <= 1 ? 0.21 : n0 <= 2 ? 0.29 : 0.13 * n0, n1 <= 1 ? 0.25 : 0.22 * n1,
-                       n2 <= 1 ? 0.41 : 0.36 * n2, 1.25 * per_cu(256, 128), 2.2 * per_cu(256, 256)};
+                       n2 <= 1 ? 0.41 : 0.36 * n2, 1.1 * per_cu(256, 128), 2.0 * per_cu(256, 256)};
   int best = 0;
   for (int i = 1; i < 5; i++)
     if (c[i] < c[best]) best = i;
@@ -338,9 +384,9 @@ hipError_t launch_linear_int8(const Int8Params& p0, hipStream_t s) {
 hipError_t launch_gate_up_int8(const Int8Params& p, hipStream_t s) {
   if (p.T < 1 || p.rows < 1 || p.cols < 16 || p.cols % 16 || p.cols > INT8_MAX_COLS) return hipErrorInvalidValue;
   // token tiles are grid rows
-  for (int t0 = 0; t0 < p.T; t0 += 1 << 20) {
+  for (long t0 = 0; t0 < p.T; t0 += 1 << 20) {
     Int8Params q = p;
-    q.T = p.T - t0 < (1 << 20) ? p.T - t0 : 1 << 20;
+    q.T = (int)(p.T - t0 < (1 << 20) ? p.T - t0 : 1 << 20);
     q.xq += (size_t)t0 * p.cols;
     q.xs += t0;
     q.y = (float*)p.y + (size_t)t0 * p.rows;
