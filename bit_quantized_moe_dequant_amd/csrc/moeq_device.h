@@ -27,8 +27,7 @@ enum {
   FMT_FP8_B128 = 5,
   FMT_MXFP8 = 6,
   FMT_FP8_B32 = 7,
-  FMT_MXFP8_TILED = 8,
-  FMT_INT8 = 9
+  FMT_MXFP8_TILED = 8
 };
 enum { ACT_BF16 = 0, ACT_F32 = 1 };
 
@@ -63,62 +62,6 @@ __device__ __forceinline__ float half_bits_f32(uint32_t h) {
 __device__ __forceinline__ uint32_t f32_bf16_rne(float f) {
   uint32_t u = __builtin_bit_cast(uint32_t, f);
   return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-}
-
-// The same for any input: NaNs stay NaN (quiet), infinities are kept.
-__device__ __forceinline__ uint32_t f32_bf16_rne_nan(float f) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, f);
-  return (u & 0x7FFFFFFFu) > 0x7F800000u ? ((u >> 16) | 0x40u) : f32_bf16_rne(f);
-}
-
-// Token scale of the int8 quantisation from the bits of the row's largest magnitude,
-// and the code of one value under it (IEEE divisions: the codes are defined by them).
-__device__ __forceinline__ float int8_scale(uint32_t amax_bits) {
-  return amax_bits >= 0x7F800000u ? u2f(0x7FC00000u) : u2f(amax_bits) / 127.0f;
-}
-__device__ __forceinline__ int int8_code(float v, float s) {
-  const float q = __builtin_fminf(__builtin_fmaxf(__builtin_rintf(v / s), -127.0f), 127.0f);
-  return s > 0.f ? (int)q : 0;
-}
-// N codes at a time, four to a word, r = 1 / s. The product v r is within 127.5 * 2^-23 of
-// fl(v / s), so its nearest integer is the code unless it lies that near a half: then (and
-// where r is not finite: s zero, NaN or tiny) the divisions are made. Adding 1.5 * 2^23
-// rounds to the nearest integer, ties to even, and leaves it in the low bits.
-template <int N>
-__device__ __forceinline__ void int8_codes(const float (&v)[N], float s, float r, uint32_t (&out)[N / 4]) {
-  constexpr float MAGIC = 12582912.0f;
-  float far = 0.f;
-#pragma unroll
-  for (int j = 0; j < N / 4; j++) {
-    uint32_t t[4];
-#pragma unroll
-    for (int k = 0; k < 4; k++) {
-      const float m = __builtin_fmaf(v[4 * j + k], r, MAGIC);
-      far = __builtin_fmaxf(far, __builtin_fabsf(__builtin_fmaf(v[4 * j + k], r, MAGIC - m)));
-      t[k] = f2u(m);
-    }
-    out[j] = __builtin_amdgcn_perm(t[1], t[0], 0x0C0C0400u) | __builtin_amdgcn_perm(t[3], t[2], 0x04000C0Cu);
-  }
-  if (!(far < 0.499976f) || !(r <= 3.402823466e38f)) {
-#pragma unroll
-    for (int j = 0; j < N / 4; j++) {
-      out[j] = 0;
-#pragma unroll
-      for (int k = 0; k < 4; k++) out[j] |= ((uint32_t)int8_code(v[4 * j + k], s) & 255u) << (8 * k);
-    }
-  }
-}
-
-// Largest of the lanes' values, by row shifts and row broadcasts (the result gathers in
-// lane 63): a tenth of the latency of six exchanges through LDS.
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false));  // row_shr:1
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false));  // row_shr:2
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false));  // row_shr:4
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false));  // row_shr:8
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));  // row_bcast:15 into rows 1, 3
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));  // row_bcast:31 into rows 2, 3
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
 // Split two fp32 values into hi and lo bf16 pairs with a + b ~ value to 16 bits.

@@ -39,6 +39,7 @@
 #include <hip/hip_runtime.h>
 
 #include "moeq_device.h"
+#include "moeq_int8.h"
 #include "moeq_kernels.h"
 
 namespace moeq {

@@ -3,10 +3,56 @@
 #pragma once
 #include "moeq_device.h"
 #include "moeq_kernels.h"
+#include "moeq_wave.h"
 
 namespace moeq {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+
+// fp32 -> bf16 bits, round to nearest even, for any input: NaNs stay NaN (quiet), infinities
+// are kept.
+__device__ __forceinline__ uint32_t f32_bf16_rne_nan(float f) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, f);
+  return (u & 0x7FFFFFFFu) > 0x7F800000u ? ((u >> 16) | 0x40u) : f32_bf16_rne(f);
+}
+
+// Token scale of the int8 quantisation from the bits of the row's largest magnitude,
+// and the code of one value under it (IEEE divisions: the codes are defined by them).
+__device__ __forceinline__ float int8_scale(uint32_t amax_bits) {
+  return amax_bits >= 0x7F800000u ? u2f(0x7FC00000u) : u2f(amax_bits) / 127.0f;
+}
+__device__ __forceinline__ int int8_code(float v, float s) {
+  const float q = __builtin_fminf(__builtin_fmaxf(__builtin_rintf(v / s), -127.0f), 127.0f);
+  return s > 0.f ? (int)q : 0;
+}
+// N codes at a time, four to a word, r = 1 / s. The product v r is within 127.5 * 2^-23 of
+// fl(v / s), so its nearest integer is the code unless it lies that near a half: then (and
+// where r is not finite: s zero, NaN or tiny) the divisions are made. Adding 1.5 * 2^23
+// rounds to the nearest integer, ties to even, and leaves it in the low bits.
+template <int N>
+__device__ __forceinline__ void int8_codes(const float (&v)[N], float s, float r, uint32_t (&out)[N / 4]) {
+  constexpr float MAGIC = 12582912.0f;
+  float far = 0.f;
+#pragma unroll
+  for (int j = 0; j < N / 4; j++) {
+    uint32_t t[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const float m = __builtin_fmaf(v[4 * j + k], r, MAGIC);
+      far = __builtin_fmaxf(far, __builtin_fabsf(__builtin_fmaf(v[4 * j + k], r, MAGIC - m)));
+      t[k] = f2u(m);
+    }
+    out[j] = __builtin_amdgcn_perm(t[1], t[0], 0x0C0C0400u) | __builtin_amdgcn_perm(t[3], t[2], 0x04000C0Cu);
+  }
+  if (!(far < 0.499976f) || !(r <= 3.402823466e38f)) {
+#pragma unroll
+    for (int j = 0; j < N / 4; j++) {
+      out[j] = 0;
+#pragma unroll
+      for (int k = 0; k < 4; k++) out[j] |= ((uint32_t)int8_code(v[4 * j + k], s) & 255u) << (8 * k);
+    }
+  }
+}
 
 // The bias and the added term of one output.
 __device__ __forceinline__ float finish(const Int8Params& P, size_t t, int r, float v) {

@@ -107,6 +107,8 @@ struct Mx8Params {
   int rows, cols, T;
 };
 
+enum { FMT_INT8 = 9 };  // beside the FMT_* of moeq_device.h
+
 // 8-bit integer linear of one expert tensor.
 constexpr int INT8_MAX_COLS = 65536;  // 2^14 per product: the int32 sum stays below 2^31
 struct Int8Params {

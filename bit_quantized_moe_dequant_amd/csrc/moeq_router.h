@@ -3,6 +3,7 @@
 #pragma once
 #include "moeq_device.h"
 #include "moeq_kernels.h"
+#include "moeq_wave.h"
 
 namespace moeq {
 
