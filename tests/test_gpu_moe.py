@@ -128,6 +128,52 @@ def test_layer(shape):
     assert mq.check_device_error(c.moe.workspace(T)) == 0
 
 
+def test_wide_hidden_size():
+    """A hidden size whose tokens' codes do not fit the first launch, off the FP4 kernels."""
+    say("moe wide")
+    for T in (1, 12):
+        c = Case(8192, 256, 6, 2, MX, MX, 64, seed=90 + T)
+        bits, xt = c.x(T, 91)
+        c.check(bits, xt, *mq.moe_forward(c.moe, xt))
+
+
+def test_a_token_that_is_not_finite_stays_alone():
+    say("moe nan")
+    c = Case(1024, 512, 16, 6, MX, MX, 512, seed=93)
+    for T in (4, 16):
+        _, xt = c.x(T, 94)
+        good = mq.moe_forward(c.moe, xt)
+        bad = xt.clone()
+        bad[2, 7] = float("nan")
+        y, ids, rw = mq.moe_forward(c.moe, bad)
+        rest = [t for t in range(T) if t != 2]
+        for a, b in zip((y, ids, rw), good):
+            assert torch.equal(a[rest], b[rest])
+        assert bool(y[2].isnan().all()) and ids[2].tolist() == list(range(6))
+
+
+def test_c_entry_without_routing_outputs_and_an_initialised_workspace():
+    """ids and rw may be NULL; the workspace only needs moeq_workspace_init."""
+    say("moe null outputs")
+    c = Case(512, 512, 12, 4, MX, MX, 256, seed=95)
+    lib = mq._lib()
+    for T in (1, 8, 20):
+        _, xt = c.x(T, 96 + T)
+        ref = mq.moe_forward(c.moe, xt)[0]
+        n = lib.moeq_moe_workspace_bytes(*c.moe._refs, T)
+        raw = torch.randint(0, 256, (n + 512,), dtype=torch.uint8, device="cuda")
+        off = (-raw.data_ptr()) % 256
+        ws = raw[off:off + n]
+        tail = raw[off + n:].clone()
+        stream = torch.cuda.current_stream().cuda_stream
+        assert lib.moeq_workspace_init(ws.data_ptr(), n, stream) == 0
+        y = torch.empty_like(ref)
+        for _ in range(2):
+            assert lib.moeq_moe_forward(*c.moe._refs, xt.data_ptr(), T, y.data_ptr(), None, None, ws.data_ptr(), n, stream) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(y, ref) and torch.equal(raw[off + n:], tail)
+
+
 def test_full_size():
     for T in (1, 3):
         say("moe full size", T)

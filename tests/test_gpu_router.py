@@ -101,6 +101,44 @@ def test_near_ties_are_decided_in_64_bits(T, kind):
     assert np.array_equal(ids.cpu().numpy()[clear], ref[0][clear])
 
 
+@pytest.mark.parametrize("T,H,E,K", [(65, 8, 5, 2), (100, 16, 3, 3), (66, 1032, 64, 1), (257, 2056, 513, 16), (90, 8200, 33, 6)])
+@pytest.mark.parametrize("kind", SCORES)
+def test_many_tokens_at_odd_sizes(T, H, E, K, kind):
+    """Beyond the one-launch form: rows shorter than a step, parts of the hidden size that
+    end inside one, rows longer than a lane's registers hold."""
+    say("many", T, H, E, K, kind)
+    x, w, b = make(T, H, E, T + H)
+    for bias in (b, None):
+        ids, rw = mq.router_topk(mq.Router(w, K, scoring=kind, bias=bias), x)
+        ref = route_ref(host(x), host(w), K, kind, False, 1.0, host(bias))
+        key = -np.sort(-ref[2], axis=1)[:, :K + 1]
+        assert np.abs(np.diff(key, axis=1)).min() > 1e-12
+        check(ids, rw, ref)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -100, 2.0 ** 60, 2.0 ** 100])
+@pytest.mark.parametrize("T", [4, 100])
+def test_magnitudes_beyond_fp32(T, scale):
+    """Logits whose products or sums leave fp32's range on either side: order by the fp64 logit."""
+    say("magnitudes", T, scale)
+    x, w, _ = make(T, 512, 40, 31)
+    x, w = (x.float() * scale).to(torch.bfloat16), (w.float() * scale).to(torch.bfloat16)
+    x[1] = 0
+    ids, _ = mq.router_topk(mq.Router(w, 5, scoring="softmax"), x)
+    z = x.double().cpu().numpy() @ w.double().cpu().numpy().T
+    assert np.array_equal(ids.cpu().numpy(), np.argsort(-z, axis=1, kind="stable")[:, :5])
+
+
+def test_one_workspace_for_several_sizes():
+    """A workspace for the most tokens serves fewer, one call after another."""
+    x, w, b = make(300, 256, 60, 8)
+    r = mq.Router(w, 4, scoring="sigmoid", bias=b)
+    ws = r.workspace(300)
+    for T in (300, 1, 64, 65, 9, 300):
+        ids, rw = mq.router_topk(r, x[:T], ws=ws)
+        check(ids, rw, route_ref(host(x[:T]), host(w), 4, "sigmoid", False, 1.0, host(b)))
+
+
 def test_exact_ties_take_the_lowest_id():
     say("ties")
     for T in (1, 150):
