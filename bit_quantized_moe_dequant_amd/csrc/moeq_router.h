@@ -221,6 +221,7 @@ __device__ __forceinline__ void router_few(const RouterParams& P, int block, int
   __syncthreads();
   if (is_last && wave < tn) {
     if (P.n_experts <= 256) choose<4, true>(P, t0 + wave, lane);
+    else if (P.n_experts <= 512) choose<8, true>(P, t0 + wave, lane);
     else choose<16, true>(P, t0 + wave, lane);
   }
 }

@@ -66,6 +66,7 @@ __global__ __launch_bounds__(256) void k_router_choose(RouterParams P) {
   const int t = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (t >= P.T) return;
   if (P.n_experts <= 256) choose<4, false>(P, t, lane);
+  else if (P.n_experts <= 512) choose<8, false>(P, t, lane);
   else choose<16, false>(P, t, lane);
 }
 
@@ -88,7 +89,10 @@ __global__ __launch_bounds__(256) void k_router_choose(RouterParams P) {
 // included); twice that is taken, with the rounding of the ROUTER_MM_Z stored parts, and
 // 2^-100 for products that underflow.
 //
-// Measured at 2048 tokens, 4096 x 256: 262 us with all logits in fp64.
+// Measured at 2048 tokens, 4096 x 256, 6 of them: 36.5 us (13 and 25) against 262 with all
+// logits in fp64; what bounds it is the vector unit's fp64 work and the chain of choices in
+// k_router_pick. Up to ROUTER_FEW_T tokens the one-launch form is faster (64 tokens 24.0
+// against 26.1 us; 128 tokens 38.0 against 26.7).
 constexpr int RM_FLUSH = 4;          // steps of 64 products
 constexpr int RM_E = 64, RM_T = 64;  // experts and tokens of a tile
 
@@ -420,6 +424,7 @@ hipError_t launch_router(const RouterParams& p, hipStream_t s) {
     const double unit = (2.0 * (16 + 4 * RM_FLUSH) + ROUTER_MM_Z) * 0x1p-23;
     const dim3 g((unsigned)((p.T + 3) / 4)), b(256);
     if (p.n_experts <= 256) hipLaunchKernelGGL(k_router_pick<4>, g, b, 0, s, p, z, unit);
+    else if (p.n_experts <= 512) hipLaunchKernelGGL(k_router_pick<8>, g, b, 0, s, p, z, unit);
     else hipLaunchKernelGGL(k_router_pick<16>, g, b, 0, s, p, z, unit);
     return hipGetLastError();
   }
