@@ -346,7 +346,11 @@ __global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_co
     const double v = logit(e);
     const double s = score(v);
     const uint64_t kv = order_of(P.bias ? s + (double)P.bias[e] : s);
+    int out = e;  // the one that is not among the K any more
+    double zo = v;
     if (kv > low || (kv == low && e < __builtin_amdgcn_readlane(id, worst))) {
+      out = __builtin_amdgcn_readlane(id, worst);
+      zo = read_lane(zk, worst);
       if (lane == worst) {
         id = e;
         zk = v;
@@ -354,6 +358,10 @@ __global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_co
         key = kv;
       }
     }
+    // for the normaliser: its approximate logit may be an overflow's infinity or NaN
+#pragma unroll
+    for (int i = 0; i < N; i++)
+      if (lane + 64 * i == out) z[i] = zo;
   }
 
   if (soft) {  // the normaliser over all experts: the chosen ones' logits exact, the others' not

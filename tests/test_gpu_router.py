@@ -129,6 +129,72 @@ def test_magnitudes_beyond_fp32(T, scale):
     assert np.array_equal(ids.cpu().numpy(), np.argsort(-z, axis=1, kind="stable")[:, :5])
 
 
+def wide(T, E, seed):
+    """Numbers of one magnitude in fp64 from factors at both ends of bf16's range: x near
+    2^126, w below 2^-126 (subnormal)."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((T, 256), generator=g).sign() * 2.0 ** torch.randint(120, 127, (T, 256), generator=g)
+    w = torch.randint(-127, 128, (E, 256), generator=g).double() * 2.0 ** -133
+    return x.to(torch.bfloat16).cuda(), w.float().to(torch.bfloat16).cuda()
+
+
+@pytest.mark.parametrize("T", [4, 100])
+def test_weights_below_the_normal_range(T):
+    say("subnormal", T)
+    x, w = wide(T, 40, 12)
+    assert bool((w != 0).any(dim=1).all()) and float(w.float().abs().max()) < 2.0 ** -126
+    for kind in SCORES:
+        ids, rw = mq.router_topk(mq.Router(w, 5, scoring=kind, normalize=True), x)
+        ref = route_ref(host(x), host(w), 5, kind, True, 1.0, None)
+        key = -np.sort(-ref[2], axis=1)[:, :6]
+        clear = (np.abs(np.diff(key, axis=1)) > 1e-12 * np.abs(key[:, :1])).all(axis=1)
+        assert clear.mean() > 0.5
+        assert np.array_equal(ids.cpu().numpy()[clear], ref[0][clear])
+
+
+@pytest.mark.parametrize("T", [4, 100])
+def test_softmax_over_logits_whose_sums_overflow_on_the_way(T):
+    """Exact logits of 0 and small numbers, of which some pass 2^128 in their partial sums:
+    the experts that are not chosen must not spoil the denominator."""
+    say("overflow on the way", T)
+    g = torch.Generator().manual_seed(5)
+    x = torch.zeros((T, 512))
+    x[:, :256] = 2.0 ** 70
+    x[:, 256:] = torch.randn((T, 256), generator=g) / 16
+    w = torch.randn((40, 512), generator=g)
+    w[:, :256] = 0
+    for e in (3, 17, 31):             # + and - 2^140, in halves and in turn
+        w[e] = 0
+        w[e, :128], w[e, 128:256] = 2.0 ** 70, -2.0 ** 70
+    w[22] = 0
+    w[22, 0:256:2], w[22, 1:256:2] = 2.0 ** 70, -2.0 ** 70
+    x, w = x.to(torch.bfloat16).cuda(), w.to(torch.bfloat16).cuda()
+    for K in (1, 5):
+        ids, rw = mq.router_topk(mq.Router(w, K, scoring="softmax"), x)
+        ref = route_ref(host(x), host(w), K, "softmax", False, 1.0, None)
+        assert np.isfinite(ref[1]).all() and np.array_equal(ids.cpu().numpy(), ref[0])
+        # the other denominators' terms: fp32 sums of at most 40 numbers below 4
+        assert np.all(np.abs(rw.cpu().numpy() - ref[1]) <= 2.0 ** -18 * ref[1])
+
+
+@pytest.mark.parametrize("T", [64, 100])
+def test_softmax_weights_beside_a_large_common_part(T):
+    """An activation outlier adds the same large number to every logit. Up to 64 tokens the
+    weights are fp64 throughout; beyond, logits that are not chosen enter the denominator
+    with the error of fp32 sums, at most 2^-16 |W_e| |x|."""
+    say("outlier", T)
+    x, w, _ = make(T, 1024, 96, 44)
+    x[:, 5], w[:, 5] = 512.0, 1.0
+    ids, rw = mq.router_topk(mq.Router(w, 6, scoring="softmax"), x)
+    X, W = host(x).astype(np.float64), host(w).astype(np.float64)
+    ref = route_ref(host(x), host(w), 6, "softmax", False, 1.0, None)
+    assert np.array_equal(ids.cpu().numpy(), ref[0])
+    d = 0.0 if T <= 64 else 2.0 ** -16 * np.linalg.norm(X, axis=1)[:, None] * np.linalg.norm(W, axis=1).max()
+    assert np.all(np.abs(rw.cpu().numpy() - ref[1]) <= (2.0 ** -23 + np.expm1(d)) * ref[1])
+    ids2, rw2 = mq.router_topk(mq.Router(w, 6, scoring="softmax", normalize=True), x)
+    check(ids2, rw2, route_ref(host(x), host(w), 6, "softmax", True, 1.0, None))  # no denominator: exact
+
+
 def test_one_workspace_for_several_sizes():
     """A workspace for the most tokens serves fewer, one call after another."""
     x, w, b = make(300, 256, 60, 8)
