@@ -398,7 +398,7 @@ int check_linear_int8(const moeq_weight* w, int expert, int T, const float* bias
   int rc = check_weight(w, false);
   if (rc) return rc;
   if (w->fmt != MOEQ_FMT_INT8) return MOEQ_E_FMT;
-  if (w->cols > INT8_MAX_COLS) return MOEQ_E_SHAPE;
+  if (w->cols > INT8_MAX_COLS || w->rows > INT8_MAX_ROWS) return MOEQ_E_SHAPE;
   if (expert < 0 || expert >= w->n_experts || T < 0 || !y) return MOEQ_E_INVAL;
   if (out_type != MOEQ_OUT_F32 && out_type != MOEQ_OUT_BF16) return MOEQ_E_INVAL;
   if (!aligned(y, out_type == MOEQ_OUT_BF16 ? 2 : 4) || (bias && !aligned(bias, 4))) return MOEQ_E_ALIGN;
@@ -504,7 +504,7 @@ int check_shared(const moeq_layer* L, const moeq_shared* S) {
   for (const moeq_weight* w : {&S->gate, &S->up, &S->down}) {
     if ((rc = check_weight(w, false))) return rc;
     if (w->fmt != MOEQ_FMT_INT8) return MOEQ_E_FMT;
-    if (w->cols > INT8_MAX_COLS) return MOEQ_E_SHAPE;
+    if (w->cols > INT8_MAX_COLS || w->rows > INT8_MAX_ROWS) return MOEQ_E_SHAPE;
   }
   for (const moeq_weight* w : {&S->gate, &S->up})
     if (w->rows != S->inter || w->cols != L->hidden) return MOEQ_E_SHAPE;

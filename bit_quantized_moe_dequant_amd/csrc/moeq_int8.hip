@@ -346,14 +346,13 @@ hipError_t few_x(const Int8Params& p0, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_linear_int8_few(const Int8Params& p, bool in_f32, hipStream_t s) {
-  if (!few_bf16_fits(p.T, p.cols) || p.rows < 1 || p.cols < 16 || p.cols % 16) return hipErrorInvalidValue;
+  if (!few_bf16_fits(p.T, p.cols) || p.rows < 1 || p.rows > INT8_MAX_ROWS || p.cols < 16 || p.cols % 16) return hipErrorInvalidValue;
   return in_f32 ? few_x<1, 1>(p, s) : few_x<1, 0>(p, s);
 }
 
-hipError_t launch_linear_int8(const Int8Params& p0, hipStream_t s) {
-  Int8Params p = p0;
+namespace {
+hipError_t linear_int8(Int8Params p, hipStream_t s) {
   p.vec4 = p.rows % 4 == 0 && (uintptr_t)p.y % (p.out_bf16 ? 8 : 16) == 0;
-  if (p.T < 1 || p.rows < 1 || p.cols < 16 || p.cols % 16 || p.cols > INT8_MAX_COLS) return hipErrorInvalidValue;
   if (p.T <= 16) return go_few<1, 1, 8>(p, s);
   if (p.T <= 32) return go_few<1, 2, 8>(p, s);
   // The tile with the smallest estimate. A step of 128 bytes of K takes a CU, by how many
@@ -379,6 +378,25 @@ hipError_t launch_linear_int8(const Int8Params& p0, hipStream_t s) {
     case 3: return go_tiled<4, 2, 2, 2, 3, 128, 1, 2>(p, s);
   }
   return go_tiled<2, 4, 4, 2, 2, 128, 1, 2>(p, s);
+}
+}  // namespace
+
+hipError_t launch_linear_int8(const Int8Params& p, hipStream_t s) {
+  if (p.T < 1 || p.rows < 1 || p.rows > INT8_MAX_ROWS || p.cols < 16 || p.cols % 16 || p.cols > INT8_MAX_COLS)
+    return hipErrorInvalidValue;
+  // a grid holds below 2^32 threads: 2^16 tokens at a time keep every tile's number of
+  // work-groups below that for up to INT8_MAX_ROWS rows
+  for (long t0 = 0; t0 < p.T; t0 += 1 << 16) {
+    Int8Params q = p;
+    q.T = (int)(p.T - t0 < (1 << 16) ? p.T - t0 : 1 << 16);
+    q.xq += (size_t)t0 * p.cols;
+    q.xs += t0;
+    q.y = (uint8_t*)p.y + (size_t)t0 * p.rows * (p.out_bf16 ? 2 : 4);
+    if (p.add) q.add = p.add + (size_t)t0 * p.rows;
+    const hipError_t e = linear_int8(q, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_gate_up_int8(const Int8Params& p, hipStream_t s) {

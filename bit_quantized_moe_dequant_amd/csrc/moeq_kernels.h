@@ -111,6 +111,7 @@ enum { FMT_INT8 = 9 };  // beside the FMT_* of moeq_device.h
 
 // 8-bit integer linear of one expert tensor.
 constexpr int INT8_MAX_COLS = 65536;  // 2^14 per product: the int32 sum stays below 2^31
+constexpr int INT8_MAX_ROWS = 1 << 23;
 struct Int8Params {
   const int8_t* w;    // [rows][cols], 16-byte aligned
   const float* ws;    // [rows]

@@ -298,7 +298,7 @@ int moeq_prefill_down(const moeq_layer* L, const uint8_t* hq, const uint8_t* hs,
                       int T, float* y, void* ws, size_t ws_bytes, void* stream);
 
 /* Dense block-quantized linear y[T][rows] = W_expert x[T][cols] (fp32 out). Any
- * format; FP8_B128 is the dense-layer format (IQ2_XXS + Q2_K + FP8 hybrid card).
+ * format but INT8 (moeq_linear_int8); FP8_B128 is the dense-layer format (IQ2_XXS + Q2_K + FP8 hybrid card).
  * MXFP8, MXFP8_TILED and FP8_B32 run on the block-scaled FP8 matrix instruction
  * for every T (the weights' e8m0 scale is the instruction's scale; x enters as
  * two E4M3 terms per value with e8m0 scales per 32, exact to 2^-21.8 of each
@@ -340,8 +340,8 @@ int moeq_quantize_int8_f32(const float* x, int T, int K, int8_t* q, float* scale
  * of an MOEQ_FMT_INT8 weight. The sum is exact (int32; cols at most 65536, any codes);
  * the scales and the bias are applied in fp32. xq i8 [T][cols], 16-byte aligned; xs
  * fp32 [T]; bias fp32 [rows] or NULL; y [T][rows] overwritten, fp32 (MOEQ_OUT_F32) or
- * bf16 rounded to nearest even (MOEQ_OUT_BF16), aligned to its element. Any T and
- * rows; T == 0 is a no-op. The same inputs give the same bits whatever the batch they
+ * bf16 rounded to nearest even (MOEQ_OUT_BF16), aligned to its element. Any T;
+ * rows up to 2^23 (MOEQ_E_SHAPE beyond); T == 0 is a no-op. The same inputs give the same bits whatever the batch they
  * are part of. */
 int moeq_linear_int8(const moeq_weight* w, int expert, const int8_t* xq, const float* xs, int T, const float* bias,
                      int out_type, void* y, void* stream);
@@ -387,7 +387,9 @@ typedef struct moeq_shared {
  * order of the logits), and their weights s * scale, or
  * s / (sum of the K) * scale. The logits W x are sums of exact products in fp64, and so
  * are scores and sums: the choice does not depend on an order of summation beyond
- * fp64's. x bf16 [T][H], 16-byte aligned; ids int32 [T][K] (always distinct and inside
+ * fp64's. (One exception, beyond 64 tokens, softmax with normalize 0 and no bias: the
+ * logits that were not chosen enter the softmax's denominator from fp32 sums, each
+ * within 2^-16 |W_e| |x| of the exact one and far nearer as a rule.) x bf16 [T][H], 16-byte aligned; ids int32 [T][K] (always distinct and inside
  * [0, E)) and rw fp32 [T][K] overwritten: what moeq_expert_forward takes. A sum of 0
  * gives weights 0. ws: moeq_router_workspace_bytes(R, T) bytes, 256-byte aligned,
  * zero-filled once before first use (or passed to moeq_workspace_init), not shared

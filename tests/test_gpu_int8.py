@@ -233,3 +233,19 @@ def test_no_tokens():
     assert mq.linear_int8_dynamic(w, x).shape == (0, 20)
     q, s = mq.quantize_int8(x)
     assert mq.linear_int8(w, q, s).shape == (0, 20)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_more_tokens_than_one_launch(bf16):
+    """Two launches of the product, the second a few tokens short of a tile."""
+    say("launches", bf16)
+    T, K, rows = (1 << 17) + 21, 32, 24
+    x = tokens(T, K, 61)
+    w, wq, ws = weight(rows, K, 62)
+    bias = torch.randn(rows, device="cuda")
+    dt = torch.bfloat16 if bf16 else torch.float32
+    y = mq.linear_int8_dynamic(w, x, bias=bias, out_dtype=dt)
+    q, s = quant_ref(x.float().cpu().numpy())
+    check(y, q, s, wq[0], ws[0], bias.cpu().numpy(), bf16)
+    y = mq.linear_int8_dynamic(w, x, out_dtype=dt)
+    check(y, q, s, wq[0], ws[0], None, bf16)

@@ -40,6 +40,7 @@ def test_linear_refusals():
     assert linear(fake(cols=40)) == -4
     assert linear(fake(cols=65552)) == -4
     assert linear(fake(rows=0)) == -4
+    assert linear(fake(rows=(1 << 23) + 1, cols=16)) == -4
     assert linear(fake(data=0x10008)) == -3
     assert linear(fake(scales=0x20002)) == -3
     assert linear(fake(n=2, stride=100)) == -1
