@@ -247,6 +247,9 @@ class Weight:
                           0 if self.scale2 is None else self.scale2.data_ptr(),
                           0 if self.grid is None else self.grid.data_ptr())
 
+    def __getstate__(self):  # copies and pickles make descriptors of their own
+        return {**self.__dict__, "_made": None, "_struct": None, "_by": None}
+
     def _ref(self):
         """byref of this weight's descriptor, made again when a field has changed."""
         now = (self.fmt, self.rows, self.cols, self.n_experts, self.data.data_ptr(), self.expert_stride,
@@ -658,7 +661,8 @@ class Router:
         self._ws = _Workspaces(lambda T: _lib().moeq_router_workspace_bytes(self._by, T))
 
     def workspace(self, T: int):
-        """An initialised workspace for T tokens; the current stream's own (kept per stream)."""
+        """An initialised workspace for T tokens or more; the current stream's own (kept per
+        stream, until a call there needs a larger one)."""
         return self._ws.get(T, self._keep[0].device, _stream_ptr().value or 0)
 
 
@@ -692,26 +696,30 @@ class MoeLayer:
         self._ws = _Workspaces(lambda T: _lib().moeq_moe_workspace_bytes(*self._refs, T))
 
     def workspace(self, T: int):
-        """An initialised workspace for T tokens; the current stream's own (kept per stream)."""
+        """An initialised workspace for T tokens or more; the current stream's own (kept per
+        stream, until a call there needs a larger one)."""
         return self._ws.get(T, self._device, _stream_ptr().value or 0)
 
 
 class _Workspaces:
-    """Initialised, 256-byte aligned workspaces, one per stream and number of tokens: calls
-    on different streams may overlap, and must not share one. A call under graph capture
-    gets one of its own that is not kept: the graph may be replayed beside anything, and
-    what capture records (the initialisation among it) has not run yet."""
+    """Initialised, 256-byte aligned workspaces, one per stream (calls on different streams
+    may overlap, and must not share one), replaced by a larger one when a call needs it: a
+    workspace for more tokens serves fewer. A call under graph capture gets one of its own
+    that is not kept: the graph may be replayed beside anything, and what capture records
+    (the initialisation among it) has not run yet."""
 
     def __init__(self, need):
-        self.need, self.kept = need, {}
+        self.need, self.bytes, self.kept = need, {}, {}
 
     def get(self, T, device, stream):
         if _torch().cuda.is_current_stream_capturing():
             return self._make(T, device)
-        key = (stream, T)
-        ws = self.kept.get(key)
-        if ws is None:
-            ws = self.kept[key] = self._make(T, device)
+        n = self.bytes.get(T)
+        if n is None:
+            n = self.bytes[T] = int(self.need(T))
+        ws = self.kept.get(stream)
+        if ws is None or n == 0 or ws.numel() < n:
+            ws = self.kept[stream] = self._make(T, device)
         return ws
 
     def _make(self, T, device):

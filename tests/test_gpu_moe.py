@@ -237,6 +237,24 @@ def test_graph(fg, fd, T):
     del graphs
 
 
+def test_one_workspace_per_stream():
+    """Calls of many sizes keep one workspace to a stream, that of the largest, and give what
+    they give with one of their own."""
+    c = Case(512, 512, 12, 4, MX, MX, 256, seed=80)
+    say("moe workspaces")
+    sizes = (1, 7, 200, 20, 2, 65, 130, 1, 200)
+    got = []
+    for T in sizes:
+        x = c.x(T, 500 + T)[1]
+        got.append((x, mq.moe_forward(c.moe, x), mq.router_topk(c.moe.router, x)))
+    assert len(c.moe._ws.kept) == 1 == len(c.moe.router._ws.kept)
+    for x, r, chosen in got:
+        fresh = mq.MoeLayer(c.moe.layer, c.moe.router, c.moe.shared)
+        for a, b in zip(r, mq.moe_forward(fresh, x)):
+            assert torch.equal(a, b)
+        assert torch.equal(chosen[0], r[1]) and torch.equal(chosen[1], r[2])
+
+
 def test_layer_then_linear():
     """As a decoder runs them: the attention output through an INT8 projection, then the layer."""
     c = Case(512, 512, 12, 4, MX, MX, 256, seed=77)

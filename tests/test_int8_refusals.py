@@ -88,6 +88,17 @@ def test_other_entry_points_refuse_the_format():
     assert lib.moeq_workspace_bytes(ctypes.byref(L), 1) == 0
 
 
+def test_copies_of_a_weight_have_descriptors_of_their_own():
+    import copy
+    import pickle
+    w = mq.Weight(9, 64, 32, 1, torch.zeros(64 * 32, dtype=torch.uint8), torch.zeros(256, dtype=torch.uint8))
+    w._ref()
+    for c in (copy.copy(w), copy.deepcopy(w), pickle.loads(pickle.dumps(w))):
+        c._ref()
+        assert c._struct is not w._struct and c._struct.data == c.data.data_ptr()
+    assert copy.deepcopy(w).data.data_ptr() != w.data.data_ptr()
+
+
 def test_binding_refusals():
     w = mq.Weight(9, 64, 32, 1, torch.zeros(64 * 32, dtype=torch.uint8), torch.zeros(256, dtype=torch.uint8))
     x = torch.zeros((3, 32), dtype=torch.bfloat16)
