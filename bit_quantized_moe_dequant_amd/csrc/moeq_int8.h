@@ -54,8 +54,10 @@ __device__ __forceinline__ void int8_codes(const float (&v)[N], float s, float r
   }
 }
 
-// The bias and the added term of one output.
+// The bias and the added term of one output; not fused with the product before, which other
+// forms of the store keep in memory in between: every form gives the same bits.
 __device__ __forceinline__ float finish(const Int8Params& P, size_t t, int r, float v) {
+#pragma clang fp contract(off)
   if (P.bias) v += P.bias[r];
   if (P.add) v += P.add[t * P.rows + r];
   return v;

@@ -205,8 +205,9 @@ __device__ __forceinline__ void store4(const Int8Params& P, int t, int r, float 
 }
 
 // ---------------------------------------------------------------- many tokens
-// RUNS: bf16 outputs without bias or added term, rows a multiple of 8, 16-byte aligned.
-template <int WM, int WN, int TM, int TN, int STAGES, int G_BK, int Q, int SPREAD, bool RUNS>
+// RUNS 1: bf16 outputs without bias or added term; 2: with; for both rows a multiple of 8
+// and everything 16-byte aligned. 0: any.
+template <int WM, int WN, int TM, int TN, int STAGES, int G_BK, int Q, int SPREAD, int RUNS>
 __global__ __launch_bounds__(64 * WM * WN) void k_int8_tiled(Int8Params P) {
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
   __shared__ __attribute__((aligned(16))) uint8_t lds[tiled_lds<WM, WN, TM, TN, STAGES, G_BK>()];
@@ -221,7 +222,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_tiled(Int8Params P) {
                                                                P.T - t0, K, K, lds, acc);
   const int wm = wave % WM, wn = wave / WM;
   const int n = lane & 31, g = lane >> 5;
-  if constexpr (RUNS) {
+  if constexpr (RUNS == 1) {
     // Through LDS, 32 tokens at a time and each wave for itself (past the last barrier nobody
     // reads operands any more), so that a store writes whole runs of channels: stored from
     // the registers, 8 bytes to a lane, a wave's store touches 32 rows (2048 x 4096 x 4096:
@@ -259,6 +260,58 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_tiled(Int8Params P) {
           *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(P.y) + (size_t)(tb + row) * P.rows + rb + c) = v;
       }
     }
+  } else if constexpr (RUNS == 2) {
+    // The same in fp32, 64 channels at a time, so that bias and added term are read in whole
+    // runs too (2048 x 4096 x 2048 with an added term: 56.7 us from the registers, 32 so).
+    constexpr int CB = (TM < 2 ? TM : 2) * 32, PITCH = 4 * CB + 16;
+    static_assert(WM * WN * 32 * PITCH <= sizeof(lds), "the outputs of 32 tokens fit");
+    uint8_t* mine = lds + wave * 32 * PITCH;
+#pragma unroll
+    for (int j = 0; j < TN; j++) {
+      const int tb = t0 + (wn * TN + j) * 32;
+      const float xs = P.xs[min(tb + n, P.T - 1)];
+#pragma unroll
+      for (int i0 = 0; i0 < TM; i0 += CB / 32) {
+        const int rb = r0 + (wm * TM + i0) * 32;
+#pragma unroll
+        for (int i = 0; i < CB / 32; i++)
+#pragma unroll
+          for (int q = 0; q < 4; q++) {
+            const int c = i * 32 + 8 * q + 4 * g;
+            u32x4 f;
+#pragma unroll
+            for (int e = 0; e < 4; e++) f[e] = f2u((float)acc[i0 + i][j][4 * q + e] * xs * P.ws[min(rb + c + e, P.rows - 1)]);
+            *reinterpret_cast<u32x4*>(mine + n * PITCH + 4 * c) = f;
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        constexpr int LPR = CB / 8;  // lanes to a row
+#pragma unroll
+        for (int k = 0; k < 32 * LPR / 64; k++) {
+          const int row = k * (64 / LPR) + lane / LPR, t = tb + row, r = rb + 8 * (lane % LPR);
+          const u32x4 v[2] = {*reinterpret_cast<const u32x4*>(mine + row * PITCH + 32 * (lane % LPR)),
+                              *reinterpret_cast<const u32x4*>(mine + row * PITCH + 32 * (lane % LPR) + 16)};
+          if (t < P.T && r < P.rows) {
+            uint32_t o[4];
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              float f[4];
+              u32x4 b = u32x4{0u, 0u, 0u, 0u}, a = b;
+              if (P.bias) b = ld16(P.bias + r + 4 * h);
+              if (P.add) a = ld16(P.add + (size_t)t * P.rows + r + 4 * h);
+#pragma unroll
+              for (int e = 0; e < 4; e++) {
+                f[e] = u2f(v[h][e]);
+                if (P.bias) f[e] += u2f(b[e]);
+                if (P.add) f[e] += u2f(a[e]);
+              }
+              o[2 * h] = f32_bf16_rne_nan(f[0]) | (f32_bf16_rne_nan(f[1]) << 16);
+              o[2 * h + 1] = f32_bf16_rne_nan(f[2]) | (f32_bf16_rne_nan(f[3]) << 16);
+            }
+            *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(P.y) + (size_t)t * P.rows + r) = u32x4{o[0], o[1], o[2], o[3]};
+          }
+        }
+      }
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < TN; j++) {
@@ -270,6 +323,42 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_tiled(Int8Params P) {
         for (int q = 0; q < 4; q++)  // four consecutive channels
           store4(P, t, r0 + (wm * TM + i) * 32 + 8 * q + 4 * g, xs, acc[i][j][4 * q], acc[i][j][4 * q + 1],
                  acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+    }
+  }
+}
+
+// A gate/up pair: h = silu(gate) * up, fp32, rows a multiple of 4, y 16-byte aligned. A wave
+// ends with the gate and the up sums of the same 32 channels.
+template <int WM, int WN, int TN, int STAGES, int G_BK, int Q, int SPREAD>
+__global__ __launch_bounds__(64 * WM * WN) void k_gu_int8_tiled(Int8Params P) {
+  constexpr int BM = WM * 32, BN = WN * TN * 32;  // channels, tokens
+  __shared__ __attribute__((aligned(16))) uint8_t lds[tiled_lds<WM, WN, 2, TN, STAGES, G_BK>()];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int K = P.cols;
+  int bm, bn;
+  tile_of(blockIdx.x, (P.rows + BM - 1) / BM, (P.T + BN - 1) / BN, bm, bn);
+  const int r0 = bm * BM, t0 = bn * BN;
+  i32x16 acc[2][TN];
+  tiled_product<MmaI8, WM, WN, 2, TN, STAGES, G_BK, Q, SPREAD, Nothing, true>(
+      P.w + (size_t)r0 * K, P.rows - r0, P.xq + (size_t)t0 * K, P.T - t0, K, K, lds, acc, {}, P.w2 + (size_t)r0 * K);
+  const int wm = wave % WM, wn = wave / WM;
+  const int n = lane & 31, g = lane >> 5;
+#pragma unroll
+  for (int j = 0; j < TN; j++) {
+    const int t = t0 + (wn * TN + j) * 32 + n;
+    const float xs = P.xs[min(t, P.T - 1)];
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+      const int r = r0 + wm * 32 + 8 * q + 4 * g;
+      if (t < P.T && r < P.rows) {
+        u32x4 f;
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+          f[e] = f2u(silu_mul((float)acc[0][j][4 * q + e] * xs * P.ws[r + e], (float)acc[1][j][4 * q + e] * xs * P.ws2[r + e]));
+        *reinterpret_cast<u32x4*>(reinterpret_cast<float*>(P.y) + (size_t)t * P.rows + r) = f;
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 }
@@ -286,10 +375,22 @@ hipError_t go_tiled(const Int8Params& p, hipStream_t s) {
   const long blocks = (long)((p.rows + BM - 1) / BM) * ((p.T + BN - 1) / BN);
   if (blocks > 0x7FFFFF) return hipErrorInvalidValue;
   const dim3 g((unsigned)blocks), b(64 * WM * WN);
-  if (p.out_bf16 && p.rows % 8 == 0 && (uintptr_t)p.y % 16 == 0 && !p.bias && !p.add)
-    hipLaunchKernelGGL((k_int8_tiled<WM, WN, TM, TN, STAGES, BK, Q, SPREAD, true>), g, b, 0, s, p);
+  const bool runs = p.out_bf16 && p.rows % 8 == 0 && ((uintptr_t)p.y | (uintptr_t)p.bias | (uintptr_t)p.add) % 16 == 0;
+  if (runs && !p.bias && !p.add)
+    hipLaunchKernelGGL((k_int8_tiled<WM, WN, TM, TN, STAGES, BK, Q, SPREAD, 1>), g, b, 0, s, p);
+  else if (runs)
+    hipLaunchKernelGGL((k_int8_tiled<WM, WN, TM, TN, STAGES, BK, Q, SPREAD, 2>), g, b, 0, s, p);
   else
-    hipLaunchKernelGGL((k_int8_tiled<WM, WN, TM, TN, STAGES, BK, Q, SPREAD, false>), g, b, 0, s, p);
+    hipLaunchKernelGGL((k_int8_tiled<WM, WN, TM, TN, STAGES, BK, Q, SPREAD, 0>), g, b, 0, s, p);
+  return hipGetLastError();
+}
+
+template <int WM, int WN, int TN, int STAGES, int BK, int Q, int SPREAD>
+hipError_t go_gu_tiled(const Int8Params& p, hipStream_t s) {
+  constexpr int BM = WM * 32, BN = WN * TN * 32;
+  const long blocks = (long)((p.rows + BM - 1) / BM) * ((p.T + BN - 1) / BN);
+  if (blocks > 0x7FFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((k_gu_int8_tiled<WM, WN, TN, STAGES, BK, Q, SPREAD>), dim3((unsigned)blocks), dim3(64 * WM * WN), 0, s, p);
   return hipGetLastError();
 }
 
@@ -399,16 +500,44 @@ hipError_t launch_linear_int8(const Int8Params& p, hipStream_t s) {
   return hipSuccess;
 }
 
+namespace {
+hipError_t gate_up_int8(const Int8Params& p, hipStream_t s) {
+  if (p.T <= 16) return go_few<2, 1, 4>(p, s);
+  if (p.T <= 32) return go_few<2, 2, 4>(p, s);
+  auto per_cu = [&](int bm, int bn) {
+    return (double)(((long)((p.rows + bm - 1) / bm) * ((p.T + bn - 1) / bn) + 255) / 256);
+  };
+  // The tile (channels x tokens) with the smallest estimate, as in linear_int8: a step of 128
+  // bytes takes a CU that holds n work-groups 0.23 + 0.22 n us with 32 x 64, 0.35 + 0.34 n
+  // with 64 x 64, 0.93 n with 128 x 64 and 1.2 n with 128 x 128. At 2 x 2048 x 4096 (us), with
+  // go_few's tile of 16 x 64 first: T = 64 16.0, 14.7, 21.5, 29.4, 31.7; T = 256 29.6, 14.5,
+  // 22.5, 28.5, 34.2; T = 1024 108, 36.0, 32.9, 29.8, 35.1; T = 2048 216, 63.8, 54.8, 53.6,
+  // 39.8. T = 32: 11.8 with go_few's tile of 16 x 32, 14.2 with 32 x 64.
+  const double c[4] = {0.23 + 0.22 * per_cu(32, 64), 0.35 + 0.34 * per_cu(64, 64), 0.93 * per_cu(128, 64),
+                       1.2 * per_cu(128, 128)};
+  int best = 0;
+  for (int i = 1; i < 4; i++)
+    if (c[i] < c[best]) best = i;
+  switch (best) {
+    case 0: return go_gu_tiled<1, 2, 1, 4, 128, 4, 1>(p, s);
+    case 1: return go_gu_tiled<2, 2, 1, 3, 128, 4, 1>(p, s);
+    case 2: return go_gu_tiled<4, 2, 1, 3, 128, 4, 1>(p, s);
+  }
+  return go_gu_tiled<4, 2, 2, 3, 128, 1, 2>(p, s);
+}
+}  // namespace
+
 hipError_t launch_gate_up_int8(const Int8Params& p, hipStream_t s) {
-  if (p.T < 1 || p.rows < 1 || p.cols < 16 || p.cols % 16 || p.cols > INT8_MAX_COLS) return hipErrorInvalidValue;
-  // token tiles are grid rows
-  for (long t0 = 0; t0 < p.T; t0 += 1 << 20) {
+  if (p.T < 1 || p.rows < 1 || p.rows > INT8_MAX_ROWS || p.cols < 16 || p.cols % 16 || p.cols > INT8_MAX_COLS ||
+      p.rows % 4 || (uintptr_t)p.y % 16)
+    return hipErrorInvalidValue;
+  for (long t0 = 0; t0 < p.T; t0 += 1 << 16) {  // as launch_linear_int8
     Int8Params q = p;
-    q.T = (int)(p.T - t0 < (1 << 20) ? p.T - t0 : 1 << 20);
+    q.T = (int)(p.T - t0 < (1 << 16) ? p.T - t0 : 1 << 16);
     q.xq += (size_t)t0 * p.cols;
     q.xs += t0;
     q.y = (float*)p.y + (size_t)t0 * p.rows;
-    const hipError_t e = q.T <= 16 ? go_few<2, 1, 4>(q, s) : go_few<2, 4, 2>(q, s);
+    const hipError_t e = gate_up_int8(q, s);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

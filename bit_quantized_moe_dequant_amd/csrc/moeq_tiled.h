@@ -83,12 +83,18 @@ constexpr int tiled_lds() {
 }
 
 // after(s) is called behind step s's products and may change acc.
+// PAIR (TM = 2): two first operands at once, whose rows take turns in blocks of 32:
+// acc[0] holds the sums of wbase's rows, acc[1] those of w2base's at the same place; wrows
+// counts the rows of one, of which a tile takes BM / 2.
 struct Nothing {
   __device__ __forceinline__ void operator()(int) const {}
 };
-template <class M, int WM, int WN, int TM, int TN, int STAGES, int G_BK, int Q, int SPREAD, class After = Nothing>
+template <class M, int WM, int WN, int TM, int TN, int STAGES, int G_BK, int Q, int SPREAD, class After = Nothing,
+          bool PAIR = false>
 __device__ __forceinline__ void tiled_product(const int8_t* wbase, int wrows, const int8_t* xbase, int xrows, int pitch,
-                                              int K, uint8_t* lds, typename M::Acc (&acc)[TM][TN], After after = {}) {
+                                              int K, uint8_t* lds, typename M::Acc (&acc)[TM][TN], After after = {},
+                                              const int8_t* w2base = nullptr) {
+  static_assert(!PAIR || TM == 2, "a wave holds a block of each");
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32, WAVES = WM * WN;
   constexpr int ROWS = BM + BN;                 // rows of one buffer: channels, then tokens
   constexpr int CPR = G_BK / 16, RPC = 64 / CPR;  // chunks of a row, rows of a copy
@@ -106,8 +112,10 @@ __device__ __forceinline__ void tiled_product(const int8_t* wbase, int wrows, co
 #pragma unroll
   for (int j = 0; j < WL; j++) {
     const int row = wrow + RPC * j + lane / CPR;
-    off[j] = min(row, wrows - 1) * pitch + c16(row);
+    off[j] = min(PAIR ? (row >> 6) * 32 + (row & 31) : row, wrows - 1) * pitch + c16(row);
   }
+  // a copy's rows lie in one block of 32
+  auto base = [&](int j) { return j >= WL ? xbase : PAIR && ((wrow + RPC * j) & 32) ? w2base : wbase; };
 #pragma unroll
   for (int j = 0; j < XL; j++) {
     const int row = xrow + RPC * j + lane / CPR;
@@ -119,7 +127,7 @@ __device__ __forceinline__ void tiled_product(const int8_t* wbase, int wrows, co
   auto copy = [&](int s, int at, int part) {
 #pragma unroll
     for (int j = part * LOADS / SPREAD; j < (part + 1) * LOADS / SPREAD; j++)
-      copy16(j < WL ? wbase : xbase, off[j], s * G_BK, lds + at + (j < WL ? wrow + RPC * j : BM + xrow + RPC * (j - WL)) * G_BK);
+      copy16(base(j), off[j], s * G_BK, lds + at + (j < WL ? wrow + RPC * j : BM + xrow + RPC * (j - WL)) * G_BK);
   };
   // any step, none past the end; in the last, partial one chunks past K are zeros
   auto copy_any = [&](int s, int at, int part) {
@@ -130,7 +138,7 @@ __device__ __forceinline__ void tiled_product(const int8_t* wbase, int wrows, co
       for (int j = part * LOADS / SPREAD; j < (part + 1) * LOADS / SPREAD; j++) {
         const int row = j < WL ? wrow + RPC * j : xrow + RPC * (j - WL);
         u32x4 v = u32x4{0u, 0u, 0u, 0u};
-        if (s * G_BK + c16(row + lane / CPR) < K) v = ld16((j < WL ? wbase : xbase) + off[j] + (size_t)s * G_BK);
+        if (s * G_BK + c16(row + lane / CPR) < K) v = ld16(base(j) + off[j] + (size_t)s * G_BK);
         *reinterpret_cast<u32x4*>(lds + at + (j < WL ? row : BM + row) * G_BK + 16 * lane) = v;
       }
     }

@@ -249,3 +249,24 @@ def test_more_tokens_than_one_launch(bf16):
     check(y, q, s, wq[0], ws[0], bias.cpu().numpy(), bf16)
     y = mq.linear_int8_dynamic(w, x, out_dtype=dt)
     check(y, q, s, wq[0], ws[0], None, bf16)
+
+
+@pytest.mark.parametrize("T,rows,cols", [(40, 72, 144), (300, 520, 144), (1100, 2056, 272), (2050, 4096, 144), (8187, 8192, 144)])
+def test_bias_at_every_tile(T, rows, cols):
+    """bf16 outputs with a bias are the fp32 outputs without one, plus it, rounded once more;
+    the bits do not depend on the batch."""
+    say("bias", T, rows, cols)
+    x = tokens(T, cols, 71)
+    w, _, _ = weight(rows, cols, 72)
+    bias = 40.0 * torch.randn(rows, device="cuda")
+    plain = mq.linear_int8_dynamic(w, x, out_dtype=torch.float32)
+    with_bias = mq.linear_int8_dynamic(w, x, bias=bias, out_dtype=torch.float32)
+    assert torch.equal(with_bias, plain + bias)
+    y = mq.linear_int8_dynamic(w, x, bias=bias)
+    assert torch.equal(y, (plain + bias).to(torch.bfloat16))
+    assert torch.equal(mq.linear_int8_dynamic(w, x, bias=bias[:]), y)
+    odd = torch.empty(rows + 1, device="cuda")[1:]  # not 16-byte aligned
+    odd.copy_(bias)
+    assert torch.equal(mq.linear_int8_dynamic(w, x, bias=odd), y)
+    for t, n in ((0, 1), (3, 16), (T - 33, 33)):
+        assert torch.equal(mq.linear_int8_dynamic(w, x[t:t + n], bias=bias), y[t:t + n])

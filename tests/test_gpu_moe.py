@@ -237,6 +237,26 @@ def test_graph(fg, fd, T):
     del graphs
 
 
+@pytest.mark.parametrize("T,shared", [(24, 272), (40, 272), (300, 2064), (1100, 2064), (2060, 2064)])
+def test_shared_expert_of_many_tokens(T, shared):
+    """Every tile of the shared expert's products, with channels and tokens past its end; the
+    shared part alone is the same for a token on its own."""
+    say("moe many", T, shared)
+    c = Case(256, 256, 12, 4, MX, MX, shared, seed=90)
+    bits, xt = c.x(T, 600)
+    y, ids, rw = mq.moe_forward(c.moe, xt)
+    c.check(bits, xt, y, ids, rw)
+    routed = mq.expert_forward(c.layer, xt, ids, rw)
+    assert bool(routed.isfinite().all())
+    # the routed experts' scales to 2^-127: nothing beside the shared part, which has the same
+    # bits in every form
+    c.layer.down.scales.zero_()
+    y = mq.moe_forward(c.moe, xt)[0]
+    for t in (0, T // 2, T - 1):
+        one = mq.moe_forward(c.moe, xt[t:t + 1])[0].float()
+        assert bool(((y[t:t + 1].float() - one).abs() <= 1e-30).all())
+
+
 def test_one_workspace_per_stream():
     """Calls of many sizes keep one workspace to a stream, that of the largest, and give what
     they give with one of their own."""
