@@ -205,8 +205,8 @@ __device__ __forceinline__ void store4(const Int8Params& P, int t, int r, float 
 }
 
 // ---------------------------------------------------------------- many tokens
-// RUNS 1: bf16 outputs without bias or added term; 2: with; for both rows a multiple of 8
-// and everything 16-byte aligned. 0: any.
+// RUNS 1: bf16 outputs without bias or added term; 2: the others; for both rows a multiple
+// of 8 and everything 16-byte aligned. 0: any.
 template <int WM, int WN, int TM, int TN, int STAGES, int G_BK, int Q, int SPREAD, int RUNS>
 __global__ __launch_bounds__(64 * WM * WN) void k_int8_tiled(Int8Params P) {
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
@@ -262,7 +262,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_tiled(Int8Params P) {
     }
   } else if constexpr (RUNS == 2) {
     // The same in fp32, 64 channels at a time, so that bias and added term are read in whole
-    // runs too (2048 x 4096 x 2048 with an added term: 56.7 us from the registers, 32 so).
+    // runs too (2048 x 4096 x 2048 with an added term: 56.7 us from the registers, 35 so; fp32
+    // outputs of 2048 x 4096 x 4096 48 and 43, of 8192^3 534 and 505).
     constexpr int CB = (TM < 2 ? TM : 2) * 32, PITCH = 4 * CB + 16;
     static_assert(WM * WN * 32 * PITCH <= sizeof(lds), "the outputs of 32 tokens fit");
     uint8_t* mine = lds + wave * 32 * PITCH;
@@ -291,23 +292,28 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_tiled(Int8Params P) {
           const u32x4 v[2] = {*reinterpret_cast<const u32x4*>(mine + row * PITCH + 32 * (lane % LPR)),
                               *reinterpret_cast<const u32x4*>(mine + row * PITCH + 32 * (lane % LPR) + 16)};
           if (t < P.T && r < P.rows) {
-            uint32_t o[4];
+            u32x4 o[2];
 #pragma unroll
             for (int h = 0; h < 2; h++) {
-              float f[4];
               u32x4 b = u32x4{0u, 0u, 0u, 0u}, a = b;
               if (P.bias) b = ld16(P.bias + r + 4 * h);
               if (P.add) a = ld16(P.add + (size_t)t * P.rows + r + 4 * h);
 #pragma unroll
               for (int e = 0; e < 4; e++) {
-                f[e] = u2f(v[h][e]);
-                if (P.bias) f[e] += u2f(b[e]);
-                if (P.add) f[e] += u2f(a[e]);
+                float f = u2f(v[h][e]);
+                if (P.bias) f += u2f(b[e]);
+                if (P.add) f += u2f(a[e]);
+                o[h][e] = P.out_bf16 ? f32_bf16_rne_nan(f) : f2u(f);
               }
-              o[2 * h] = f32_bf16_rne_nan(f[0]) | (f32_bf16_rne_nan(f[1]) << 16);
-              o[2 * h + 1] = f32_bf16_rne_nan(f[2]) | (f32_bf16_rne_nan(f[3]) << 16);
             }
-            *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(P.y) + (size_t)t * P.rows + r) = u32x4{o[0], o[1], o[2], o[3]};
+            const size_t at = (size_t)t * P.rows + r;
+            if (P.out_bf16) {
+              *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(P.y) + at) =
+                  u32x4{o[0][0] | (o[0][1] << 16), o[0][2] | (o[0][3] << 16), o[1][0] | (o[1][1] << 16), o[1][2] | (o[1][3] << 16)};
+            } else {
+              *reinterpret_cast<u32x4*>(reinterpret_cast<float*>(P.y) + at) = o[0];
+              *reinterpret_cast<u32x4*>(reinterpret_cast<float*>(P.y) + at + 4) = o[1];
+            }
           }
         }
       }
@@ -375,8 +381,8 @@ hipError_t go_tiled(const Int8Params& p, hipStream_t s) {
   const long blocks = (long)((p.rows + BM - 1) / BM) * ((p.T + BN - 1) / BN);
   if (blocks > 0x7FFFFF) return hipErrorInvalidValue;
   const dim3 g((unsigned)blocks), b(64 * WM * WN);
-  const bool runs = p.out_bf16 && p.rows % 8 == 0 && ((uintptr_t)p.y | (uintptr_t)p.bias | (uintptr_t)p.add) % 16 == 0;
-  if (runs && !p.bias && !p.add)
+  const bool runs = p.rows % 8 == 0 && ((uintptr_t)p.y | (uintptr_t)p.bias | (uintptr_t)p.add) % 16 == 0;
+  if (runs && p.out_bf16 && !p.bias && !p.add)
     hipLaunchKernelGGL((k_int8_tiled<WM, WN, TM, TN, STAGES, BK, Q, SPREAD, 1>), g, b, 0, s, p);
   else if (runs)
     hipLaunchKernelGGL((k_int8_tiled<WM, WN, TM, TN, STAGES, BK, Q, SPREAD, 2>), g, b, 0, s, p);
