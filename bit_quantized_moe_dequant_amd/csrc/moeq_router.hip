@@ -5,7 +5,7 @@
 //   ids  = the top_k largest s + bias (fp64), ties to the lowest id
 //   w    = s[ids] (/ their sum) * scale
 //
-// Everything up to the weights is held in fp64. The choice of experts is discontinuous:
+// Everything up to the weights is held in fp64 (but for one denominator: k_router_pick). The choice of experts is discontinuous:
 // fp32 logits carry an error of about 1e-6 that depends on the order of summation, so
 // two correct fp32 routers disagree on a near tie and a token's output jumps. A product
 // of two bf16 values is exact in fp64 and the vector unit issues fp64 FMAs at the fp32
@@ -364,7 +364,10 @@ __global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_co
       if (lane + 64 * i == out) z[i] = zo;
   }
 
-  if (soft) {  // the normaliser over all experts: the chosen ones' logits exact, the others' not
+  // The normaliser over all experts: the chosen ones' logits exact, the others' from fp32 sums
+  // (within the bound above; it cancels where the K are normalised). All of them exact would
+  // take the 262 us of the fp64 form.
+  if (soft) {
     double top = mine ? zk : -__builtin_inf(), sum = mine ? 1.0 : 0.0;
 #pragma unroll
     for (int i = 0; i < N; i++) top = z[i] > top ? z[i] : top;
