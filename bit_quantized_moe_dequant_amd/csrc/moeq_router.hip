@@ -5,11 +5,11 @@
 //   ids  = the top_k largest s + bias (fp64), ties to the lowest id
 //   w    = s[ids] (/ their sum) * scale
 //
-// Everything up to the weights is held in fp64 (but for one denominator: k_router_pick). The choice of experts is discontinuous:
-// fp32 logits carry an error of about 1e-6 that depends on the order of summation, so
-// two correct fp32 routers disagree on a near tie and a token's output jumps. A product
-// of two bf16 values is exact in fp64 and the vector unit issues fp64 FMAs at the fp32
-// rate here, so the exactness costs the conversions only.
+// Everything up to the weights is held in fp64 (but for one denominator: k_router_pick).
+// The choice of experts is discontinuous: fp32 logits carry an error of about 1e-6 that
+// depends on the order of summation, so two correct fp32 routers disagree on a near tie
+// and a token's output jumps. A product of two bf16 values is exact in fp64 and the vector
+// unit issues fp64 FMAs at the fp32 rate here, so the exactness costs the conversions only.
 #include "moeq_router.h"
 #include "moeq_tiled.h"
 
