@@ -368,7 +368,14 @@ __global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_co
   // (within the bound above; it cancels where the K are normalised). All of them exact would
   // take the 262 us of the fp64 form.
   if (soft) {
-    double top = mine ? zk : -__builtin_inf(), sum = mine ? 1.0 : 0.0;
+    // the chosen ones' approximate logits leave first: they may be an overflow's infinity too
+    for (int k = 0; k < K; k++) {
+      const int e = __builtin_amdgcn_readlane(id, k);
+#pragma unroll
+      for (int i = 0; i < N; i++)
+        if (lane + 64 * i == e) z[i] = -__builtin_inf();
+    }
+    double top = mine ? zk : -__builtin_inf();
 #pragma unroll
     for (int i = 0; i < N; i++) top = z[i] > top ? z[i] : top;
 #pragma unroll
@@ -377,13 +384,7 @@ __global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_co
       top = v > top ? v : top;
     }
     sk = exp(zk - top);
-    if (mine) sum = sk;
-    for (int k = 0; k < K; k++) {
-      const int e = __builtin_amdgcn_readlane(id, k);
-#pragma unroll
-      for (int i = 0; i < N; i++)
-        if (lane + 64 * i == e) z[i] = -__builtin_inf();
-    }
+    double sum = mine ? sk : 0.0;
 #pragma unroll
     for (int i = 0; i < N; i++) sum += lane + 64 * i < E ? exp(z[i] - top) : 0.0;
     sk /= wave_sum(sum);
