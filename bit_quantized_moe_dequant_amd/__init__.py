@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import threading
 
 import numpy as np
 
@@ -706,12 +707,21 @@ class _Workspaces:
     may overlap, and must not share one), replaced by a larger one when a call needs it: a
     workspace for more tokens serves fewer. A call under graph capture gets one of its own
     that is not kept: the graph may be replayed beside anything, and what capture records
-    (the initialisation among it) has not run yet."""
+    (the initialisation among it) has not run yet.
+
+    Host threads on one stream share its workspace, and ctypes lets another thread run while
+    the library queues a call's launches: whoever calls holds `lock` from the choice of the
+    workspace until all launches are queued, so that no other call's come between them."""
 
     def __init__(self, need):
         self.need, self.bytes, self.kept = need, {}, {}
+        self.lock = threading.RLock()
 
     def get(self, T, device, stream):
+        with self.lock:
+            return self._get(T, device, stream)
+
+    def _get(self, T, device, stream):
         if _torch().cuda.is_current_stream_capturing():
             return self._make(T, device)
         n = self.bytes.get(T)
@@ -748,12 +758,14 @@ def router_topk(router: Router, x, ids=None, rw=None, ws=None):
     if T == 0:
         return ids, rw
     stream = gpu[1](dev)
-    if ws is None:
-        ws = router._ws.get(T, x.device, stream)
-    n = ws.numel()
-    _need("ws", ws, gpu[6], (n,))
-    _check("moeq_router_topk", (_LIB or _lib()).moeq_router_topk(
-        router._by, x.data_ptr(), T, ids.data_ptr(), rw.data_ptr(), ws.data_ptr(), n, stream))
+    with router._ws.lock:
+        if ws is None:
+            ws = router._ws.get(T, x.device, stream)
+        n = ws.numel()
+        _need("ws", ws, gpu[6], (n,))
+        rc = (_LIB or _lib()).moeq_router_topk(
+            router._by, x.data_ptr(), T, ids.data_ptr(), rw.data_ptr(), ws.data_ptr(), n, stream)
+    _check("moeq_router_topk", rc)
     return ids, rw
 
 
@@ -775,12 +787,14 @@ def moe_forward(moe: MoeLayer, x, y=None, ids=None, rw=None, ws=None):
     if T == 0:
         return y, ids, rw
     stream = gpu[1](dev)
-    if ws is None:
-        ws = moe._ws.get(T, x.device, stream)
-    n = ws.numel()
-    _need("ws", ws, gpu[6], (n,))
-    _check("moeq_moe_forward", (_LIB or _lib()).moeq_moe_forward(
-        *moe._refs, x.data_ptr(), T, y.data_ptr(), ids.data_ptr(), rw.data_ptr(), ws.data_ptr(), n, stream))
+    with moe._ws.lock:
+        if ws is None:
+            ws = moe._ws.get(T, x.device, stream)
+        n = ws.numel()
+        _need("ws", ws, gpu[6], (n,))
+        rc = (_LIB or _lib()).moeq_moe_forward(
+            *moe._refs, x.data_ptr(), T, y.data_ptr(), ids.data_ptr(), rw.data_ptr(), ws.data_ptr(), n, stream)
+    _check("moeq_moe_forward", rc)
     return y, ids, rw
 
 
