@@ -664,7 +664,8 @@ class Router:
     def workspace(self, T: int):
         """An initialised workspace for T tokens or more; the current stream's own (kept per
         stream, until a call there needs a larger one)."""
-        return self._ws.get(T, self._keep[0].device, _stream_ptr().value or 0)
+        dev = _on_device(self._keep[0])
+        return self._ws.get(T, self._keep[0].device, _gpu()[1](dev))
 
 
 class SharedExpert:
@@ -699,7 +700,8 @@ class MoeLayer:
     def workspace(self, T: int):
         """An initialised workspace for T tokens or more; the current stream's own (kept per
         stream, until a call there needs a larger one)."""
-        return self._ws.get(T, self._device, _stream_ptr().value or 0)
+        dev = _on_device(self._keep[0])
+        return self._ws.get(T, self._device, _gpu()[1](dev))
 
 
 class _Workspaces:

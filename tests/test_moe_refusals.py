@@ -96,3 +96,16 @@ def test_binding_refusals():
             bad()
     with pytest.raises(ValueError, match="GPU"):
         mq.router_topk(r, x)
+
+
+def test_workspaces_of_another_device_are_refused(monkeypatch):
+    """workspace() belongs to the current device's stream; weights elsewhere (here: not on a GPU)
+    are refused before anything is made there."""
+    monkeypatch.setattr(mq, "_stream_ptr", lambda: ctypes.c_void_p(0))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    router = mq.Router(torch.zeros((8, 64), dtype=torch.bfloat16), 2)
+    w = lambda: mq.Weight(1, 64, 64, 8, torch.zeros(16, dtype=torch.uint8), torch.zeros(16, dtype=torch.uint8), None, None, 2048, 128)
+    moe = mq.MoeLayer(mq.Layer(64, 64, 8, 2, w(), w(), w()), router)
+    for what in (router, moe):
+        with pytest.raises(ValueError, match="GPU"):
+            what.workspace(3)
