@@ -11,6 +11,7 @@
 // and a token's output jumps. A product of two bf16 values is exact in fp64 and the vector
 // unit issues fp64 FMAs at the fp32 rate here, so the exactness costs the conversions only.
 #include "moeq_router.h"
+#include "moeq_router_bound.h"
 #include "moeq_tiled.h"
 
 namespace moeq {
@@ -82,18 +83,12 @@ __global__ __launch_bounds__(256) void k_router_choose(RouterParams P) {
 //      K-th exact key, the one with the largest bound does too. What is left cannot be
 //      chosen.
 //
-// The bound: an fp32 sum of products p_1 .. p_n in any order errs by at most (additions a
-// term passes through) u sum |p_i|, and sum |p_i| <= |W_e| |x_t| (Cauchy-Schwarz). Between
-// two flushes a sum passes RM_FLUSH * 4 instructions, each adding 16 products in an order
-// that is not documented: at most 16 + 4 RM_FLUSH additions with u <= 2^-23 (truncation
-// included); twice that is taken, with the rounding of the ROUTER_MM_Z stored parts, and
-// 2^-100 for products that underflow.
+// The bound d_e = router_unit() |W_e| |x| + 2^-100: moeq_router_bound.h.
 //
 // Measured at 2048 tokens, 4096 x 256, 6 of them: 36.5 us (13 and 25) against 262 with all
 // logits in fp64; what bounds it is the vector unit's fp64 work and the chain of choices in
 // k_router_pick. Up to ROUTER_FEW_T tokens the one-launch form is faster (64 tokens 24.0
 // against 26.1 us; 128 tokens 38.0 against 26.7).
-constexpr int RM_FLUSH = 4;          // steps of 64 products
 constexpr int RM_E = 64, RM_T = 64;  // experts and tokens of a tile
 
 __global__ __launch_bounds__(256) void k_router_mm(RouterParams P, int z_count, int z_bytes, int tiles) {
@@ -195,7 +190,7 @@ constexpr int RP_SEG = 4096;  // values of a token held at a time (64 to a lane)
 // Two waves to a SIMD at least: left free, the compiler hoists conversions and constants
 // until a SIMD holds one.
 template <int N>
-__global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_count, double unit) {
+__global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_count) {
   const int lane = threadIdx.x & 63;
   const int t = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (t >= P.T) return;
@@ -295,7 +290,7 @@ __global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_co
     const int e = lane + 64 * i;
     bound[i] = 0;
     if (e < E) {
-      double k = z[i] + (unit * P.norms[e] * nx + 0x1p-100);
+      double k = z[i] + (router_unit() * P.norms[e] * nx + 0x1p-100);
       if (!soft) k = (double)score_above(P.scoring, (float)k);
       if (P.bias) k += (double)P.bias[e];
       // nothing is known of a sum that left fp32's range: its exact logit is needed
@@ -433,11 +428,10 @@ hipError_t launch_router(const RouterParams& p, hipStream_t s) {
     if (tiles * z > 0x7FFFFF || p.T > 0x7FFFFF) return hipErrorInvalidValue;
     hipLaunchKernelGGL(k_router_mm, dim3((unsigned)(tiles * z + (p.n_experts + 3) / 4)), dim3(256), 0, s, p, z, z_bytes,
                        (int)tiles);
-    const double unit = (2.0 * (16 + 4 * RM_FLUSH) + ROUTER_MM_Z) * 0x1p-23;
     const dim3 g((unsigned)((p.T + 3) / 4)), b(256);
-    if (p.n_experts <= 256) hipLaunchKernelGGL(k_router_pick<4>, g, b, 0, s, p, z, unit);
-    else if (p.n_experts <= 512) hipLaunchKernelGGL(k_router_pick<8>, g, b, 0, s, p, z, unit);
-    else hipLaunchKernelGGL(k_router_pick<16>, g, b, 0, s, p, z, unit);
+    if (p.n_experts <= 256) hipLaunchKernelGGL(k_router_pick<4>, g, b, 0, s, p, z);
+    else if (p.n_experts <= 512) hipLaunchKernelGGL(k_router_pick<8>, g, b, 0, s, p, z);
+    else hipLaunchKernelGGL(k_router_pick<16>, g, b, 0, s, p, z);
     return hipGetLastError();
   }
   for (int t0 = 0; t0 < p.T; t0 += 65535 * R_TOK) {  // grid rows

@@ -49,3 +49,41 @@ def test_weights_at_magnitudes_beyond_fp32(T, norm, scale):
         ids, rw = mq.router_topk(mq.Router(w, K, scoring="softmax", normalize=norm), x)
         s = np.take_along_axis(scores_ref(z, "softmax"), order[:, :K], 1)
         check(ids, rw, (order[:, :K], s / s.sum(axis=1, keepdims=True) if norm else s, None))
+
+
+def squares(T, E, H, p, seed):
+    """Tokens and experts whose products are one 1 and H - 1 times p (nearly): the largest
+    error that a running fp32 sum can have for its |W| |x|. The 1 lies at another place for
+    every expert; a token has a 1 wherever an expert does."""
+    g = torch.Generator().manual_seed(seed)
+    r = p ** 0.5
+    w = torch.full((E, H), r)
+    at = torch.randperm(H, generator=g)[:E]
+    w[torch.arange(E), at] = 1.0
+    x = torch.full((T, H), r)
+    mine = torch.arange(T) % E  # a token's own expert is the one with the product 1
+    x[torch.arange(T), at[mine]] = 1.0
+    return x.to(torch.bfloat16).cuda(), w.to(torch.bfloat16).cuda()
+
+
+@pytest.mark.parametrize("H", [256, 448])
+@pytest.mark.parametrize("p", [2.0 ** -24 * 1.02, 2.0 ** -23 * 0.985, 2.0 ** -22, 2.0 ** -12])
+def test_approximate_logits_stay_within_their_bound(H, p):
+    """The fp32 parts that a call leaves in its workspace (behind the header and the norms)
+    against the exact logits. A window of 256 products adds 16 instructions of 17 addends,
+    each within 2^-23 of the largest partial sum, which is at most |W| |x|; windows are
+    added in fp64 and the result is stored in fp32."""
+    T, E = 96, 40
+    x, w = squares(T, E, H, p, 3)
+    r = mq.Router(w, 4, scoring="softmax", normalize=True)
+    ws = r.workspace(T)
+    ids, rw = mq.router_topk(r, x, ws=ws)
+    torch.cuda.synchronize()
+    at = 256 + (E * 8 + 255) // 256 * 256
+    z = ws[at:at + 4 * T * E].clone().view(torch.float32).view(T, E).double().cpu().numpy()
+    X, W = host(x).astype(np.float64), host(w).astype(np.float64)
+    size = np.linalg.norm(X, axis=1)[:, None] * np.linalg.norm(W, axis=1)[None, :]
+    err = np.abs(z - X @ W.T) / size
+    say(f"bound H {H} p {p:.3g}: largest error {err.max() * 2 ** 23:.2f} of 2^-23 |W| |x|")
+    assert err.max() <= (16 * 17 + 1) * 2.0 ** -23
+    assert np.array_equal(ids.cpu().numpy(), route_ref(host(x), host(w), 4, "softmax", True, 1.0, None)[0])
