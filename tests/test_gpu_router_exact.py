@@ -87,3 +87,35 @@ def test_approximate_logits_stay_within_their_bound(H, p):
     say(f"bound H {H} p {p:.3g}: largest error {err.max() * 2 ** 23:.2f} of 2^-23 |W| |x|")
     assert err.max() <= (16 * 17 + 1) * 2.0 ** -23
     assert np.array_equal(ids.cpu().numpy(), route_ref(host(x), host(w), 4, "softmax", True, 1.0, None)[0])
+
+
+def near_ties(T, E, H, seed):
+    """Pairs of experts that differ in one weight by 2^-25, and tokens that hold +-1 there: a
+    pair's logits differ by 3e-8, less than fp32 resolves at their size."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((T, H), generator=g)
+    x[:, 100] = torch.randint(0, 2, (T,), generator=g) * 2.0 - 1.0
+    w = torch.randn((E, H), generator=g) / H ** 0.5
+    w[1::2] = w[0::2]
+    w[0::2, 100], w[1::2, 100] = 2.0 ** -18, 2.0 ** -18 * (1 + 2.0 ** -7)
+    return x.to(torch.bfloat16), w.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("kind", SCORES)
+@pytest.mark.parametrize("T", [40, 200])
+def test_pairs_that_fp32_does_not_resolve(T, kind):
+    say("pairs", T, kind)
+    K = 7  # odd: the border falls inside a pair
+    x, w = near_ties(T, 64, 2048, 6)
+    X, W = x.float().numpy(), w.float().numpy()
+    z32 = np.zeros((T, 64), np.float32)
+    for k in range(2048):  # a router with fp32 sums
+        z32 += X[:, k:k + 1] * W[:, k]
+    ref = route_ref(X, W, K, kind, True, 1.0, None)
+    top = -np.sort(-ref[2], axis=1)
+    gap = top[:, K - 1] - top[:, K]
+    assert ((gap > 1e-12) & (gap < 1e-7)).all()
+    wrong = (np.argsort(-z32, axis=1, kind="stable")[:, :K] != ref[0]).any(axis=1)
+    assert wrong.sum() > T // 4
+    ids, rw = mq.router_topk(mq.Router(w.cuda(), K, scoring=kind, normalize=True), x.cuda())
+    check(ids, rw, ref)
