@@ -81,7 +81,8 @@ __global__ __launch_bounds__(256) void k_router_choose(RouterParams P) {
 //      z_e + d_e is an upper bound of the expert's exact key. The K experts with the
 //      largest bounds get exact logits; then, while some other expert's bound reaches the
 //      K-th exact key, the one with the largest bound does too. What is left cannot be
-//      chosen.
+//      chosen. (Each costs 1 to 2 us, one after another: experts whose logits are equal, not
+//      known from the norms and more than a few would be slow.)
 //
 // The bound d_e = router_unit() |W_e| |x| + 2^-100: moeq_router_bound.h.
 //
@@ -285,18 +286,38 @@ __global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_co
     nx = wave_sum(nx);
   }
   nx = sqrt(nx);
+  auto score = [&](double v) { return soft ? v : score_of(P.scoring, v); };
+  uint32_t known = 0;  // experts whose logit the norms tell
 #pragma unroll
   for (int i = 0; i < N; i++) {
     const int e = lane + 64 * i;
     bound[i] = 0;
     if (e < E) {
-      double k = z[i] + (router_unit() * P.norms[e] * nx + 0x1p-100);
+      const double size = P.norms[e] * nx;
+      double k = z[i] + (router_unit() * size + 0x1p-100);
       if (!soft) k = (double)score_above(P.scoring, (float)k);
       if (P.bias) k += (double)P.bias[e];
       // nothing is known of a sum that left fp32's range: its exact logit is needed
       bound[i] = __builtin_fabs(z[i]) < __builtin_inf() && k == k ? order_of(k) : ~0ull;
       if (P.bias && P.bias[e] != P.bias[e]) bound[i] = order_of(-__builtin_inf());
+      if (!(size > 0.0)) {
+        z[i] = size;
+        known |= 1u << i;
+      }
     }
+  }
+  // Where the token or the expert is all zeros the logit is 0, and NaN where one of them holds a
+  // NaN or an infinity meets nothing but zeros: the product of the norms says which, and the
+  // key itself is the bound. Bounds above it would have every expert's exact logit taken for a
+  // token of padding (256 tokens, a third of them zeros, 2048 x 256: 419 against 31 us).
+  if (__ballot(known != 0)) {
+    const double s0 = score(0.0);
+#pragma unroll
+    for (int i = 0; i < N; i++)
+      if (known >> i & 1) {
+        const double s = z[i] == 0.0 ? s0 : z[i];
+        bound[i] = order_of(P.bias ? s + (double)P.bias[lane + 64 * i] : s);
+      }
   }
   const bool mine = lane < K;  // lane k < K: an expert of the best K so far, its exact logit and key
   int id = 0;
@@ -325,7 +346,6 @@ __global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_co
       if (lane == k) zk = v;
     }
   }
-  auto score = [&](double v) { return soft ? v : score_of(P.scoring, v); };
   double sk = score(zk);
   uint64_t key = 0;
   if (mine) key = order_of(P.bias ? sk + (double)P.bias[id] : sk);
@@ -336,7 +356,9 @@ __global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_co
     const int worst = lane_of_max(mine ? ~key : 0ull, mine ? ~(uint32_t)id : 0xFFFFFFFFu, low);
     low = ~low;
     next(e, top);
-    if (top == 0 || top < low) break;
+    // e has the lowest id of the largest bounds left: a key that is no more than equal to the
+    // worst's loses to it behind its id
+    if (top == 0 || top < low || (top == low && e > __builtin_amdgcn_readlane(id, worst))) break;
     take(e);
     const double v = logit(e);
     const double s = score(v);

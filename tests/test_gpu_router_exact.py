@@ -119,3 +119,49 @@ def test_pairs_that_fp32_does_not_resolve(T, kind):
     assert wrong.sum() > T // 4
     ids, rw = mq.router_topk(mq.Router(w.cuda(), K, scoring=kind, normalize=True), x.cuda())
     check(ids, rw, ref)
+
+
+def took(router, x):
+    """Microseconds of a call, the least of eight."""
+    ws, out = router.workspace(x.shape[0]), mq.router_topk(router, x)
+    best = float("inf")
+    for _ in range(8):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        mq.router_topk(router, x, *out, ws=ws)
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3)
+    return best
+
+
+TIES = [(w, k) for w in ("tokens of zeros", "tokens of NaN", "weights of zeros", "three experts left") for k in SCORES
+        if (w, k) != ("three experts left", "softmax")]  # a softmax with a bias takes all exact logits
+
+
+@pytest.mark.parametrize("what,kind", TIES)
+def test_tokens_and_experts_that_tie_cost_what_others_cost(what, kind):
+    """Padding, a new router and masks: all keys are equal or known without a sum, and the
+    choice is not looked for expert by expert."""
+    T, H, E, K = 256, 2048, 256, 6
+    x, w, _ = make(T, H, E, 21)
+    b = None if kind == "softmax" else torch.zeros(E, device="cuda")
+    if what == "tokens of zeros":
+        x[::3] = 0
+    elif what == "tokens of NaN":
+        x[::3, 77] = float("nan")
+    elif what == "weights of zeros":
+        w.zero_()
+    else:
+        b.fill_(float("-inf"))
+        b[[3, 40, 200]] = 0.0
+    router = mq.Router(w, K, scoring=kind, normalize=True, bias=b)
+    ids, rw = mq.router_topk(router, x)
+    if what == "tokens of NaN":
+        assert bool((ids[::3] == torch.arange(K, device="cuda", dtype=torch.int32)).all()) and bool(rw[::3].isnan().all())
+    check(ids, rw, route_ref(host(x), host(w), K, kind, True, 1.0, host(b)))
+    plain = took(mq.Router(make(T, H, E, 21)[1], K, scoring=kind, normalize=True, bias=None if b is None else 0 * rw.new_zeros(E)),
+                 make(T, H, E, 21)[0])
+    tied = took(router, x)
+    say(f"ties {what} {kind}: {tied:.1f} us, ordinary tokens {plain:.1f}")
+    assert tied < 2 * plain + 20
