@@ -5,7 +5,7 @@
 //   ids  = the top_k largest s + bias (fp64), ties to the lowest id
 //   w    = s[ids] (/ their sum) * scale
 //
-// Everything up to the weights is held in fp64 (but for one denominator: k_router_pick).
+// Everything up to the weights is held in fp64.
 // The choice of experts is discontinuous: fp32 logits carry an error of about 1e-6 that
 // depends on the order of summation, so two correct fp32 routers disagree on a near tie
 // and a token's output jumps. A product of two bf16 values is exact in fp64 and the vector
@@ -20,46 +20,53 @@ namespace {
 
 __global__ __launch_bounds__(512) void k_router_few(RouterParams P) { router_few(P, blockIdx.x, blockIdx.y); }
 
-constexpr int R_WAVES = 4;  // experts per work-group, one per wave
-constexpr int R_TOK = 8;    // tokens per work-group
+// All logits in fp64, on the fp64 matrix instruction, whose operands are converted once for
+// sixteen rows: v_mfma_f64_16x16x4, lane l: operand A's row l % 16 and B's row l % 16 at
+// K = l / 16; output register r: A's row l / 16 + 4 r times B's row l % 16. Which K a lane's
+// values stand for is free as long as both operands agree, so a lane takes whole 16-byte
+// chunks of its rows. A work-group has 16 tokens and 16 experts; its waves take runs of 128
+// bytes of K in turn, and their sums are added in the order of the waves.
+constexpr int RL_WAVES = 8;
+typedef double f64x4 __attribute__((ext_vector_type(4)));
 
-// Lane l takes the 16-byte chunks l, l + 64, ... of the expert's row.
-__global__ __launch_bounds__(64 * R_WAVES) void k_router_logits(RouterParams P) {
+__global__ __launch_bounds__(64 * RL_WAVES) void k_router_logits(RouterParams P) {
+  __shared__ double part[RL_WAVES][16][17];
   const int lane = threadIdx.x & 63;
-  const int e = blockIdx.x * R_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int t0 = blockIdx.y * R_TOK, tn = min(R_TOK, P.T - t0);
-  if (e >= P.n_experts) return;
-  const uint16_t* w = P.w + (size_t)e * P.hidden;
-  const uint16_t* x = P.x + (size_t)t0 * P.hidden;
-  double acc[R_TOK];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, g = lane >> 4;
+  const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
+  const int chunks = P.hidden / 8;
+  const uint16_t* x = P.x + (size_t)min(t0 + n, P.T - 1) * P.hidden;
+  const uint16_t* w = P.w + (size_t)min(e0 + n, P.n_experts - 1) * P.hidden;
+  f64x4 acc = {0.0, 0.0, 0.0, 0.0};
+  for (int c0 = 8 * wave; c0 < chunks; c0 += 8 * RL_WAVES) {
+    u32x4 xv[2], wv[2];
 #pragma unroll
-  for (int t = 0; t < R_TOK; t++) acc[t] = 0.0;
-  for (int c = lane; c < P.hidden / 8; c += 64) {
-    const u32x4 wv = ld16(w + 8 * c);
-    double wd[8];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      wd[2 * i] = (double)u2f(wv[i] << 16);
-      wd[2 * i + 1] = (double)u2f(wv[i] & 0xFFFF0000u);
+    for (int i = 0; i < 2; i++) {
+      const int c = c0 + 4 * i + g, in = min(c, chunks - 1);
+      xv[i] = ld16(x + 8 * (size_t)in);
+      wv[i] = ld16(w + 8 * (size_t)in);
+      if (c >= chunks) xv[i] = wv[i] = u32x4{0u, 0u, 0u, 0u};  // both: 0 times an infinity of the last chunk
     }
 #pragma unroll
-    for (int t = 0; t < R_TOK; t++) {
-      if (t < tn) {
-        const u32x4 xv = ld16(x + (size_t)t * P.hidden + 8 * c);
+    for (int i = 0; i < 2; i++)
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          acc[t] = __builtin_fma(wd[2 * i], (double)u2f(xv[i] << 16), acc[t]);
-          acc[t] = __builtin_fma(wd[2 * i + 1], (double)u2f(xv[i] & 0xFFFF0000u), acc[t]);
-        }
+      for (int j = 0; j < 4; j++) {
+        acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)u2f(xv[i][j] << 16), (double)u2f(wv[i][j] << 16), acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)u2f(xv[i][j] & 0xFFFF0000u), (double)u2f(wv[i][j] & 0xFFFF0000u),
+                                                   acc, 0, 0, 0);
       }
-    }
   }
 #pragma unroll
-  for (int t = 0; t < R_TOK; t++)
-    if (t < tn) {
-      const double z = wave_sum(acc[t]);
-      if (lane == 0) P.logits[(size_t)(t0 + t) * P.n_experts + e] = z;
-    }
+  for (int r = 0; r < 4; r++) part[wave][g + 4 * r][n] = acc[r];
+  __syncthreads();
+  const int tk = threadIdx.x >> 4, e = e0 + (threadIdx.x & 15);
+  if (threadIdx.x < 256 && t0 + tk < P.T && e < P.n_experts) {
+    double z = part[0][tk][threadIdx.x & 15];
+#pragma unroll
+    for (int v = 1; v < RL_WAVES; v++) z += part[v][tk][threadIdx.x & 15];
+    P.logits[(size_t)(t0 + tk) * P.n_experts + e] = z;
+  }
 }
 
 __global__ __launch_bounds__(256) void k_router_choose(RouterParams P) {
@@ -287,7 +294,8 @@ __global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_co
   }
   nx = sqrt(nx);
   auto score = [&](double v) { return soft ? v : score_of(P.scoring, v); };
-  uint32_t known = 0;  // experts whose logit the norms tell
+  uint32_t known = 0;   // experts whose logit the norms tell
+  bool spoilt = false;  // one of them NaN
 #pragma unroll
   for (int i = 0; i < N; i++) {
     const int e = lane + 64 * i;
@@ -303,6 +311,7 @@ __global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_co
       if (!(size > 0.0)) {
         z[i] = size;
         known |= 1u << i;
+        spoilt |= size != size;
       }
     }
   }
@@ -349,6 +358,7 @@ __global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_co
   double sk = score(zk);
   uint64_t key = 0;
   if (mine) key = order_of(P.bias ? sk + (double)P.bias[id] : sk);
+  bool nan = __ballot((mine && zk != zk) || spoilt) != 0;
   for (;;) {
     int e;
     uint64_t top, low;
@@ -363,11 +373,8 @@ __global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_co
     const double v = logit(e);
     const double s = score(v);
     const uint64_t kv = order_of(P.bias ? s + (double)P.bias[e] : s);
-    int out = e;  // the one that is not among the K any more
-    double zo = v;
+    nan |= v != v;
     if (kv > low || (kv == low && e < __builtin_amdgcn_readlane(id, worst))) {
-      out = __builtin_amdgcn_readlane(id, worst);
-      zo = read_lane(zk, worst);
       if (lane == worst) {
         id = e;
         zk = v;
@@ -375,36 +382,18 @@ __global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_co
         key = kv;
       }
     }
-    // for the normaliser: its approximate logit may be an overflow's infinity or NaN
-#pragma unroll
-    for (int i = 0; i < N; i++)
-      if (lane + 64 * i == out) z[i] = zo;
   }
 
-  // The normaliser over all experts: the chosen ones' logits exact, the others' from fp32 sums
-  // (within the bound above; it cancels where the K are normalised). All of them exact would
-  // take the 262 us of the fp64 form.
+  // Normalised over the K, so the denominator over all experts cancels: but for a NaN logit
+  // in it, chosen or not, which leaves no number.
   if (soft) {
-    // the chosen ones' approximate logits leave first: they may be an overflow's infinity too
-    for (int k = 0; k < K; k++) {
-      const int e = __builtin_amdgcn_readlane(id, k);
-#pragma unroll
-      for (int i = 0; i < N; i++)
-        if (lane + 64 * i == e) z[i] = -__builtin_inf();
-    }
     double top = mine ? zk : -__builtin_inf();
-#pragma unroll
-    for (int i = 0; i < N; i++) top = z[i] > top ? z[i] : top;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const double v = __shfl_xor(top, o, 64);
       top = v > top ? v : top;
     }
-    sk = exp(zk - top);
-    double sum = mine ? sk : 0.0;
-#pragma unroll
-    for (int i = 0; i < N; i++) sum += lane + 64 * i < E ? exp(z[i] - top) : 0.0;
-    sk /= wave_sum(sum);
+    sk = nan ? __builtin_nan("") : exp(zk - top);
   }
   int rank = 0;
   for (int k = 0; k < K; k++) {
@@ -442,8 +431,10 @@ hipError_t launch_router(const RouterParams& p, hipStream_t s) {
     hipLaunchKernelGGL(k_router_few, g, dim3(512), 0, s, p);
     return hipGetLastError();
   }
-  // A softmax with a bias orders the experts by the normaliser too: all logits in fp64.
-  if (!(p.scoring == SCORE_SOFTMAX && p.bias)) {
+  // The denominator of a softmax takes all logits, and fp32 ones would be off by up to
+  // 274 x 2^-23 |W_e| |x| each. It cancels where the K weights are normalised, unless a bias makes
+  // the choice depend on it.
+  if (p.scoring != SCORE_SOFTMAX || (p.normalize && !p.bias)) {
     const long tiles = (long)((p.n_experts + RM_E - 1) / RM_E) * ((p.T + RM_T - 1) / RM_T);
     const int z = mm_split(p, tiles);
     const int z_bytes = (2 * p.hidden / z + 127) / 128 * 128;
@@ -456,15 +447,15 @@ hipError_t launch_router(const RouterParams& p, hipStream_t s) {
     else hipLaunchKernelGGL(k_router_pick<16>, g, b, 0, s, p, z);
     return hipGetLastError();
   }
-  for (int t0 = 0; t0 < p.T; t0 += 65535 * R_TOK) {  // grid rows
+  for (long t0 = 0; t0 < p.T; t0 += 1 << 19) {  // grid rows
     RouterParams q = p;
-    q.T = p.T - t0 < 65535 * R_TOK ? p.T - t0 : 65535 * R_TOK;
+    q.T = (int)(p.T - t0 < (1 << 19) ? p.T - t0 : 1 << 19);
     q.x += (size_t)t0 * p.hidden;
     q.logits += (size_t)t0 * p.n_experts;
     q.ids += (size_t)t0 * p.top_k;
     q.rw += (size_t)t0 * p.top_k;
-    const dim3 g((unsigned)((p.n_experts + R_WAVES - 1) / R_WAVES), (unsigned)((q.T + R_TOK - 1) / R_TOK));
-    hipLaunchKernelGGL(k_router_logits, g, dim3(64 * R_WAVES), 0, s, q);
+    const dim3 g((unsigned)((p.n_experts + 15) / 16), (unsigned)((q.T + 15) / 16));
+    hipLaunchKernelGGL(k_router_logits, g, dim3(64 * RL_WAVES), 0, s, q);
     hipLaunchKernelGGL(k_router_choose, dim3((unsigned)((q.T + 3) / 4)), dim3(256), 0, s, q);
   }
   return hipGetLastError();

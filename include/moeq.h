@@ -386,11 +386,10 @@ typedef struct moeq_shared {
  * lower id first; a NaN counts below every number; softmax without a bias: in the
  * order of the logits), and their weights s * scale, or
  * s / (sum of the K) * scale. The logits W x are sums of exact products in fp64, and so
- * are scores and sums: the choice does not depend on an order of summation beyond
- * fp64's. (One exception, beyond 64 tokens, softmax with normalize 0 and no bias: the
- * logits that were not chosen enter the softmax's denominator from fp32 sums, each
- * within 2^-16 |W_e| |x| of the exact one and far nearer as a rule.) x bf16 [T][H], 16-byte aligned; ids int32 [T][K] (always distinct and inside
- * [0, E)) and rw fp32 [T][K] overwritten: what moeq_expert_forward takes. A sum of 0
+ * are scores, sums and denominators at every T: neither the choice nor the weights
+ * depend on an order of summation beyond fp64's. x bf16 [T][H], 16-byte aligned; ids
+ * int32 [T][K] (always distinct and inside [0, E)) and rw fp32 [T][K] overwritten:
+ * what moeq_expert_forward takes. A sum of 0
  * gives weights 0. ws: moeq_router_workspace_bytes(R, T) bytes, 256-byte aligned,
  * zero-filled once before first use (or passed to moeq_workspace_init), not shared
  * with an overlapping call. T == 0 is a no-op. */

@@ -165,3 +165,46 @@ def test_tokens_and_experts_that_tie_cost_what_others_cost(what, kind):
     tied = took(router, x)
     say(f"ties {what} {kind}: {tied:.1f} us, ordinary tokens {plain:.1f}")
     assert tied < 2 * plain + 20
+
+
+@pytest.mark.parametrize("T,H,E,K", [(65, 1024, 96, 6), (100, 8, 5, 2), (66, 1032, 64, 1), (257, 2056, 513, 16), (300, 4096, 256, 6),
+                                     (90, 8200, 33, 6)])
+@pytest.mark.parametrize("common", [0.0, 512.0])
+def test_softmax_weights_do_not_depend_on_the_number_of_tokens(T, H, E, K, common):
+    """Weights over all experts, with and without an activation outlier that adds the same
+    large number to every logit: the fp64 values at every number of tokens."""
+    say("softmax weights", T, H, E, K, common)
+    x, w, _ = make(T, H, E, 44 + T)
+    if common:
+        x[:, 5], w[:, 5] = common, 1.0
+    router = mq.Router(w, K, scoring="softmax")
+    ids, rw = mq.router_topk(router, x)
+    check(ids, rw, route_ref(host(x), host(w), K, "softmax", False, 1.0, None))
+    few = mq.router_topk(router, x[:40])
+    assert torch.equal(few[0], ids[:40])
+    assert bool(((few[1] - rw[:40]).abs() <= 2.0 ** -23 * rw[:40]).all())
+
+
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("T", [4, 100])
+def test_an_expert_without_a_logit(T, norm):
+    """A NaN in one expert's weights: it comes last, a softmax over it has no weights, and the
+    other scores do not see it. An infinity that meets zeros is the same."""
+    say("expert NaN", T, norm)
+    for bad in (float("nan"), float("inf")):
+        x, w, _ = make(T, 512, 90, 51)
+        w[37] = 0
+        w[37, 9] = bad
+        x[:, 9] = 0
+        z = x.double().cpu().numpy() @ np.nan_to_num(w.double().cpu().numpy(), nan=0.0, posinf=0.0).T
+        z[:, 37] = -np.inf
+        order = np.argsort(-z, axis=1, kind="stable")[:, :6]
+        for kind in SCORES:
+            ids, rw = mq.router_topk(mq.Router(w, 6, scoring=kind, normalize=norm), x)
+            assert np.array_equal(ids.cpu().numpy(), order)
+            if kind == "softmax":
+                assert bool(rw.isnan().all())
+            else:
+                s = np.take_along_axis(scores_ref(z, kind), order, 1)
+                check(ids, rw, (order, s / s.sum(axis=1, keepdims=True) if norm else s, None))
+
