@@ -10,6 +10,7 @@
 // 2^31 in any order, so every split of K below gives the same bits. The scales
 // multiply the sum once, in fp32: int32 -> fp32 is the first rounding, two products
 // and the bias follow, and bf16 outputs are rounded once more at the store.
+#include "moeq_grid.h"
 #include "moeq_int8.h"
 #include "moeq_tiled.h"
 
@@ -379,7 +380,7 @@ template <int WM, int WN, int TM, int TN, int STAGES, int BK, int Q, int SPREAD>
 hipError_t go_tiled(const Int8Params& p, hipStream_t s) {
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
   const long blocks = (long)((p.rows + BM - 1) / BM) * ((p.T + BN - 1) / BN);
-  if (blocks > 0x7FFFFF) return hipErrorInvalidValue;
+  if (blocks > GRID_MAX_BLOCKS) return hipErrorInvalidValue;
   const dim3 g((unsigned)blocks), b(64 * WM * WN);
   const bool runs = p.rows % 8 == 0 && ((uintptr_t)p.y | (uintptr_t)p.bias | (uintptr_t)p.add) % 16 == 0;
   if (runs && p.out_bf16 && !p.bias && !p.add)
@@ -395,7 +396,7 @@ template <int WM, int WN, int TN, int STAGES, int BK, int Q, int SPREAD>
 hipError_t go_gu_tiled(const Int8Params& p, hipStream_t s) {
   constexpr int BM = WM * 32, BN = WN * TN * 32;
   const long blocks = (long)((p.rows + BM - 1) / BM) * ((p.T + BN - 1) / BN);
-  if (blocks > 0x7FFFFF) return hipErrorInvalidValue;
+  if (blocks > GRID_MAX_BLOCKS) return hipErrorInvalidValue;
   hipLaunchKernelGGL((k_gu_int8_tiled<WM, WN, TN, STAGES, BK, Q, SPREAD>), dim3((unsigned)blocks), dim3(64 * WM * WN), 0, s, p);
   return hipGetLastError();
 }
@@ -491,11 +492,10 @@ hipError_t linear_int8(Int8Params p, hipStream_t s) {
 hipError_t launch_linear_int8(const Int8Params& p, hipStream_t s) {
   if (p.T < 1 || p.rows < 1 || p.rows > INT8_MAX_ROWS || p.cols < 16 || p.cols % 16 || p.cols > INT8_MAX_COLS)
     return hipErrorInvalidValue;
-  // a grid holds below 2^32 threads: 2^16 tokens at a time keep every tile's number of
-  // work-groups below that for up to INT8_MAX_ROWS rows
-  for (long t0 = 0; t0 < p.T; t0 += 1 << 16) {
+  const long most = int8_tokens(p.rows);
+  for (long t0 = 0; t0 < p.T; t0 += most) {
     Int8Params q = p;
-    q.T = (int)(p.T - t0 < (1 << 16) ? p.T - t0 : 1 << 16);
+    q.T = (int)(p.T - t0 < most ? p.T - t0 : most);
     q.xq += (size_t)t0 * p.cols;
     q.xs += t0;
     q.y = (uint8_t*)p.y + (size_t)t0 * p.rows * (p.out_bf16 ? 2 : 4);
@@ -537,9 +537,10 @@ hipError_t launch_gate_up_int8(const Int8Params& p, hipStream_t s) {
   if (p.T < 1 || p.rows < 1 || p.rows > INT8_MAX_ROWS || p.cols < 16 || p.cols % 16 || p.cols > INT8_MAX_COLS ||
       p.rows % 4 || (uintptr_t)p.y % 16)
     return hipErrorInvalidValue;
-  for (long t0 = 0; t0 < p.T; t0 += 1 << 16) {  // as launch_linear_int8
+  const long most = int8_tokens(p.rows);
+  for (long t0 = 0; t0 < p.T; t0 += most) {
     Int8Params q = p;
-    q.T = (int)(p.T - t0 < (1 << 16) ? p.T - t0 : 1 << 16);
+    q.T = (int)(p.T - t0 < most ? p.T - t0 : most);
     q.xq += (size_t)t0 * p.cols;
     q.xs += t0;
     q.y = (float*)p.y + (size_t)t0 * p.rows;
