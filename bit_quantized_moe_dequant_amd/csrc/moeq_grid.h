@@ -13,4 +13,8 @@ constexpr long int8_tokens(int rows) {
   return t < (1 << 16) ? t : 1 << 16;
 }
 
+// The router: 2^22 tokens are 2^20 tiles of 64 tokens x 64 of up to 1024 experts (whose hidden
+// size is not split at that number), and 2^20 work-groups of four tokens.
+constexpr long ROUTER_TOKENS = 1 << 22;
+
 }  // namespace moeq

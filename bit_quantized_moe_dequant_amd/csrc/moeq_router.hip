@@ -10,6 +10,7 @@
 // depends on the order of summation, so two correct fp32 routers disagree on a near tie
 // and a token's output jumps. A product of two bf16 values is exact in fp64 and the vector
 // unit issues fp64 FMAs at the fp32 rate here, so the exactness costs the conversions only.
+#include "moeq_grid.h"
 #include "moeq_router.h"
 #include "moeq_router_bound.h"
 #include "moeq_tiled.h"
@@ -435,16 +436,21 @@ hipError_t launch_router(const RouterParams& p, hipStream_t s) {
   // 274 x 2^-23 |W_e| |x| each. It cancels where the K weights are normalised, unless a bias makes
   // the choice depend on it.
   if (p.scoring != SCORE_SOFTMAX || (p.normalize && !p.bias)) {
-    const long tiles = (long)((p.n_experts + RM_E - 1) / RM_E) * ((p.T + RM_T - 1) / RM_T);
-    const int z = mm_split(p, tiles);
-    const int z_bytes = (2 * p.hidden / z + 127) / 128 * 128;
-    if (tiles * z > 0x7FFFFF || p.T > 0x7FFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(k_router_mm, dim3((unsigned)(tiles * z + (p.n_experts + 3) / 4)), dim3(256), 0, s, p, z, z_bytes,
-                       (int)tiles);
-    const dim3 g((unsigned)((p.T + 3) / 4)), b(256);
-    if (p.n_experts <= 256) hipLaunchKernelGGL(k_router_pick<4>, g, b, 0, s, p, z);
-    else if (p.n_experts <= 512) hipLaunchKernelGGL(k_router_pick<8>, g, b, 0, s, p, z);
-    else hipLaunchKernelGGL(k_router_pick<16>, g, b, 0, s, p, z);
+    for (long t0 = 0; t0 < p.T; t0 += ROUTER_TOKENS) {
+      RouterParams q = p;
+      q.T = (int)(p.T - t0 < ROUTER_TOKENS ? p.T - t0 : ROUTER_TOKENS);
+      q.x += (size_t)t0 * p.hidden;
+      q.ids += (size_t)t0 * p.top_k;
+      q.rw += (size_t)t0 * p.top_k;
+      const int tiles = (q.n_experts + RM_E - 1) / RM_E * ((q.T + RM_T - 1) / RM_T);
+      const int z = mm_split(q, tiles);
+      const int z_bytes = (2 * q.hidden / z + 127) / 128 * 128;
+      hipLaunchKernelGGL(k_router_mm, dim3((unsigned)(tiles * z + (q.n_experts + 3) / 4)), dim3(256), 0, s, q, z, z_bytes, tiles);
+      const dim3 g((unsigned)((q.T + 3) / 4)), b(256);
+      if (q.n_experts <= 256) hipLaunchKernelGGL(k_router_pick<4>, g, b, 0, s, q, z);
+      else if (q.n_experts <= 512) hipLaunchKernelGGL(k_router_pick<8>, g, b, 0, s, q, z);
+      else hipLaunchKernelGGL(k_router_pick<16>, g, b, 0, s, q, z);
+    }
     return hipGetLastError();
   }
   for (long t0 = 0; t0 < p.T; t0 += 1 << 19) {  // grid rows

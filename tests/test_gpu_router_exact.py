@@ -208,3 +208,24 @@ def test_an_expert_without_a_logit(T, norm):
                 s = np.take_along_axis(scores_ref(z, kind), order, 1)
                 check(ids, rw, (order, s / s.sum(axis=1, keepdims=True) if norm else s, None))
 
+
+
+@pytest.mark.parametrize("kind,norm", [("sigmoid", True), ("softmax", False)])
+def test_more_tokens_than_one_launch(kind, norm):
+    say("launches", kind)
+    T, H, E, K = (1 << 23) + 70, 8, 4, 2
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    x = torch.randn((T, H), generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn((E, H), generator=g, device="cuda").to(torch.bfloat16)
+    ids, rw = mq.router_topk(mq.Router(w, K, scoring=kind, normalize=norm), x)
+    z = torch.zeros((T, E), dtype=torch.float64, device="cuda")
+    for h in range(H):
+        z += x[:, h:h + 1].double() * w[:, h].double()
+    s = torch.sigmoid(z) if kind == "sigmoid" else torch.softmax(z, dim=1)
+    val, ref = torch.sort(z, dim=1, descending=True, stable=True)
+    clear = (val[:, :K] - val[:, 1:K + 1]).amin(dim=1) > 1e-12
+    assert torch.equal(ids.long()[clear], ref[clear, :K]) and bool((clear | (ids >= 0).all(dim=1)).all())
+    top = s.gather(1, ids.long())
+    top = top / top.sum(dim=1, keepdim=True) if norm else top
+    assert bool(((rw.double() - top).abs() <= 2.0 ** -23 * top).all())

@@ -24,6 +24,8 @@ int main() {
     }
   }
   if (moeq::int8_tokens(8192) != 1 << 16) return 3;
+  const long tiles_router = 1024 / 64 * (moeq::ROUTER_TOKENS / 64), groups = moeq::ROUTER_TOKENS / 4;
+  if ((tiles_router + 256) * 256 >= 1l << 32 || groups * 256 >= 1l << 32 || tiles_router < 256) return 4;
   std::puts("ok");
 }
 '''
