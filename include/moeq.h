@@ -298,7 +298,8 @@ int moeq_prefill_down(const moeq_layer* L, const uint8_t* hq, const uint8_t* hs,
                       int T, float* y, void* ws, size_t ws_bytes, void* stream);
 
 /* Dense block-quantized linear y[T][rows] = W_expert x[T][cols] (fp32 out). Any
- * format but INT8 (moeq_linear_int8); FP8_B128 is the dense-layer format (IQ2_XXS + Q2_K + FP8 hybrid card).
+ * format but INT8 (moeq_linear_int8); FP8_B128 is the dense-layer format (IQ2_XXS +
+ * Q2_K + FP8 hybrid card).
  * MXFP8, MXFP8_TILED and FP8_B32 run on the block-scaled FP8 matrix instruction
  * for every T (the weights' e8m0 scale is the instruction's scale; x enters as
  * two E4M3 terms per value with e8m0 scales per 32, exact to 2^-21.8 of each
@@ -340,9 +341,9 @@ int moeq_quantize_int8_f32(const float* x, int T, int K, int8_t* q, float* scale
  * of an MOEQ_FMT_INT8 weight. The sum is exact (int32; cols at most 65536, any codes);
  * the scales and the bias are applied in fp32. xq i8 [T][cols], 16-byte aligned; xs
  * fp32 [T]; bias fp32 [rows] or NULL; y [T][rows] overwritten, fp32 (MOEQ_OUT_F32) or
- * bf16 rounded to nearest even (MOEQ_OUT_BF16), aligned to its element. Any T;
- * rows up to 2^23 (MOEQ_E_SHAPE beyond); T == 0 is a no-op. The same inputs give the same bits whatever the batch they
- * are part of. */
+ * bf16 rounded to nearest even (MOEQ_OUT_BF16), aligned to its element. Any T; rows
+ * up to 2^23 (MOEQ_E_SHAPE beyond); T == 0 is a no-op. The same inputs give the same
+ * bits whatever the batch they are part of. */
 int moeq_linear_int8(const moeq_weight* w, int expert, const int8_t* xq, const float* xs, int T, const float* bias,
                      int out_type, void* y, void* stream);
 
@@ -389,18 +390,21 @@ typedef struct moeq_shared {
  * are scores, sums and denominators at every T: neither the choice nor the weights
  * depend on an order of summation beyond fp64's. x bf16 [T][H], 16-byte aligned; ids
  * int32 [T][K] (always distinct and inside [0, E)) and rw fp32 [T][K] overwritten:
- * what moeq_expert_forward takes. A sum of 0
- * gives weights 0. ws: moeq_router_workspace_bytes(R, T) bytes, 256-byte aligned,
- * zero-filled once before first use (or passed to moeq_workspace_init), not shared
- * with an overlapping call. T == 0 is a no-op. */
+ * what moeq_expert_forward takes. A sum of 0 gives weights 0. ws:
+ * moeq_router_workspace_bytes(R, T) bytes, 256-byte aligned, zero-filled once before
+ * first use (or passed to moeq_workspace_init), not shared with an overlapping call
+ * (calls on one stream do not overlap if no other thread queues launches between
+ * theirs). Any T; T == 0 is a no-op. */
 size_t moeq_router_workspace_bytes(const moeq_router* R, int T);
 int moeq_router_topk(const moeq_router* R, const void* x, int T, int32_t* ids, float* rw, void* ws, size_t ws_bytes,
                      void* stream);
 
 /* The whole layer for x[T][H] (bf16): y = bf16(routed + shared), with the routed
- * experts of moeq_router_topk as moeq_expert_forward computes them and the shared
- * expert Ds (silu(Gs x) * (Us x)) on the INT8 linears: x and the intermediate h
- * (fp32) quantised per token as by moeq_quantize_int8, sums in fp32, one rounding to
+ * experts of moeq_router_topk as moeq_expert_forward computes them (so from 128 tokens
+ * on an MXFP4 projection takes its activations as MXFP8, which moves the routed part by
+ * 3 to 5 % of its RMS; below, and for the other formats, they keep all their bits) and
+ * the shared expert Ds (silu(Gs x) * (Us x)) on the INT8 linears: x and the intermediate
+ * h (fp32) quantised per token as by moeq_quantize_int8, sums in fp32, one rounding to
  * bf16 at the end. S may be NULL (no shared expert). R and L agree on hidden,
  * n_experts and top_k. ids and rw (int32 / fp32 [T][K]) receive the routing, or NULL.
  * ws: moeq_moe_workspace_bytes bytes, 256-byte aligned, zero-filled once before first
