@@ -402,7 +402,7 @@ int moeq_router_topk(const moeq_router* R, const void* x, int T, int32_t* ids, f
 /* The whole layer for x[T][H] (bf16): y = bf16(routed + shared), with the routed
  * experts of moeq_router_topk as moeq_expert_forward computes them (so from 128 tokens
  * on an MXFP4 projection takes its activations as MXFP8, which moves the routed part by
- * 3 to 5 % of its RMS; below, and for the other formats, they keep all their bits) and
+ * 3 to 5 % of its RMS; fewer tokens and other formats' are not rounded to 8 bits) and
  * the shared expert Ds (silu(Gs x) * (Us x)) on the INT8 linears: x and the intermediate
  * h (fp32) quantised per token as by moeq_quantize_int8, sums in fp32, one rounding to
  * bf16 at the end. S may be NULL (no shared expert). R and L agree on hidden,
