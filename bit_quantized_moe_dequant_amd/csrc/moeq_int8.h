@@ -7,8 +7,6 @@
 
 namespace moeq {
 
-typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-
 // fp32 -> bf16 bits, round to nearest even, for any input: NaNs stay NaN (quiet), infinities
 // are kept.
 __device__ __forceinline__ uint32_t f32_bf16_rne_nan(float f) {

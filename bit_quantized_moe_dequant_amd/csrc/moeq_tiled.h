@@ -17,10 +17,10 @@
 // loop over whole steps has no branches (they cost a third of a 64 x 64 tile's time).
 #pragma once
 #include "moeq_device.h"
+#include "moeq_wave.h"
 
 namespace moeq {
 
-typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));

@@ -1,9 +1,12 @@
-// Reductions over a wave.
+// Reductions over a wave, and the operand type of the matrix instructions that take 16 bytes
+// to a lane.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 namespace moeq {
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 // Largest of the lanes' values, by row shifts and row broadcasts (the result gathers in
 // lane 63): a tenth of the latency of six exchanges through LDS.

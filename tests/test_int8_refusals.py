@@ -114,3 +114,15 @@ def test_binding_refusals():
             bad()
     with pytest.raises(ValueError, match="GPU"):  # well-formed, but not on a GPU
         mq.linear_int8(w, xq, xs, y=torch.zeros((3, 64)))
+
+
+def test_the_binding_knows_which_calls_store_no_codes():
+    """linear_int8_dynamic makes no workspace where the library needs none (an empty one of 256
+    bytes), and one wherever it does."""
+    lib = mq._lib()
+    for cols in (16, 64, 4080, 4096, 4112, 8192, 8208, 16384, 16400, 32768, 32784, 65536):
+        for T in range(1, 20):
+            stored = T > 16 or cols << (T - 1).bit_length() > 65536  # as in linear_int8_dynamic
+            assert (lib.moeq_linear_int8_workspace_bytes(T, cols) > 256) == stored, (T, cols)
+            got = dynamic(fake(cols=cols), T=T, ws=0, n=0) if stored else None
+            assert got in (None, -5)
