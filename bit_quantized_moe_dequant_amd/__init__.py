@@ -164,9 +164,9 @@ def _require_cuda(*ts):
 
 def _want(name, t, dtypes, shape):
     """Raise ValueError unless t is a contiguous tensor of one of `dtypes` with
-    exactly `shape` (whether it is on the GPU is checked after all of them). The C ABI sees raw pointers only, so a wrong dtype (int64 ids
-    read as pairs of int32), a short buffer or a strided view must be caught here,
-    before anything is launched."""
+    exactly `shape` (whether it is on the GPU is checked after all of them). The C ABI
+    sees raw pointers only, so a wrong dtype (int64 ids read as pairs of int32), a short
+    buffer or a strided view must be caught here, before anything is launched."""
     torch = _torch()
     if t is None:
         raise ValueError(f"{name}: missing")
@@ -746,7 +746,10 @@ class _Workspaces:
 
 
 def router_topk(router: Router, x, ids=None, rw=None, ws=None):
-    """(ids [T, K] int32, route weights [T, K] fp32) of bf16 tokens x [T, H]."""
+    """(ids [T, K] int32, route weights [T, K] fp32) of bf16 tokens x [T, H]. Without ws the
+    router's own for the current stream is used; host threads may share a router. Under
+    capture that is an allocation and a clearing launch in the graph: pass a ws made before
+    (workspace()) and kept as long as the graph to spare them."""
     T = _tokens("x", x, router.hidden)
     gpu = _gpu()
     _need("x", x, gpu[2], (T, router.hidden))
@@ -772,7 +775,9 @@ def router_topk(router: Router, x, ids=None, rw=None, ws=None):
 
 
 def moe_forward(moe: MoeLayer, x, y=None, ids=None, rw=None, ws=None):
-    """The whole layer on bf16 tokens x [T, H]: (y [T, H] bf16, ids [T, K], route weights [T, K])."""
+    """The whole layer on bf16 tokens x [T, H]: (y [T, H] bf16, ids [T, K], route weights [T, K]).
+    ws, threads and capture as for router_topk. From 128 tokens on, MXFP4 projections take
+    8-bit activations, as in expert_forward."""
     T = _tokens("x", x, moe.hidden)
     gpu = _gpu()
     _need("x", x, gpu[2], (T, moe.hidden))

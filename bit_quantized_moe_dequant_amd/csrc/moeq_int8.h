@@ -70,8 +70,9 @@ __device__ __forceinline__ void store_out(const Int8Params& P, size_t t, int r, 
 // pair's silu(gate) * up (MATS = 2), by one work-group of W waves for 16 weight rows. Every
 // work-group makes the codes of its tokens itself, in LDS, while its weight loads are on
 // their way: a second launch and a round trip of the codes through memory cost more at
-// these sizes than the repeated conversion (one token, 4096 x 4096: 6.6 us in two launches,
-// 4.2 in one). Wave w works on tokens w / wpt + (W / wpt) j (wpt waves to a token, TPW
+// these sizes than the repeated conversion (one token, 4096 x 4096, in a graph over twenty
+// weights: 8.7 us in two launches, 6.1 in one; 7.7 and 4.4 where the weight stays in L2;
+// sixteen tokens, 2048 x 4096: 9.2 and 9.0). Wave w works on tokens w / wpt + (W / wpt) j (wpt waves to a token, TPW
 // tokens to a wave), lane l on chunks of 8 values l, l + 64 wpt, ... (CPL of them), so the
 // codes take at most 512 W TPW CPL bytes. The product is that of k_int8_few.
 template <int MATS, int TPW, int CPL, int W, int IN_F32>

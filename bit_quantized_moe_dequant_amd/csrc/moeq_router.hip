@@ -26,7 +26,9 @@ __global__ __launch_bounds__(512) void k_router_few(RouterParams P) { router_few
 // K = l / 16; output register r: A's row l / 16 + 4 r times B's row l % 16. Which K a lane's
 // values stand for is free as long as both operands agree, so a lane takes whole 16-byte
 // chunks of its rows. A work-group has 16 tokens and 16 experts; its waves take runs of 128
-// bytes of K in turn, and their sums are added in the order of the waves.
+// bytes of K in turn, and their sums are added in the order of the waves. 2048 tokens, 4096 x
+// 256: 85 us, 50 TFLOP/s (one FMA chain per token and expert on the vector unit, its operands
+// converted for each: 235); the fp64 matrix rate bounds it, at 78.6 a floor of 55.
 constexpr int RL_WAVES = 8;
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
@@ -94,10 +96,10 @@ __global__ __launch_bounds__(256) void k_router_choose(RouterParams P) {
 //
 // The bound d_e = router_unit() |W_e| |x| + 2^-100: moeq_router_bound.h.
 //
-// Measured at 2048 tokens, 4096 x 256, 6 of them: 36.5 us (13 and 25) against 262 with all
-// logits in fp64; what bounds it is the vector unit's fp64 work and the chain of choices in
-// k_router_pick. Up to ROUTER_FEW_T tokens the one-launch form is faster (64 tokens 24.0
-// against 26.1 us; 128 tokens 38.0 against 26.7).
+// Measured at 2048 tokens, 4096 x 256, 6 of them: 38 us (13 and 26) against 92 with all logits
+// in fp64 (k_router_logits 85); what bounds it is the vector unit's fp64 work and the chain of
+// choices in k_router_pick. Up to ROUTER_FEW_T tokens the one-launch form is faster (64 tokens
+// 24.0 against 26.1 us; 128 tokens 38.0 against 26.7).
 constexpr int RM_E = 64, RM_T = 64;  // experts and tokens of a tile
 
 __global__ __launch_bounds__(256) void k_router_mm(RouterParams P, int z_count, int z_bytes, int tiles) {
