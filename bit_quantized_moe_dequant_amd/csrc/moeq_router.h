@@ -48,7 +48,8 @@ __device__ __forceinline__ double get_agent(const double* p) {
 }
 
 // The choice of one token's experts by one wave; lane l holds experts l, l + 64, ... P.logits
-// has logits (SCORED: scores, unless the rule is softmax).
+// has logits for a softmax, scores for the other rules (which come with SCORED only: written by
+// other work-groups of this launch).
 template <int N, bool SCORED>
 __device__ __forceinline__ void choose(const RouterParams& P, int t, int lane) {
   const double* z = P.logits + (size_t)t * P.n_experts;
@@ -97,10 +98,6 @@ __device__ __forceinline__ void choose(const RouterParams& P, int t, int lane) {
     for (int i = 0; i < N; i++) s[i] /= sum;
     if (P.bias) keys(s, true);
   } else {
-    if (!SCORED) {
-#pragma unroll
-      for (int i = 0; i < N; i++) s[i] = score_of(P.scoring, s[i]);
-    }
     keys(s, P.bias != nullptr);
   }
   double mine = 0.0, sum = 0.0;

@@ -229,3 +229,39 @@ def test_more_tokens_than_one_launch(kind, norm):
     top = s.gather(1, ids.long())
     top = top / top.sum(dim=1, keepdim=True) if norm else top
     assert bool(((rw.double() - top).abs() <= 2.0 ** -23 * top).all())
+
+
+@pytest.mark.parametrize("norm", [True, False])
+def test_softmax_in_a_graph(norm):
+    """Both forms beyond one launch, captured with a workspace made before and without one, and
+    replayed on new tokens in turn with eager calls."""
+    say("softmax graph", norm)
+    T, H, E, K = 300, 1024, 128, 6
+    x, w, _ = make(T, H, E, 61)
+    r = mq.Router(w, K, scoring="softmax", normalize=norm)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    graphs, outs = [], []
+    with torch.cuda.stream(stream):
+        mq.router_topk(r, x)
+        for ws in (r.workspace(T), None):
+            out = (torch.empty((T, K), dtype=torch.int32, device="cuda"), torch.empty((T, K), device="cuda"))
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=stream):
+                mq.router_topk(r, x, *out, ws=ws)
+            graphs.append(graph)
+            outs.append(out)
+    torch.cuda.synchronize()
+    for rep in range(4):
+        x.copy_(make(T, H, E, 70 + rep)[0])
+        eager = mq.router_topk(r, x)
+        torch.cuda.synchronize()
+        for graph, out in zip(graphs, outs):
+            out[0].fill_(-1)
+            out[1].fill_(float("nan"))
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out[0], eager[0]) and torch.equal(out[1], eager[1])
+    check(*eager, route_ref(host(x), host(w), K, "softmax", norm, 1.0, None))
+    del graphs
