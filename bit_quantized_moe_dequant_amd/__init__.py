@@ -25,9 +25,14 @@ _HEADER = os.path.join(os.path.dirname(_HERE), "include", "moeq.h")
 
 FMT_MXFP4, FMT_NVFP4, FMT_Q2_K, FMT_IQ2_XXS, FMT_FP8_B128 = 1, 2, 3, 4, 5
 FMT_MXFP8, FMT_FP8_B32, FMT_MXFP8_TILED, FMT_INT8 = 6, 7, 8, 9
+FMT_INT4_G32, FMT_INT4_G64, FMT_INT4_G128 = 10, 11, 12     # a scale per group
+FMT_INT4Z_G32, FMT_INT4Z_G64, FMT_INT4Z_G128 = 13, 14, 15  # and a zero point
 FMT_BY_NAME = {"mxfp4": 1, "nvfp4": 2, "q2_k": 3, "iq2_xxs": 4, "fp8_b128": 5, "mxfp8": 6, "fp8_b32": 7,
-               "mxfp8_tiled": 8, "int8": 9}
+               "mxfp8_tiled": 8, "int8": 9, "int4_g32": 10, "int4_g64": 11, "int4_g128": 12, "int4z_g32": 13,
+               "int4z_g64": 14, "int4z_g128": 15}
 OUT_F32, OUT_BF16 = 0, 1
+GROUP_SCORE_BY_NAME = {"top2": 0, "max": 1}
+INT4_FEW_T = 16  # tokens up to which linear_int4 needs no workspace
 SCORE_BY_NAME = {"softmax": 0, "sigmoid": 1, "sqrtsoftplus": 2}
 
 MOEQ_OK = 0
@@ -59,6 +64,10 @@ class MoeqRouter(ctypes.Structure):
     _fields_ = [("hidden", ctypes.c_int), ("n_experts", ctypes.c_int), ("top_k", ctypes.c_int),
                 ("scoring", ctypes.c_int), ("normalize", ctypes.c_int), ("scale", ctypes.c_float),
                 ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class MoeqRouterGroups(ctypes.Structure):
+    _fields_ = [("n_groups", ctypes.c_int), ("top_groups", ctypes.c_int), ("score", ctypes.c_int)]
 
 
 class MoeqShared(ctypes.Structure):
@@ -94,6 +103,11 @@ _SIGS = {
     "moeq_linear_int8": (_i, [ctypes.POINTER(MoeqWeight), _i, _vp, _vp, _i, _vp, _i, _vp, _vp]),
     "moeq_linear_int8_workspace_bytes": (_sz, [_i, _i]),
     "moeq_linear_int8_dynamic": (_i, [ctypes.POINTER(MoeqWeight), _i, _vp, _i, _vp, _i, _vp, _vp, _sz, _vp]),
+    "moeq_pack_int4": (_i, [_i, _vp, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _vp, _vp]),
+    "moeq_linear_int4": (_i, [ctypes.POINTER(MoeqWeight), _i, _vp, _i, _vp, _i, _vp, _vp, _sz, _vp]),
+    "moeq_linear_int4_workspace_bytes": (_sz, [_i, _i]),
+    "moeq_router_topk_groups": (_i, [ctypes.POINTER(MoeqRouter), _vp, _vp, _i, _vp, _vp, _vp, _sz, _vp]),
+    "moeq_moe_forward_groups": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
     "moeq_router_workspace_bytes": (_sz, [ctypes.POINTER(MoeqRouter), _i]),
     "moeq_router_topk": (_i, [ctypes.POINTER(MoeqRouter), _vp, _i, _vp, _vp, _vp, _sz, _vp]),
     "moeq_moe_workspace_bytes": (_sz, [_vp, _vp, _vp, _i]),
@@ -234,7 +248,8 @@ class Weight:
         s0, s1 = _round16(p0), _round16(p1)
         data = torch.empty(s0 * n_experts, dtype=torch.uint8, device=device)
         scales = torch.empty(s1 * n_experts, dtype=torch.uint8, device=device)
-        scale2 = torch.ones(n_experts, dtype=torch.float32, device=device) if fmt == FMT_NVFP4 else None
+        with_scale2 = fmt == FMT_NVFP4 or FMT_INT4_G32 <= fmt <= FMT_INT4Z_G128
+        scale2 = torch.ones(n_experts, dtype=torch.float32, device=device) if with_scale2 else None
         return cls(fmt, rows, cols, n_experts, data, scales, scale2, None, s0, s1)
 
     def expert_planes(self, e):
@@ -635,14 +650,90 @@ def linear_int8_dynamic(w: Weight, x, expert: int = 0, bias=None, y=None, out_dt
     return y
 
 
+def pack_int4(codes, scales, zeros=None, w: Weight = None) -> Weight:
+    """An INT4 weight from row-major tensors on the GPU: codes uint8 [n, rows, cols / 2] (the
+    even column in a byte's low half), scales fp16 or bf16 [n, rows, cols / G] with G 32, 64 or
+    128, and zeros uint8 like scales (without them: 8). Two-dimensional tensors are one expert.
+    w: a Weight of the same format and shape to fill instead of a new one."""
+    torch = _torch()
+    if not isinstance(codes, torch.Tensor) or codes.dim() not in (2, 3):
+        raise ValueError("codes: expected an [n, rows, cols / 2] tensor")
+    if not isinstance(scales, torch.Tensor) or scales.dim() != codes.dim():
+        raise ValueError("scales: expected an [n, rows, cols / G] tensor")
+    n, rows, half = codes.shape if codes.dim() == 3 else (1, *codes.shape)
+    cols, per = 2 * half, scales.shape[-1]
+    group = cols // per if per and cols % per == 0 else 0
+    if group not in (32, 64, 128):
+        raise ValueError(f"scales: {per} to a row of {cols} columns, expected one per 32, 64 or 128")
+    _want("codes", codes, (torch.uint8,), tuple(codes.shape))
+    _want("scales", scales, (torch.float16, torch.bfloat16), (*codes.shape[:-1], per))
+    if zeros is not None:
+        _want("zeros", zeros, (torch.uint8,), tuple(scales.shape))
+    fmt = {32: FMT_INT4_G32, 64: FMT_INT4_G64, 128: FMT_INT4_G128}[group] + (0 if zeros is None else 3)
+    if w is None:
+        w = Weight.empty(fmt, rows, cols, n, codes.device)
+    elif (w.fmt, w.rows, w.cols, w.n_experts) != (fmt, rows, cols, n):
+        raise ValueError(f"w: format {w.fmt}, {w.n_experts} x {w.rows} x {w.cols}, expected {fmt}, {n} x {rows} x {cols}")
+    if w.expert_stride != plane_bytes(fmt, rows, cols, 0) or w.scale_expert_stride != plane_bytes(fmt, rows, cols, 1):
+        raise ValueError("w: experts must lie back to back")
+    _want("w.data", w.data, (torch.uint8,), (n * w.expert_stride,))
+    _want("w.scales", w.scales, (torch.uint8,), (n * w.scale_expert_stride,))
+    _want("w.scale2", w.scale2, (torch.float32,), (n,))
+    dev = _on_device(codes, scales, zeros, w.data, w.scales, w.scale2)
+    _check("moeq_pack_int4", _lib().moeq_pack_int4(
+        fmt, codes.data_ptr(), scales.data_ptr(), 1 if scales.dtype == torch.bfloat16 else 0,
+        None if zeros is None else zeros.data_ptr(), rows, cols, n, w.data.data_ptr(), w.scales.data_ptr(),
+        w.scale2.data_ptr(), _gpu()[1](dev)))
+    return w
+
+
+def linear_int4_workspace(T: int, cols: int, device="cuda"):
+    """A workspace for linear_int4 on up to T tokens."""
+    torch = _torch()
+    n = int(_lib().moeq_linear_int4_workspace_bytes(T, cols))
+    if n == 0:
+        raise MoeqError("moeq_linear_int4_workspace_bytes", -4)
+    ws = torch.empty(n + 256, dtype=torch.uint8, device=device)
+    off = (-ws.data_ptr()) % 256
+    return ws[off:off + n] if off else ws
+
+
+def linear_int4(w: Weight, x, expert: int = 0, bias=None, y=None, out_dtype=None, ws=None):
+    """y [T, rows] = x W^T (+ bias) of bf16 tokens x [T, cols] and an INT4 weight (pack_int4);
+    bf16 unless y or out_dtype says fp32. More than 16 tokens need a workspace: without ws it is
+    allocated for the call from torch's caching allocator (on the current stream, so calls on
+    different streams never share one)."""
+    T = _tokens("x", x, w.cols)
+    gpu = _gpu()
+    _need("x", x, gpu[2], (T, w.cols))
+    y, out = _int8_out(w, T, bias, y, out_dtype, x.device)
+    dev = _on_device(x, bias, y, ws, w.data, w.scales, w.scale2)
+    if T == 0:
+        return y
+    at, n = None, 0
+    if T > INT4_FEW_T:
+        if ws is None:
+            ws = linear_int4_workspace(T, w.cols, x.device)
+        n = ws.numel()
+        _need("ws", ws, gpu[6], (n,))
+        at = ws.data_ptr()
+    _check("moeq_linear_int4", (_LIB or _lib()).moeq_linear_int4(
+        w._ref(), expert, x.data_ptr(), T, None if bias is None else bias.data_ptr(), out, y.data_ptr(), at, n,
+        gpu[1](dev)))
+    return y
+
+
 class Router:
     """Router weights (bf16 [E, H]), an optional fp32 [E] bias for the choice, and the
     rule: scoring "softmax", "sigmoid" or "sqrtsoftplus"; normalize divides the chosen
-    scores by their sum; scale multiplies the route weights. The descriptor is taken when
-    it is made (the tensors' contents are read by every call); make a new one after
-    replacing a tensor."""
+    scores by their sum; scale multiplies the route weights. n_groups > 1: the experts are
+    in groups of equal size, of which a token keeps top_groups before it takes its experts
+    inside them, by the sum of a group's two largest biased scores (group_score "top2") or
+    its largest ("max"). The descriptor is taken when it is made (the tensors' contents are
+    read by every call); make a new one after replacing a tensor."""
 
-    def __init__(self, weight, top_k: int, scoring="softmax", normalize=False, scale=1.0, bias=None):
+    def __init__(self, weight, top_k: int, scoring="softmax", normalize=False, scale=1.0, bias=None, n_groups=1,
+                 top_groups=1, group_score="top2"):
         torch = _torch()
         if weight is None or len(weight.shape) != 2:
             raise ValueError("weight: expected an [E, H] tensor")
@@ -652,6 +743,18 @@ class Router:
             _want("bias", bias, (torch.float32,), (self.n_experts,))
         if scoring not in SCORE_BY_NAME:
             raise ValueError(f"scoring: {scoring!r}, expected one of {', '.join(SCORE_BY_NAME)}")
+        if group_score not in GROUP_SCORE_BY_NAME:
+            raise ValueError(f"group_score: {group_score!r}, expected one of {', '.join(GROUP_SCORE_BY_NAME)}")
+        n_groups, top_groups = int(n_groups), int(top_groups)
+        if not 1 <= n_groups <= 64 or self.n_experts % n_groups:
+            raise ValueError(f"n_groups: {n_groups}, expected a divisor of {self.n_experts} experts, at most 64")
+        if not 1 <= top_groups <= n_groups:
+            raise ValueError(f"top_groups: {top_groups}, expected 1 to {n_groups}")
+        if int(top_k) > self.n_experts // n_groups * top_groups and int(top_k) <= self.n_experts:
+            raise ValueError(f"top_k: {top_k} of the {self.n_experts // n_groups * top_groups} experts of {top_groups} groups")
+        self.n_groups, self.top_groups, self.group_score = n_groups, top_groups, group_score
+        self._groups = MoeqRouterGroups(n_groups, top_groups, GROUP_SCORE_BY_NAME[group_score])
+        self._groups_at = ctypes.addressof(self._groups) if n_groups > 1 else None
         self.weight, self.bias, self.top_k = weight, bias, int(top_k)
         self._keep = (weight, bias)  # what the descriptor points to
         self.scoring, self.normalize, self.scale = scoring, bool(normalize), float(scale)
@@ -768,8 +871,11 @@ def router_topk(router: Router, x, ids=None, rw=None, ws=None):
             ws = router._ws.get(T, x.device, stream)
         n = ws.numel()
         _need("ws", ws, gpu[6], (n,))
-        rc = (_LIB or _lib()).moeq_router_topk(
-            router._by, x.data_ptr(), T, ids.data_ptr(), rw.data_ptr(), ws.data_ptr(), n, stream)
+        lib, at = _LIB or _lib(), (x.data_ptr(), T, ids.data_ptr(), rw.data_ptr(), ws.data_ptr(), n, stream)
+        if router._groups_at is None:
+            rc = lib.moeq_router_topk(router._by, *at)
+        else:
+            rc = lib.moeq_router_topk_groups(router._by, router._groups_at, *at)
     _check("moeq_router_topk", rc)
     return ids, rw
 
@@ -799,8 +905,11 @@ def moe_forward(moe: MoeLayer, x, y=None, ids=None, rw=None, ws=None):
             ws = moe._ws.get(T, x.device, stream)
         n = ws.numel()
         _need("ws", ws, gpu[6], (n,))
-        rc = (_LIB or _lib()).moeq_moe_forward(
-            *moe._refs, x.data_ptr(), T, y.data_ptr(), ids.data_ptr(), rw.data_ptr(), ws.data_ptr(), n, stream)
+        lib, at = _LIB or _lib(), (x.data_ptr(), T, y.data_ptr(), ids.data_ptr(), rw.data_ptr(), ws.data_ptr(), n, stream)
+        if moe.router._groups_at is None:
+            rc = lib.moeq_moe_forward(*moe._refs, *at)
+        else:
+            rc = lib.moeq_moe_forward_groups(moe._refs[0], moe._refs[1], moe.router._groups_at, moe._refs[2], *at)
     _check("moeq_moe_forward", rc)
     return y, ids, rw
 

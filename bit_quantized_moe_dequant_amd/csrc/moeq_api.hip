@@ -5,6 +5,7 @@
 #include <math.h>
 
 #include "moeq.h"
+#include "moeq_int4.h"
 #include "moeq_kernels.h"
 
 #include <cmath>
@@ -31,7 +32,7 @@ int block_k(int fmt) {
     case MOEQ_FMT_MXFP8_TILED: return 512;
     case MOEQ_FMT_INT8: return 16;
   }
-  return 0;
+  return is_int4(fmt) ? int4_group(fmt) : 0;
 }
 
 // Formats for dense linears only (moeq_linear, moeq_linear_int8, moeq_dequant), not for layers.
@@ -60,7 +61,8 @@ size_t plane_bytes(int fmt, int rows, int cols, int plane) {
       return plane == 0 ? n : n / 32;
     case MOEQ_FMT_INT8: return plane == 0 ? n : (size_t)rows * 4;
   }
-  return 0;
+  if (!is_int4(fmt) || rows > INT4_MAX_ROWS || cols > INT4_MAX_COLS) return 0;
+  return plane == 0 ? int4_data_bytes(rows, cols) : int4_scale_bytes(fmt, rows, cols);
 }
 
 WeightRef ref_of(const moeq_weight& w) {
@@ -69,7 +71,7 @@ WeightRef ref_of(const moeq_weight& w) {
   r.scales = (const uint8_t*)w.scales;
   r.estride = w.expert_stride;
   r.sestride = w.scale_expert_stride;
-  r.scale2 = w.fmt == MOEQ_FMT_NVFP4 ? w.scale2 : nullptr;
+  r.scale2 = w.fmt == MOEQ_FMT_NVFP4 || is_int4(w.fmt) ? w.scale2 : nullptr;
   return r;
 }
 
@@ -80,18 +82,20 @@ int check_weight(const moeq_weight* w, bool gemv) {
   if (w->n_experts <= 0) return MOEQ_E_INVAL;
   size_t p0 = plane_bytes(w->fmt, w->rows, w->cols, 0), p1 = plane_bytes(w->fmt, w->rows, w->cols, 1);
   if (p0 == 0 || p1 == 0) return MOEQ_E_SHAPE;
-  if (w->cols % weights_per_chunk(w->fmt)) return MOEQ_E_SHAPE;
-  if (gemv) {
+  const bool int4 = is_int4(w->fmt);
+  if (!int4 && w->cols % weights_per_chunk(w->fmt)) return MOEQ_E_SHAPE;
+  if (gemv && !int4) {
     int lpr, cpl;
     if (!chunk_geometry(w->fmt, w->cols, &lpr, &cpl)) return MOEQ_E_SHAPE;
   }
   if (!w->data || !w->scales) return MOEQ_E_INVAL;
-  if (!aligned(w->data, 16) || !aligned(w->scales, 4)) return MOEQ_E_ALIGN;
+  const size_t scale_align = int4 ? 16 : 4;
+  if (!aligned(w->data, 16) || !aligned(w->scales, scale_align)) return MOEQ_E_ALIGN;
   if (w->n_experts > 1) {
     if (w->expert_stride < p0 || w->scale_expert_stride < p1) return MOEQ_E_INVAL;
-    if (w->expert_stride % 16 || w->scale_expert_stride % 4) return MOEQ_E_ALIGN;
+    if (w->expert_stride % 16 || w->scale_expert_stride % scale_align) return MOEQ_E_ALIGN;
   }
-  if (w->fmt == MOEQ_FMT_NVFP4 && (!w->scale2 || !aligned(w->scale2, 4))) return MOEQ_E_INVAL;
+  if ((w->fmt == MOEQ_FMT_NVFP4 || int4) && (!w->scale2 || !aligned(w->scale2, 4))) return MOEQ_E_INVAL;
   if (w->fmt == MOEQ_FMT_IQ2_XXS && !w->grid) return MOEQ_E_INVAL;
   return MOEQ_OK;
 }
@@ -124,7 +128,7 @@ bool prefill_buffers(const moeq_layer* L, int T) {
 }
 
 struct WsLayout {
-  size_t route, h, partial, xq, xs, hq, hs, dq, ds, total;
+  size_t route, h, partial, xq, xs, hq, hs, dq, ds, h4, total;
   int P;
   uint32_t* err;  // device error word the kernels OR into (null: the workspace's own)
 };
@@ -148,6 +152,11 @@ WsLayout ws_layout(const moeq_layer* L, int T) {
     off += align_up(dn_q2k_g_digit_bytes((long)P, L->inter), 256);
     w.ds = off;
     off += align_up(dn_q2k_g_scale_bytes((long)P, L->inter), 256);
+  }
+  w.h4 = 0;
+  if (is_int4(L->down.fmt)) {  // h as two bf16 terms, when the down projection is given it in fp32
+    w.h4 = off;
+    off += align_up(P * L->inter * 4, 256);
   }
   if (prefill_buffers(L, T)) {
     w.xq = off;
@@ -285,8 +294,13 @@ bool scales16(const moeq_weight& w) {
 #ifndef MOEQ_Q2K_DIRECT_BELOW
 #define MOEQ_Q2K_DIRECT_BELOW 1.06
 #endif
+// INT4: pair by pair up to this many tokens.
+#ifndef MOEQ_INT4_DIRECT_MAX_T
+#define MOEQ_INT4_DIRECT_MAX_T 4
+#endif
 bool gu_direct(const moeq_layer* L, int T) {
   if (T == 1) return true;
+  if (is_int4(L->gate.fmt)) return T >= 1 && T <= MOEQ_INT4_DIRECT_MAX_T;
   if (L->gate.fmt == MOEQ_FMT_IQ2_XXS)  // the dequantize + GEMV over every pair
     return T >= 1 && L->up.fmt == MOEQ_FMT_IQ2_XXS && pairs_per_expert(L, T) < MOEQ_IQ2_DIRECT_BELOW;
   const int max_t = L->gate.fmt == MOEQ_FMT_MXFP4 ? MOEQ_FP4_DIRECT_MAX_T
@@ -298,6 +312,7 @@ bool gu_direct(const moeq_layer* L, int T) {
 bool dn_direct(const moeq_layer* L, int T, const float* h) {
   if (T == 1) return true;
   if (T < 1 || !aligned(h, 16)) return false;
+  if (is_int4(L->down.fmt)) return T <= MOEQ_INT4_DIRECT_MAX_T;
   if (L->down.fmt == MOEQ_FMT_MXFP4)
     return T <= MOEQ_FP4_DIRECT_MAX_T && down1_mx4_fits(L->hidden, L->inter, L->top_k) && scales16(L->down);
   if (L->down.fmt == MOEQ_FMT_Q2_K)
@@ -305,8 +320,64 @@ bool dn_direct(const moeq_layer* L, int T, const float* h) {
   return false;
 }
 
+int route_slots(const moeq_layer* L, int T) {
+  const int pairs = T * L->top_k;
+  return (pairs < L->n_experts ? pairs : L->n_experts) + 1;
+}
+
+Int4Params int4_params(const moeq_weight& w, const void* act, size_t pitch, size_t term, int T, void* y) {
+  Int4Params p;
+  memset(&p, 0, sizeof(p));
+  p.fmt = w.fmt;
+  p.w[0] = p.w[1] = ref_of(w);
+  p.rows = w.rows;
+  p.cols = w.cols;
+  p.act = static_cast<const uint16_t*>(act);
+  p.pitch = pitch;
+  p.term = term;
+  p.T = T;
+  p.top_k = 1;
+  p.n_experts = w.n_experts;
+  p.y = y;
+  return p;
+}
+
+// out_terms: h as two bf16 terms of each value, for run_down_int4, instead of fp32.
+int run_gate_up_int4(const moeq_layer* L, const void* x, const int32_t* ids, int T, void* h, bool out_terms, void* ws,
+                     const WsLayout& lay, hipStream_t s, const LaunchEvents* ev = nullptr) {
+  Int4Params p = int4_params(L->gate, x, L->hidden, 0, T, h);
+  p.w[1] = ref_of(L->up);
+  p.top_k = L->top_k;
+  p.n_experts = L->n_experts;
+  p.grouped = !gu_direct(L, T);
+  p.ids = ids;
+  p.route = route_view(L, ws, lay);
+  p.out_terms = out_terms;
+  p.err = err_of(ws, lay);
+  return hip_rc(launch_int4_few(I4_GATE_UP, p, p.grouped ? route_slots(L, T) : T * L->top_k, s, ev));
+}
+
+// h: two bf16 terms of each value, [pairs][2][inter].
+int run_down_int4(const moeq_layer* L, const uint16_t* h, bool direct, const int32_t* ids, const float* rw, int T, float* y,
+                  void* ws, const WsLayout& lay, hipStream_t s) {
+  float* partial = (float*)((uint8_t*)ws + lay.partial);
+  Int4Params p = int4_params(L->down, h, (size_t)2 * L->inter, L->inter, T, direct ? y : partial);
+  p.top_k = L->top_k;
+  p.n_experts = L->n_experts;
+  p.grouped = !direct;
+  p.ids = ids;
+  p.rw = rw;
+  p.route = route_view(L, ws, lay);
+  p.err = err_of(ws, lay);
+  if (direct) return hip_rc(launch_int4_few(I4_DOWN_SUM, p, T, s));
+  const int rc = hip_rc(launch_int4_few(I4_DOWN_PART, p, route_slots(L, T), s));
+  if (rc) return rc;
+  return hip_rc(launch_combine(partial, T, L->top_k, L->hidden, y, s));
+}
+
 int run_gate_up(const moeq_layer* L, const void* x, const int32_t* ids, int T, float* h, void* ws, const WsLayout& lay,
                 hipStream_t s, const LaunchEvents* ev = nullptr) {
+  if (is_int4(L->gate.fmt)) return run_gate_up_int4(L, x, ids, T, h, false, ws, lay, s, ev);
   GemvParams p = gemv_params(L, L->gate, &L->up, ws, lay);
   p.act = x;
   p.ids = ids;
@@ -348,6 +419,11 @@ Down1Params down1_params(const moeq_layer* L, const float* h, const int32_t* ids
 
 int run_down(const moeq_layer* L, const float* h, const int32_t* ids, const float* rw, int T, float* y, void* ws,
              const WsLayout& lay, hipStream_t s) {
+  if (is_int4(L->down.fmt)) {
+    uint16_t* terms = (uint16_t*)((uint8_t*)ws + lay.h4);
+    const int rc = hip_rc(launch_int4_terms(h, (size_t)T * L->top_k, L->inter, terms, s));
+    return rc ? rc : run_down_int4(L, terms, dn_direct(L, T, h), ids, rw, T, y, ws, lay, s);
+  }
   if (dn_direct(L, T, h)) {
     Down1Params d = down1_params(L, h, ids, rw, T, err_of(ws, lay));
     d.y = y;
@@ -498,6 +574,14 @@ int check_router(const moeq_router* R) {
   return MOEQ_OK;
 }
 
+int check_groups(const moeq_router* R, const moeq_router_groups* G) {
+  if (!G) return MOEQ_OK;
+  if (G->n_groups < 1 || G->top_groups < 1 || G->top_groups > G->n_groups) return MOEQ_E_INVAL;
+  if (G->score != MOEQ_GROUP_TOP2 && G->score != MOEQ_GROUP_MAX) return MOEQ_E_INVAL;
+  if (G->n_groups > 64 || R->n_experts % G->n_groups) return MOEQ_E_SHAPE;
+  return R->top_k > R->n_experts / G->n_groups * G->top_groups ? MOEQ_E_INVAL : MOEQ_OK;
+}
+
 int check_shared(const moeq_layer* L, const moeq_shared* S) {
   if (!S) return MOEQ_OK;
   int rc;
@@ -529,8 +613,8 @@ size_t router_bytes(const moeq_router* R, int T) { return 256 + router_scratch(R
 // The counters of the one-launch router lie in the workspace's header, which the caller
 // has zeroed once; every launch leaves them at zero.
 static_assert(64 + 4 * (ROUTER_FEW_T / 8) <= 256, "the counters fit the header");
-RouterParams router_params(const moeq_router* R, const void* x, int T, int32_t* ids, float* rw, void* ws,
-                           uint8_t* scratch) {
+RouterParams router_params(const moeq_router* R, const moeq_router_groups* G, const void* x, int T, int32_t* ids, float* rw,
+                           void* ws, uint8_t* scratch) {
   RouterParams p;
   memset(&p, 0, sizeof(p));
   p.x = (const uint16_t*)x;
@@ -549,6 +633,12 @@ RouterParams router_params(const moeq_router* R, const void* x, int T, int32_t* 
   p.normalize = R->normalize;
   p.T = T;
   p.scale = R->scale;
+  p.n_groups = p.top_groups = 1;
+  if (G && G->top_groups < G->n_groups) {  // all groups kept: no choice of groups
+    p.n_groups = G->n_groups;
+    p.top_groups = G->top_groups;
+    p.group_top2 = G->score == MOEQ_GROUP_TOP2;
+  }
   return p;
 }
 
@@ -581,8 +671,8 @@ MoeLayout moe_layout(const moeq_layer* L, const moeq_shared* S, int T) {
   return m;
 }
 
-int moe_forward(const moeq_layer* L, const moeq_router* R, const moeq_shared* Sh, const void* x, int T, void* y,
-                int32_t* ids, float* rw, void* ws, hipStream_t s) {
+int moe_forward(const moeq_layer* L, const moeq_router* R, const moeq_router_groups* G, const moeq_shared* Sh, const void* x,
+                int T, void* y, int32_t* ids, float* rw, void* ws, hipStream_t s) {
   const MoeLayout m = moe_layout(L, Sh, T);
   uint8_t* base = (uint8_t*)ws;
   if (!ids) ids = (int32_t*)(base + m.ids);
@@ -593,7 +683,7 @@ int moe_forward(const moeq_layer* L, const moeq_router* R, const moeq_shared* Sh
   float* xs = (float*)(base + m.xs);
   float* hs = (float*)(base + m.hs);
   float* hsh = (float*)(base + m.h);  // the shared expert's h
-  const RouterParams rp = router_params(R, x, T, ids, rw, ws, base + m.logits);
+  const RouterParams rp = router_params(R, G, x, T, ids, rw, ws, base + m.logits);
   Int8Params gu, dn;
   memset(&gu, 0, sizeof(gu));
   memset(&dn, 0, sizeof(dn));
@@ -709,7 +799,7 @@ size_t moeq_plane_bytes(int fmt, int rows, int cols, int plane) { return plane_b
 size_t moeq_packed_bytes(int fmt, int rows, int cols) {
   size_t a = plane_bytes(fmt, rows, cols, 0), b = plane_bytes(fmt, rows, cols, 1);
   if (!a || !b) return 0;
-  return a + b + (fmt == MOEQ_FMT_NVFP4 ? 4 : 0);
+  return a + b + (fmt == MOEQ_FMT_NVFP4 || is_int4(fmt) ? 4 : 0);
 }
 
 int moeq_pack_ggml(int fmt, const void* blocks_host, int rows, int cols, void* data_host, void* scales_host) {
@@ -807,6 +897,7 @@ int moeq_dequant(const moeq_weight* w, int expert, float* out, void* stream) {
     const Int8Params p = int8_params(*w, expert);
     return hip_rc(launch_dequant_int8(p.w, p.ws, w->rows, w->cols, out, S(stream)));
   }
+  if (is_int4(w->fmt)) return hip_rc(launch_dequant_int4(w->fmt, ref_of(*w), w->rows, w->cols, expert, out, S(stream)));
   return hip_rc(launch_dequant(w->fmt, ref_of(*w), w->grid, w->rows, w->cols, expert, out, S(stream)));
 }
 
@@ -910,6 +1001,10 @@ int forward(const moeq_layer* L, const void* x, const int32_t* ids, const float*
   uint8_t* xs = (uint8_t*)ws + lay.xs;
   uint8_t* hq = (uint8_t*)ws + lay.hq;
   uint8_t* hs = (uint8_t*)ws + lay.hs;
+  if (is_int4(L->gate.fmt) && is_int4(L->down.fmt)) {
+    if ((rc = run_gate_up_int4(L, x, ids, T, h, true, ws, lay, s))) return rc;
+    return run_down_int4(L, (const uint16_t*)h, dn_direct(L, T, h), ids, rw, T, y, ws, lay, s);
+  }
   if (gu_pf) {  // W4A8: MXFP8 x; fp32 h too when the down projection needs it
     if ((rc = hip_rc(launch_quant_mxfp8(0, x, T, L->hidden, xq, xs, s)))) return rc;
     if ((rc = run_prefill_gate_up(L, xq, xs, T, dn_pf ? nullptr : h, hq, hs, ws, lay, s))) return rc;
@@ -955,7 +1050,7 @@ int moeq_prefill_down(const moeq_layer* L, const uint8_t* hq, const uint8_t* hs,
 int moeq_linear(const moeq_weight* w, int expert, const void* x, int T, float* y, void* stream) {
   int rc = check_weight(w, false);
   if (rc) return rc;
-  if (w->fmt == MOEQ_FMT_INT8) return MOEQ_E_FMT;  // moeq_linear_int8 takes it
+  if (w->fmt == MOEQ_FMT_INT8 || is_int4(w->fmt)) return MOEQ_E_FMT;  // moeq_linear_int8, moeq_linear_int4 take them
   const bool mx8 = dense_only(w->fmt);
   if (mx8 && !linear_mx8_fits(w->fmt, w->rows, w->cols)) return MOEQ_E_SHAPE;
   const bool mfma = w->fmt == MOEQ_FMT_FP8_B128 && T > 1 && linear_fp8_fits(w->rows, w->cols);
@@ -1076,21 +1171,63 @@ int moeq_linear_int8_dynamic(const moeq_weight* w, int expert, const void* x, in
   return hip_rc(launch_linear_int8(p, S(stream)));
 }
 
+int moeq_pack_int4(int fmt, const void* codes, const void* scales, int scale_type, const uint8_t* zeros, int rows, int cols,
+                   int n, void* data, void* scales_out, float* scale2, void* stream) {
+  if (!is_int4(fmt)) return MOEQ_E_FMT;
+  if (!codes || !scales || !data || !scales_out || !scale2 || n < 0) return MOEQ_E_INVAL;
+  if (scale_type != MOEQ_SCALE_F16 && scale_type != MOEQ_SCALE_BF16) return MOEQ_E_INVAL;
+  if (int4_zeros(fmt) != (zeros != nullptr)) return MOEQ_E_INVAL;
+  if (plane_bytes(fmt, rows, cols, 0) == 0) return MOEQ_E_SHAPE;
+  if (!aligned(scales, 2) || !aligned(data, 16) || !aligned(scales_out, 16) || !aligned(scale2, 4)) return MOEQ_E_ALIGN;
+  if (n == 0) return MOEQ_OK;
+  return hip_rc(launch_pack_int4(fmt, (const uint8_t*)codes, (const uint16_t*)scales, scale_type == MOEQ_SCALE_BF16, zeros, rows,
+                                 cols, n, (uint8_t*)data, (uint8_t*)scales_out, scale2, S(stream)));
+}
+
+int moeq_linear_int4(const moeq_weight* w, int expert, const void* x, int T, const float* bias, int out_type, void* y, void* ws,
+                     size_t ws_bytes, void* stream) {
+  int rc = check_weight(w, false);
+  if (rc) return rc;
+  if (!is_int4(w->fmt)) return MOEQ_E_FMT;
+  if (expert < 0 || expert >= w->n_experts || T < 0 || !x || !y) return MOEQ_E_INVAL;
+  if (out_type != MOEQ_OUT_F32 && out_type != MOEQ_OUT_BF16) return MOEQ_E_INVAL;
+  if (!aligned(x, 16) || !aligned(y, out_type == MOEQ_OUT_BF16 ? 2 : 4) || (bias && !aligned(bias, 4))) return MOEQ_E_ALIGN;
+  if (T > INT4_FEW_T && (!ws || ws_bytes < moeq_linear_int4_workspace_bytes(T, w->cols))) return MOEQ_E_WORKSPACE;
+  if (!aligned(ws, 256)) return MOEQ_E_ALIGN;
+  if (T == 0) return MOEQ_OK;
+  Int4Params p = int4_params(*w, x, w->cols, 0, T, y);
+  p.expert = expert;
+  p.bias = bias;
+  p.out_bf16 = out_type == MOEQ_OUT_BF16;
+  return hip_rc(launch_int4_few(I4_LINEAR, p, 1, S(stream)));
+}
+
+size_t moeq_linear_int4_workspace_bytes(int T, int cols) {
+  if (T < 0 || cols <= 0 || cols % 32 || cols > INT4_MAX_COLS) return 0;
+  if (T <= INT4_FEW_T) return 256;
+  return align_up((size_t)T * 4, 256) + align_up((size_t)T * int4_ktiles(cols) * 256, 256);
+}
+
 size_t moeq_router_workspace_bytes(const moeq_router* R, int T) {
   if (check_router(R) || T < 0) return 0;
   return router_bytes(R, T);
 }
 
-int moeq_router_topk(const moeq_router* R, const void* x, int T, int32_t* ids, float* rw, void* ws, size_t ws_bytes,
-                     void* stream) {
+int moeq_router_topk_groups(const moeq_router* R, const moeq_router_groups* G, const void* x, int T, int32_t* ids, float* rw,
+                            void* ws, size_t ws_bytes, void* stream) {
   int rc = check_router(R);
-  if (rc) return rc;
+  if (rc || (rc = check_groups(R, G))) return rc;
   if (T < 0 || !x || !ids || !rw) return MOEQ_E_INVAL;
   if (!aligned(x, 16) || !aligned(ids, 4) || !aligned(rw, 4)) return MOEQ_E_ALIGN;
   if (!ws || ws_bytes < router_bytes(R, T)) return MOEQ_E_WORKSPACE;
   if (!aligned(ws, 256)) return MOEQ_E_ALIGN;
   if (T == 0) return MOEQ_OK;
-  return hip_rc(launch_router(router_params(R, x, T, ids, rw, ws, (uint8_t*)ws + 256), S(stream)));
+  return hip_rc(launch_router(router_params(R, G, x, T, ids, rw, ws, (uint8_t*)ws + 256), S(stream)));
+}
+
+int moeq_router_topk(const moeq_router* R, const void* x, int T, int32_t* ids, float* rw, void* ws, size_t ws_bytes,
+                     void* stream) {
+  return moeq_router_topk_groups(R, nullptr, x, T, ids, rw, ws, ws_bytes, stream);
 }
 
 size_t moeq_moe_workspace_bytes(const moeq_layer* L, const moeq_router* R, const moeq_shared* Sh, int T) {
@@ -1098,16 +1235,21 @@ size_t moeq_moe_workspace_bytes(const moeq_layer* L, const moeq_router* R, const
   return moe_layout(L, Sh, T).total;
 }
 
-int moeq_moe_forward(const moeq_layer* L, const moeq_router* R, const moeq_shared* Sh, const void* x, int T, void* y,
-                     int32_t* ids, float* rw, void* ws, size_t ws_bytes, void* stream) {
+int moeq_moe_forward_groups(const moeq_layer* L, const moeq_router* R, const moeq_router_groups* G, const moeq_shared* Sh,
+                            const void* x, int T, void* y, int32_t* ids, float* rw, void* ws, size_t ws_bytes, void* stream) {
   int rc = check_moe(L, R, Sh);
-  if (rc) return rc;
+  if (rc || (rc = check_groups(R, G))) return rc;
   if (T < 0 || !x || !y) return MOEQ_E_INVAL;
   if (!aligned(x, 16) || !aligned(y, 16) || (ids && !aligned(ids, 4)) || (rw && !aligned(rw, 4))) return MOEQ_E_ALIGN;
   if (!ws || ws_bytes < moe_layout(L, Sh, T).total) return MOEQ_E_WORKSPACE;
   if (!aligned(ws, 256)) return MOEQ_E_ALIGN;
   if (T == 0) return MOEQ_OK;
-  return moe_forward(L, R, Sh, x, T, y, ids, rw, ws, S(stream));
+  return moe_forward(L, R, G, Sh, x, T, y, ids, rw, ws, S(stream));
+}
+
+int moeq_moe_forward(const moeq_layer* L, const moeq_router* R, const moeq_shared* Sh, const void* x, int T, void* y,
+                     int32_t* ids, float* rw, void* ws, size_t ws_bytes, void* stream) {
+  return moeq_moe_forward_groups(L, R, nullptr, Sh, x, T, y, ids, rw, ws, ws_bytes, stream);
 }
 
 int moeq_check_device_error(void* ws, void* stream, uint32_t* err_host, int clear) {

@@ -109,6 +109,30 @@ struct Mx8Params {
 
 enum { FMT_INT8 = 9 };  // beside the FMT_* of moeq_device.h
 
+constexpr int INT4_FEW_T = 16;  // tokens of the linear that takes no workspace
+
+// Products of INT4 weights (moeq_int4.h) with rows of activations in bf16: tokens, or the
+// intermediate h as two terms (hi + lo) of each value.
+enum { I4_LINEAR = 0, I4_GATE_UP = 1, I4_DOWN_SUM = 2, I4_DOWN_PART = 3 };
+struct Int4Params {
+  int fmt;
+  WeightRef w[2];       // gate and up, or one matrix
+  int rows, cols;       // of the weight
+  const uint16_t* act;  // bf16 rows `pitch` values apart; the second term `term` values behind the first
+  size_t pitch, term;
+  int T, top_k, n_experts;
+  int expert;           // I4_LINEAR: the one tensor
+  bool grouped;         // experts in the order of `route`; else pair by pair (ids)
+  const int32_t* ids;
+  RouteView route;
+  const float* rw;      // route weights [T][top_k]
+  const float* bias;    // I4_LINEAR: [rows] or null
+  void* y;              // linear [T][rows]; gate/up h [pairs][rows]; down [T][rows] or [pairs][rows]
+  bool out_bf16;        // I4_LINEAR: y is bf16
+  bool out_terms;       // I4_GATE_UP: h as two bf16 planes, [pairs][2][rows]
+  uint32_t* err;
+};
+
 // 8-bit integer linear of one expert tensor.
 constexpr int INT8_MAX_COLS = 65536;  // 2^14 per product: the int32 sum stays below 2^31
 constexpr int INT8_MAX_ROWS = 1 << 23;
@@ -146,6 +170,7 @@ struct RouterParams {
   float* rw;          // [T][top_k]
   int hidden, n_experts, top_k, scoring, normalize, T;
   float scale;
+  int n_groups, top_groups, group_top2;  // groups of experts (1: none), those kept, and by what
 };
 
 // Launchers (return hipError_t of the launch).
@@ -239,6 +264,16 @@ hipError_t launch_router(const RouterParams& p, hipStream_t s);
 // y bf16 = x fp32, n values.
 hipError_t launch_to_bf16(const float* x, size_t n, uint16_t* y, hipStream_t s);
 hipError_t launch_dequant_int8(const int8_t* w, const float* ws, int rows, int cols, float* out, hipStream_t s);
+
+// Row-major INT4 codes [rows][cols / 2] (low half first), scales [rows][cols / G] (fp16, or bf16)
+// and zero points (null: 8) of n tensors back to back, to the layout of moeq_int4.h.
+hipError_t launch_pack_int4(int fmt, const uint8_t* codes, const uint16_t* scales, bool scales_bf16, const uint8_t* zeros,
+                            int rows, int cols, int n, uint8_t* data, uint8_t* out_scales, float* scale2, hipStream_t s);
+hipError_t launch_dequant_int4(int fmt, const WeightRef& w, int rows, int cols, int expert, float* out, hipStream_t s);
+// Products for a few rows to an expert (any number is right, in tiles of up to 16 or 8 rows).
+hipError_t launch_int4_few(int kind, const Int4Params& p, int items, hipStream_t s, const LaunchEvents* ev = nullptr);
+// fp32 rows -> their two bf16 terms [n_rows][2][cols].
+hipError_t launch_int4_terms(const float* h, size_t n_rows, int cols, uint16_t* planes, hipStream_t s);
 
 // Chunk geometry: weights per 16-byte chunk; lanes per row and chunks per lane.
 int weights_per_chunk(int fmt);

@@ -17,12 +17,21 @@ namespace {
 
 // The first work-groups are the router's, so that its chain (logits, count, choice) starts
 // with the launch.
-template <int TPW, int CPL>
+template <int TPW, int CPL, bool GROUPS>
 __global__ __launch_bounds__(512) void k_moe_front(RouterParams R, Int8Params G) {
   const int nb = (R.n_experts + RF_EXPERTS - 1) / RF_EXPERTS, nr = nb * ((R.T + RF_TOK - 1) / RF_TOK);
   const int b = blockIdx.x;
-  if (b < nr) router_few(R, b % nb, b / nb);
+  if (b < nr) router_few<GROUPS>(R, b % nb, b / nb);
   else int8_few<2, TPW, CPL, 8, 0>(G, b - nr);
+}
+
+template <bool GROUPS>
+void moe_front(const FewPlan& f, dim3 g, dim3 b, const RouterParams& r, const Int8Params& p, hipStream_t s) {
+  if (f.tpw == 1 && f.cpl <= 1) hipLaunchKernelGGL((k_moe_front<1, 1, GROUPS>), g, b, 0, s, r, p);
+  else if (f.tpw == 1 && f.cpl <= 4) hipLaunchKernelGGL((k_moe_front<1, 4, GROUPS>), g, b, 0, s, r, p);
+  else if (f.tpw == 1) hipLaunchKernelGGL((k_moe_front<1, 16, GROUPS>), g, b, 0, s, r, p);
+  else if (f.cpl <= 2) hipLaunchKernelGGL((k_moe_front<2, 2, GROUPS>), g, b, 0, s, r, p);
+  else hipLaunchKernelGGL((k_moe_front<2, 8, GROUPS>), g, b, 0, s, r, p);
 }
 
 }  // namespace
@@ -36,11 +45,8 @@ hipError_t launch_moe_front(const RouterParams& r, const Int8Params& g0, hipStre
   p.wpt = f.wpt;
   const int nb = (r.n_experts + RF_EXPERTS - 1) / RF_EXPERTS * ((r.T + RF_TOK - 1) / RF_TOK);
   const dim3 g((unsigned)(nb + (p.rows + 15) / 16)), b(512);
-  if (f.tpw == 1 && f.cpl <= 1) hipLaunchKernelGGL((k_moe_front<1, 1>), g, b, 0, s, r, p);
-  else if (f.tpw == 1 && f.cpl <= 4) hipLaunchKernelGGL((k_moe_front<1, 4>), g, b, 0, s, r, p);
-  else if (f.tpw == 1) hipLaunchKernelGGL((k_moe_front<1, 16>), g, b, 0, s, r, p);
-  else if (f.cpl <= 2) hipLaunchKernelGGL((k_moe_front<2, 2>), g, b, 0, s, r, p);
-  else hipLaunchKernelGGL((k_moe_front<2, 8>), g, b, 0, s, r, p);
+  if (r.n_groups > 1) moe_front<true>(f, g, b, r, p, s);
+  else moe_front<false>(f, g, b, r, p, s);
   return hipGetLastError();
 }
 

@@ -47,10 +47,44 @@ __device__ __forceinline__ double get_agent(const double* p) {
   return __builtin_bit_cast(double, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
 }
 
+// A number as an unsigned integer of the same order; a NaN counts as -inf, -0 as 0.
+__device__ __forceinline__ uint64_t order_of(double k) {
+  k = k == k ? k + 0.0 : -__builtin_inf();
+  const uint64_t b = __builtin_bit_cast(uint64_t, k);
+  return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+}
+
+// Lanes to a group of experts: the largest power of two that leaves every group its own.
+__device__ __forceinline__ int group_lanes(int n_groups) { return 1 << (31 - __builtin_clz(64 / n_groups)); }
+
+// Which groups of experts a wave's token keeps. Lanes gl q .. gl q + gl - 1 (gl =
+// group_lanes()) hold the two largest biased scores of their parts of group q, a NaN as
+// -inf; the result's bit gl q is set where q is kept. Groups past the last take part with
+// lanes of their own that hold -inf and are never counted.
+__device__ __forceinline__ uint64_t keep_groups(double a, double b, int n_groups, int top_groups, bool top2, int lane) {
+  const int gl = group_lanes(n_groups);
+  for (int o = 1; o < gl; o <<= 1) {
+    const double c = __shfl_xor(a, o, 64), d = __shfl_xor(b, o, 64);
+    const double low = a < c ? a : c;
+    a = a > c ? a : c;
+    b = b > d ? b : d;
+    b = b > low ? b : low;
+  }
+  const uint64_t mine = order_of(top2 && b > -__builtin_inf() ? a + b : top2 ? -__builtin_inf() : a);
+  const int q = lane / gl;
+  int rank = 0;
+  for (int o = 0; o < n_groups; o++) {
+    const uint64_t v = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)mine, o * gl) |
+                       ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(mine >> 32), o * gl) << 32);
+    rank += v > mine || (v == mine && o < q);
+  }
+  return __ballot(q < n_groups && lane % gl == 0 && rank < top_groups);
+}
+
 // The choice of one token's experts by one wave; lane l holds experts l, l + 64, ... P.logits
-// has logits for a softmax, scores for the other rules (which come with SCORED only: written by
-// other work-groups of this launch).
-template <int N, bool SCORED>
+// has logits for a softmax, scores for the other rules (SCORED: written by other work-groups of
+// this launch). GROUPS: inside the best groups of experts only.
+template <int N, bool SCORED, bool GROUPS = false>
 __device__ __forceinline__ void choose(const RouterParams& P, int t, int lane) {
   const double* z = P.logits + (size_t)t * P.n_experts;
   double s[N];
@@ -77,9 +111,9 @@ __device__ __forceinline__ void choose(const RouterParams& P, int t, int lane) {
       lo[i] = (uint32_t)b;
     }
   };
+  double m = -__builtin_inf(), denom = 1.0;
   if (P.scoring == SCORE_SOFTMAX) {
     if (!P.bias) keys(s, false);
-    double m = -__builtin_inf();
 #pragma unroll
     for (int i = 0; i < N; i++) m = s[i] > m ? s[i] : m;
 #pragma unroll
@@ -93,12 +127,32 @@ __device__ __forceinline__ void choose(const RouterParams& P, int t, int lane) {
       s[i] = lane + 64 * i < P.n_experts ? exp(s[i] - m) : 0.0;
       sum += s[i];
     }
-    sum = wave_sum(sum);
+    denom = wave_sum(sum);
 #pragma unroll
-    for (int i = 0; i < N; i++) s[i] /= sum;
+    for (int i = 0; i < N; i++) s[i] /= denom;
     if (P.bias) keys(s, true);
   } else {
     keys(s, P.bias != nullptr);
+  }
+  if constexpr (GROUPS) {
+    // The scores once more, group by group: a group's experts do not lie in one lane's registers.
+    const int size = P.n_experts / P.n_groups, gl = group_lanes(P.n_groups), q = lane / gl;
+    double a = -__builtin_inf(), b = -__builtin_inf();
+    if (q < P.n_groups)
+      for (int i = lane % gl; i < size; i += gl) {
+        const int e = q * size + i;
+        double v = SCORED ? get_agent(z + e) : z[e];
+        if (P.scoring == SCORE_SOFTMAX) v = exp(v - m) / denom;
+        if (P.bias) v += (double)P.bias[e];
+        v = v == v ? v : -__builtin_inf();
+        const double low = a < v ? a : v;
+        a = a > v ? a : v;
+        b = b > low ? b : low;
+      }
+    const uint64_t kept = keep_groups(a, b, P.n_groups, P.top_groups, P.group_top2 && size > 1, lane);
+#pragma unroll
+    for (int i = 0; i < N; i++)
+      if (!(kept >> ((lane + 64 * i) / size * gl & 63) & 1)) hi[i] = lo[i] = 0;
   }
   double mine = 0.0, sum = 0.0;
   for (int k = 0; k < P.top_k; k++) {
@@ -152,6 +206,7 @@ __device__ __forceinline__ void choose(const RouterParams& P, int t, int lane) {
 // into scores and counts itself in; the last to arrive for the tokens makes their choice.
 constexpr int RF_EXPERTS = 4, RF_TOK = 8, RF_DEPTH = 4;
 
+template <bool GROUPS>
 __device__ __forceinline__ void router_few(const RouterParams& P, int block, int group) {
   __shared__ double part[8][RF_TOK];
   __shared__ int is_last;
@@ -217,9 +272,9 @@ __device__ __forceinline__ void router_few(const RouterParams& P, int block, int
   }
   __syncthreads();
   if (is_last && wave < tn) {
-    if (P.n_experts <= 256) choose<4, true>(P, t0 + wave, lane);
-    else if (P.n_experts <= 512) choose<8, true>(P, t0 + wave, lane);
-    else choose<16, true>(P, t0 + wave, lane);
+    if (P.n_experts <= 256) choose<4, true, GROUPS>(P, t0 + wave, lane);
+    else if (P.n_experts <= 512) choose<8, true, GROUPS>(P, t0 + wave, lane);
+    else choose<16, true, GROUPS>(P, t0 + wave, lane);
   }
 }
 

@@ -19,7 +19,10 @@ namespace moeq {
 
 namespace {
 
-__global__ __launch_bounds__(512) void k_router_few(RouterParams P) { router_few(P, blockIdx.x, blockIdx.y); }
+template <bool GROUPS>
+__global__ __launch_bounds__(512) void k_router_few(RouterParams P) {
+  router_few<GROUPS>(P, blockIdx.x, blockIdx.y);
+}
 
 // All logits in fp64, on the fp64 matrix instruction, whose operands are converted once for
 // sixteen rows: v_mfma_f64_16x16x4, lane l: operand A's row l % 16 and B's row l % 16 at
@@ -68,17 +71,18 @@ __global__ __launch_bounds__(64 * RL_WAVES) void k_router_logits(RouterParams P)
     double z = part[0][tk][threadIdx.x & 15];
 #pragma unroll
     for (int v = 1; v < RL_WAVES; v++) z += part[v][tk][threadIdx.x & 15];
-    P.logits[(size_t)(t0 + tk) * P.n_experts + e] = z;
+    P.logits[(size_t)(t0 + tk) * P.n_experts + e] = P.scoring == SCORE_SOFTMAX ? z : score_of(P.scoring, z);
   }
 }
 
+template <bool GROUPS>
 __global__ __launch_bounds__(256) void k_router_choose(RouterParams P) {
   const int lane = threadIdx.x & 63;
   const int t = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (t >= P.T) return;
-  if (P.n_experts <= 256) choose<4, false>(P, t, lane);
-  else if (P.n_experts <= 512) choose<8, false>(P, t, lane);
-  else choose<16, false>(P, t, lane);
+  if (P.n_experts <= 256) choose<4, false, GROUPS>(P, t, lane);
+  else if (P.n_experts <= 512) choose<8, false, GROUPS>(P, t, lane);
+  else choose<16, false, GROUPS>(P, t, lane);
 }
 
 // ---------------------------------------------------------------- many tokens
@@ -154,13 +158,6 @@ __global__ __launch_bounds__(256) void k_router_mm(RouterParams P, int z_count, 
       if (e < P.n_experts) out[e] = (float)sum[r];
     }
   }
-}
-
-// A number as an unsigned integer of the same order; a NaN counts as -inf, -0 as 0.
-__device__ __forceinline__ uint64_t order_of(double k) {
-  k = k == k ? k + 0.0 : -__builtin_inf();
-  const uint64_t b = __builtin_bit_cast(uint64_t, k);
-  return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
 }
 
 // A number not below the score of any logit that is not above v, from the fast fp32
@@ -429,15 +426,19 @@ hipError_t launch_router(const RouterParams& p, hipStream_t s) {
   if (p.T < 1 || p.n_experts < 1 || p.n_experts > 1024 || p.top_k < 1 || p.top_k > 16 || p.top_k > p.n_experts ||
       p.hidden < 8 || p.hidden % 8)
     return hipErrorInvalidValue;
+  const bool groups = p.n_groups > 1;
+  if (groups && (p.n_groups > 64 || p.n_experts % p.n_groups || p.top_groups < 1 || p.top_groups > p.n_groups))
+    return hipErrorInvalidValue;
   if (router_few_fits(p.T)) {
     const dim3 g((unsigned)((p.n_experts + RF_EXPERTS - 1) / RF_EXPERTS), (unsigned)((p.T + RF_TOK - 1) / RF_TOK));
-    hipLaunchKernelGGL(k_router_few, g, dim3(512), 0, s, p);
+    if (groups) hipLaunchKernelGGL(k_router_few<true>, g, dim3(512), 0, s, p);
+    else hipLaunchKernelGGL(k_router_few<false>, g, dim3(512), 0, s, p);
     return hipGetLastError();
   }
   // The denominator of a softmax takes all logits, and fp32 ones would be off by up to
   // 274 x 2^-23 |W_e| |x| each. It cancels where the K weights are normalised, unless a bias makes
   // the choice depend on it.
-  if (p.scoring != SCORE_SOFTMAX || (p.normalize && !p.bias)) {
+  if (!groups && (p.scoring != SCORE_SOFTMAX || (p.normalize && !p.bias))) {
     for (long t0 = 0; t0 < p.T; t0 += ROUTER_TOKENS) {
       RouterParams q = p;
       q.T = (int)(p.T - t0 < ROUTER_TOKENS ? p.T - t0 : ROUTER_TOKENS);
@@ -464,7 +465,9 @@ hipError_t launch_router(const RouterParams& p, hipStream_t s) {
     q.rw += (size_t)t0 * p.top_k;
     const dim3 g((unsigned)((p.n_experts + 15) / 16), (unsigned)((q.T + 15) / 16));
     hipLaunchKernelGGL(k_router_logits, g, dim3(64 * RL_WAVES), 0, s, q);
-    hipLaunchKernelGGL(k_router_choose, dim3((unsigned)((q.T + 3) / 4)), dim3(256), 0, s, q);
+    const dim3 c((unsigned)((q.T + 3) / 4));
+    if (groups) hipLaunchKernelGGL(k_router_choose<true>, c, dim3(256), 0, s, q);
+    else hipLaunchKernelGGL(k_router_choose<false>, c, dim3(256), 0, s, q);
   }
   return hipGetLastError();
 }

@@ -94,6 +94,19 @@ extern "C" {
  *   of moeq_moe_forward only (elsewhere MOEQ_E_FMT). data: i8 [rows][cols], cols a
  *   multiple of 16; scales: fp32 [rows]; weight = code * scale (codes -128..127).
  *
+ * MOEQ_FMT_INT4_G32 / _G64 / _G128 - 4-bit integers with a scale per group of 32, 64 or
+ *   128 along cols: weight = scale2 * s * (q - 8), q 0..15. MOEQ_FMT_INT4Z_*: with a zero
+ *   point per group, weight = scale2 * s * (q - z), z 0..255. For layers, moeq_linear_int4
+ *   and moeq_dequant. Any rows (up to 2^23); cols a multiple of the group (up to 2^20).
+ *   Made by moeq_pack_int4 from row-major codes, in the order of the matrix instruction's
+ *   operand, in tiles of 16 rows x 128 cols; rows and cols past the end are padding with
+ *   scale 0. tile = (r/16) * ceil(cols/128) + c/128.
+ *   data: 1024 bytes at tile * 1024; lane n + 16g of the tile holds row n in four words
+ *   j = 0..3 at 16 (n + 16g) + 4j: cols 32j + 8g + 0..7 of the tile, col 2p in bits 4p of
+ *   the word, col 2p + 1 in bits 16 + 4p.
+ *   scales: fp16 [tile][16][128/G]; then, for INT4Z, the zero points u8 [tile][16][128/G].
+ *   16-byte aligned, as is scale_expert_stride. scale2: fp32 [n_experts], a power of two.
+ *
  * Dense-linear formats (moeq_linear and moeq_dequant only; a layer using one is
  * refused with MOEQ_E_FMT):
  * MOEQ_FMT_FP8_B32 - E4M3 weights with one UE8M0 scale per 32x32 tile, the dense
@@ -123,6 +136,12 @@ extern "C" {
 #define MOEQ_FMT_FP8_B32 7
 #define MOEQ_FMT_MXFP8_TILED 8
 #define MOEQ_FMT_INT8 9
+#define MOEQ_FMT_INT4_G32 10
+#define MOEQ_FMT_INT4_G64 11
+#define MOEQ_FMT_INT4_G128 12
+#define MOEQ_FMT_INT4Z_G32 13
+#define MOEQ_FMT_INT4Z_G64 14
+#define MOEQ_FMT_INT4Z_G128 15
 
 /* Types of the outputs that come in more than one. */
 #define MOEQ_OUT_F32 0
@@ -153,7 +172,7 @@ typedef struct moeq_weight {
   size_t expert_stride;       /* bytes between experts in data, multiple of 16 */
   const void* scales;         /* 4-byte aligned */
   size_t scale_expert_stride; /* bytes between experts in scales, multiple of 4 */
-  const float* scale2;        /* NVFP4: fp32 [n_experts]; else ignored */
+  const float* scale2;        /* NVFP4, INT4: fp32 [n_experts]; else ignored */
   const uint8_t* grid;        /* IQ2_XXS: u8 [256][8]; else ignored */
 } moeq_weight;
 
@@ -171,10 +190,11 @@ const char* moeq_status_string(int status);
 
 /* Bytes of plane 0 (data) or plane 1 (scales) of one expert tensor [rows, cols];
  * 0 for an invalid format, plane or shape. cols must be a multiple of the format's
- * block: 32 MXFP4, 16 NVFP4, 256 Q2_K and IQ2_XXS, 128 FP8_B128 (rows too), 16 INT8. */
+ * block: 32 MXFP4, 16 NVFP4, 256 Q2_K and IQ2_XXS, 128 FP8_B128 (rows too), 16 INT8, the
+ * group of INT4. */
 size_t moeq_plane_bytes(int fmt, int rows, int cols, int plane);
 
-/* Total bytes of one expert tensor, both planes plus NVFP4's 4-byte scale_2. The
+/* Total bytes of one expert tensor, both planes plus NVFP4's and INT4's 4-byte scale2. The
  * algorithmic bytes per weight equal the format's bits per weight / 8. */
 size_t moeq_packed_bytes(int fmt, int rows, int cols);
 
@@ -357,6 +377,36 @@ size_t moeq_linear_int8_workspace_bytes(int T, int cols);
 int moeq_linear_int8_dynamic(const moeq_weight* w, int expert, const void* x, int T, const float* bias, int out_type,
                              void* y, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------ 4-bit integers */
+
+/* Types of the scales that moeq_pack_int4 takes. */
+#define MOEQ_SCALE_F16 0
+#define MOEQ_SCALE_BF16 1
+
+/* Row-major INT4 tensors to the planes of MOEQ_FMT_INT4*, for n tensors back to back in
+ * device memory: codes u8 [n][rows][cols/2] (the even column in the low half of its byte),
+ * scales [n][rows][cols/G] fp16 or bf16 (any sign), zeros u8 [n][rows][cols/G] for the
+ * formats with zero points and NULL for the others. data, scales_out (moeq_plane_bytes
+ * apart) and scale2 fp32 [n] are overwritten. scale2 is the power of two that brings the
+ * tensor's largest finite |scale| into [64, 128); stored scales are exact unless they are
+ * below 2^-20 of the largest, where they are rounded to 2^-31 of it. Infinite and NaN
+ * scales stay what they are. data and scales_out 16-byte aligned; outputs must not overlap
+ * inputs. Asynchronous on `stream`; n == 0 is a no-op. */
+int moeq_pack_int4(int fmt, const void* codes, const void* scales, int scale_type, const uint8_t* zeros, int rows, int cols,
+                   int n, void* data, void* scales_out, float* scale2, void* stream);
+
+/* y[t][r] = sum_k W[r][k] x[t][k] (+ bias[r]) for expert `expert` of an INT4 weight. Products
+ * are exact, sums are fp32 with the scales applied to them, one rounding to the output type.
+ * x bf16 [T][cols], 16-byte aligned; bias fp32 [rows] or NULL; y [T][rows] overwritten, fp32
+ * or bf16 (MOEQ_OUT_*), aligned to its element. A token that holds an infinity or a NaN
+ * gives NaN, and nobody else's outputs change. Sums over a group have to stay inside fp32's
+ * range, which |x| < 2^112 ensures. ws: moeq_linear_int4_workspace_bytes(T, cols) bytes,
+ * 256-byte aligned, contents arbitrary, not shared with an overlapping call; NULL for up to
+ * 16 tokens. Any T; T == 0 is a no-op. */
+size_t moeq_linear_int4_workspace_bytes(int T, int cols);
+int moeq_linear_int4(const moeq_weight* w, int expert, const void* x, int T, const float* bias, int out_type, void* y, void* ws,
+                     size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ router, whole layer */
 
 /* Scores s of the logits z: softmax over the experts, 1 / (1 + e^-z), or
@@ -399,6 +449,24 @@ size_t moeq_router_workspace_bytes(const moeq_router* R, int T);
 int moeq_router_topk(const moeq_router* R, const void* x, int T, int32_t* ids, float* rw, void* ws, size_t ws_bytes,
                      void* stream);
 
+/* The same with the experts in n_groups groups of equal size (experts e of group
+ * e / (n_experts / n_groups)), of which every token takes top_groups before it takes its
+ * experts inside them. A group's merit is the sum of its two largest s + bias (one, if it
+ * has one expert) or its largest, in fp64; ties go to the lower group; a NaN counts as
+ * minus infinity. Softmax scores count with their denominators over all experts, so do
+ * route weights. n_groups at most 64, a divisor of n_experts; top_k at most the experts of
+ * top_groups groups. G == NULL, n_groups == 1 or top_groups == n_groups:
+ * moeq_router_topk. Same workspace. */
+#define MOEQ_GROUP_TOP2 0
+#define MOEQ_GROUP_MAX 1
+typedef struct moeq_router_groups {
+  int n_groups;
+  int top_groups;
+  int score; /* MOEQ_GROUP_* */
+} moeq_router_groups;
+int moeq_router_topk_groups(const moeq_router* R, const moeq_router_groups* G, const void* x, int T, int32_t* ids, float* rw,
+                            void* ws, size_t ws_bytes, void* stream);
+
 /* The whole layer for x[T][H] (bf16): y = bf16(routed + shared), with the routed
  * experts of moeq_router_topk as moeq_expert_forward computes them (so from 128 tokens
  * on an MXFP4 projection takes its activations as MXFP8, which moves the routed part by
@@ -414,6 +482,10 @@ int moeq_router_topk(const moeq_router* R, const void* x, int T, int32_t* ids, f
 size_t moeq_moe_workspace_bytes(const moeq_layer* L, const moeq_router* R, const moeq_shared* S, int T);
 int moeq_moe_forward(const moeq_layer* L, const moeq_router* R, const moeq_shared* S, const void* x, int T, void* y,
                      int32_t* ids, float* rw, void* ws, size_t ws_bytes, void* stream);
+
+/* moeq_moe_forward with the router of moeq_router_topk_groups. Same workspace. */
+int moeq_moe_forward_groups(const moeq_layer* L, const moeq_router* R, const moeq_router_groups* G, const moeq_shared* S,
+                            const void* x, int T, void* y, int32_t* ids, float* rw, void* ws, size_t ws_bytes, void* stream);
 
 /* Synchronise `stream`, then read (and with clear != 0, zero) the device error word. */
 int moeq_check_device_error(void* ws, void* stream, uint32_t* err_host, int clear);
