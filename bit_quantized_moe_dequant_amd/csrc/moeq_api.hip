@@ -127,8 +127,18 @@ bool prefill_buffers(const moeq_layer* L, int T) {
   return T >= PREFILL_MIN_T && (L->gate.fmt == MOEQ_FMT_MXFP4 || L->down.fmt == MOEQ_FMT_MXFP4);
 }
 
+// INT4: from this many pairs per expert on (and while 32-bit offsets reach every row) as a
+// tiled product over each expert's tokens.
+#ifndef MOEQ_INT4_TILED_FROM
+#define MOEQ_INT4_TILED_FROM 8.0
+#endif
+bool int4_many(const moeq_layer* L, int T) {
+  const size_t P = (size_t)T * L->top_k;
+  return T > 1 && P >= MOEQ_INT4_TILED_FROM * L->n_experts && int4_rows_fit(T, 1, L->hidden) && int4_rows_fit(P, 2, L->inter);
+}
+
 struct WsLayout {
-  size_t route, h, partial, xq, xs, hq, hs, dq, ds, h4, total;
+  size_t route, h, partial, xq, xs, hq, hs, dq, ds, h4, xr, xrs, hr, hrs, total;
   int P;
   uint32_t* err;  // device error word the kernels OR into (null: the workspace's own)
 };
@@ -153,10 +163,22 @@ WsLayout ws_layout(const moeq_layer* L, int T) {
     w.ds = off;
     off += align_up(dn_q2k_g_scale_bytes((long)P, L->inter), 256);
   }
-  w.h4 = 0;
-  if (is_int4(L->down.fmt)) {  // h as two bf16 terms, when the down projection is given it in fp32
+  w.h4 = w.xr = w.xrs = w.hr = w.hrs = 0;
+  const bool many = int4_many(L, T);
+  if (is_int4(L->gate.fmt) && many) {  // the tokens' fp16 rows and their scales
+    w.xr = off;
+    off += align_up(int4_rows_bytes(T, 1, L->hidden), 256);
+    w.xrs = off;
+    off += align_up((size_t)T * 4, 256);
+  }
+  if (is_int4(L->down.fmt) && many) {  // and those of h
+    w.hr = off;
+    off += align_up(int4_rows_bytes(P, 2, L->inter), 256);
+    w.hrs = off;
+    off += align_up(P * 4, 256);
+  } else if (is_int4(L->down.fmt)) {  // h as three bf16 terms
     w.h4 = off;
-    off += align_up(P * L->inter * 4, 256);
+    off += align_up(P * L->inter * 6, 256);
   }
   if (prefill_buffers(L, T)) {
     w.xq = off;
@@ -300,7 +322,7 @@ bool scales16(const moeq_weight& w) {
 #endif
 bool gu_direct(const moeq_layer* L, int T) {
   if (T == 1) return true;
-  if (is_int4(L->gate.fmt)) return T >= 1 && T <= MOEQ_INT4_DIRECT_MAX_T;
+  if (is_int4(L->gate.fmt)) return T >= 1 && T <= MOEQ_INT4_DIRECT_MAX_T && !int4_many(L, T);
   if (L->gate.fmt == MOEQ_FMT_IQ2_XXS)  // the dequantize + GEMV over every pair
     return T >= 1 && L->up.fmt == MOEQ_FMT_IQ2_XXS && pairs_per_expert(L, T) < MOEQ_IQ2_DIRECT_BELOW;
   const int max_t = L->gate.fmt == MOEQ_FMT_MXFP4 ? MOEQ_FP4_DIRECT_MAX_T
@@ -312,7 +334,7 @@ bool gu_direct(const moeq_layer* L, int T) {
 bool dn_direct(const moeq_layer* L, int T, const float* h) {
   if (T == 1) return true;
   if (T < 1 || !aligned(h, 16)) return false;
-  if (is_int4(L->down.fmt)) return T <= MOEQ_INT4_DIRECT_MAX_T;
+  if (is_int4(L->down.fmt)) return T <= MOEQ_INT4_DIRECT_MAX_T && !int4_many(L, T);
   if (L->down.fmt == MOEQ_FMT_MXFP4)
     return T <= MOEQ_FP4_DIRECT_MAX_T && down1_mx4_fits(L->hidden, L->inter, L->top_k) && scales16(L->down);
   if (L->down.fmt == MOEQ_FMT_Q2_K)
@@ -342,9 +364,35 @@ Int4Params int4_params(const moeq_weight& w, const void* act, size_t pitch, size
   return p;
 }
 
-// out_terms: h as two bf16 terms of each value, for run_down_int4, instead of fp32.
+Int4Rows int4_rows(const moeq_weight& w, const moeq_layer* L, int T, const uint16_t* act, const float* scale, void* y) {
+  Int4Rows p;
+  memset(&p, 0, sizeof(p));
+  p.fmt = w.fmt;
+  p.w[0] = p.w[1] = ref_of(w);
+  p.rows = w.rows;
+  p.cols = w.cols;
+  p.act = act;
+  p.act_scale = scale;
+  p.T = T;
+  p.top_k = L ? L->top_k : 1;
+  p.n_experts = L ? L->n_experts : w.n_experts;
+  p.y = y;
+  return p;
+}
+
+// out_terms: h as bf16 terms, for run_down_int4, instead of fp32.
 int run_gate_up_int4(const moeq_layer* L, const void* x, const int32_t* ids, int T, void* h, bool out_terms, void* ws,
                      const WsLayout& lay, hipStream_t s, const LaunchEvents* ev = nullptr) {
+  if (lay.xr) {
+    uint16_t* xr = (uint16_t*)((uint8_t*)ws + lay.xr);
+    float* xrs = (float*)((uint8_t*)ws + lay.xrs);
+    const int rc = hip_rc(launch_int4_rows(false, x, T, L->hidden, xr, xrs, s));
+    if (rc) return rc;
+    Int4Rows p = int4_rows(L->gate, L, T, xr, xrs, h);
+    p.w[1] = ref_of(L->up);
+    p.route = route_view(L, ws, lay);
+    return hip_rc(launch_int4_tiled(I4_GATE_UP, p, s));
+  }
   Int4Params p = int4_params(L->gate, x, L->hidden, 0, T, h);
   p.w[1] = ref_of(L->up);
   p.top_k = L->top_k;
@@ -357,11 +405,11 @@ int run_gate_up_int4(const moeq_layer* L, const void* x, const int32_t* ids, int
   return hip_rc(launch_int4_few(I4_GATE_UP, p, p.grouped ? route_slots(L, T) : T * L->top_k, s, ev));
 }
 
-// h: two bf16 terms of each value, [pairs][2][inter].
+// h: bf16 terms, [pairs][3][inter].
 int run_down_int4(const moeq_layer* L, const uint16_t* h, bool direct, const int32_t* ids, const float* rw, int T, float* y,
                   void* ws, const WsLayout& lay, hipStream_t s) {
   float* partial = (float*)((uint8_t*)ws + lay.partial);
-  Int4Params p = int4_params(L->down, h, (size_t)2 * L->inter, L->inter, T, direct ? y : partial);
+  Int4Params p = int4_params(L->down, h, (size_t)3 * L->inter, L->inter, T, direct ? y : partial);
   p.top_k = L->top_k;
   p.n_experts = L->n_experts;
   p.grouped = !direct;
@@ -419,6 +467,18 @@ Down1Params down1_params(const moeq_layer* L, const float* h, const int32_t* ids
 
 int run_down(const moeq_layer* L, const float* h, const int32_t* ids, const float* rw, int T, float* y, void* ws,
              const WsLayout& lay, hipStream_t s) {
+  if (is_int4(L->down.fmt) && lay.hr) {
+    uint16_t* hr = (uint16_t*)((uint8_t*)ws + lay.hr);
+    float* hrs = (float*)((uint8_t*)ws + lay.hrs);
+    float* partial = (float*)((uint8_t*)ws + lay.partial);
+    int rc = hip_rc(launch_int4_rows(true, h, (size_t)T * L->top_k, L->inter, hr, hrs, s));
+    if (rc) return rc;
+    Int4Rows p = int4_rows(L->down, L, T, hr, hrs, partial);
+    p.route = route_view(L, ws, lay);
+    p.rw = rw;
+    if ((rc = hip_rc(launch_int4_tiled(I4_DOWN_PART, p, s)))) return rc;
+    return hip_rc(launch_combine(partial, T, L->top_k, L->hidden, y, s));
+  }
   if (is_int4(L->down.fmt)) {
     uint16_t* terms = (uint16_t*)((uint8_t*)ws + lay.h4);
     const int rc = hip_rc(launch_int4_terms(h, (size_t)T * L->top_k, L->inter, terms, s));
@@ -1001,9 +1061,10 @@ int forward(const moeq_layer* L, const void* x, const int32_t* ids, const float*
   uint8_t* xs = (uint8_t*)ws + lay.xs;
   uint8_t* hq = (uint8_t*)ws + lay.hq;
   uint8_t* hs = (uint8_t*)ws + lay.hs;
-  if (is_int4(L->gate.fmt) && is_int4(L->down.fmt)) {
-    if ((rc = run_gate_up_int4(L, x, ids, T, h, true, ws, lay, s))) return rc;
-    return run_down_int4(L, (const uint16_t*)h, dn_direct(L, T, h), ids, rw, T, y, ws, lay, s);
+  if (is_int4(L->gate.fmt) && is_int4(L->down.fmt) && lay.h4) {
+    uint16_t* terms = (uint16_t*)((uint8_t*)ws + lay.h4);
+    if ((rc = run_gate_up_int4(L, x, ids, T, terms, true, ws, lay, s))) return rc;
+    return run_down_int4(L, terms, dn_direct(L, T, h), ids, rw, T, y, ws, lay, s);
   }
   if (gu_pf) {  // W4A8: MXFP8 x; fp32 h too when the down projection needs it
     if ((rc = hip_rc(launch_quant_mxfp8(0, x, T, L->hidden, xq, xs, s)))) return rc;
@@ -1195,6 +1256,16 @@ int moeq_linear_int4(const moeq_weight* w, int expert, const void* x, int T, con
   if (T > INT4_FEW_T && (!ws || ws_bytes < moeq_linear_int4_workspace_bytes(T, w->cols))) return MOEQ_E_WORKSPACE;
   if (!aligned(ws, 256)) return MOEQ_E_ALIGN;
   if (T == 0) return MOEQ_OK;
+  if (T > INT4_FEW_T) {
+    float* scale = (float*)ws;
+    uint16_t* act = (uint16_t*)((uint8_t*)ws + align_up((size_t)T * 4, 256));
+    if ((rc = hip_rc(launch_int4_rows(false, x, T, w->cols, act, scale, S(stream))))) return rc;
+    Int4Rows p = int4_rows(*w, nullptr, T, act, scale, y);
+    p.expert = expert;
+    p.bias = bias;
+    p.out_bf16 = out_type == MOEQ_OUT_BF16;
+    return hip_rc(launch_int4_tiled(I4_LINEAR, p, S(stream)));
+  }
   Int4Params p = int4_params(*w, x, w->cols, 0, T, y);
   p.expert = expert;
   p.bias = bias;

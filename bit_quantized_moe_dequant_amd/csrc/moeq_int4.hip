@@ -118,17 +118,33 @@ __global__ __launch_bounds__(256) void k_int4_dequant(int group, const uint8_t* 
   }
 }
 
+// An fp32 value as the sum of three bf16 ones of eight bits each: exact (but for subnormals).
+__device__ __forceinline__ void bf16_terms(float h, uint32_t (&b)[3]) {
+#pragma unroll
+  for (int a = 0; a < 3; a++) {
+    const uint32_t top = f2u(h) & 0xFFFF0000u;
+    b[a] = top >> 16;
+    h -= u2f(top);  // not a number behind an infinity
+  }
+}
+
 __global__ __launch_bounds__(256) void k_int4_terms(const float* h, size_t n, int cols, uint16_t* planes) {
   const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= n) return;
   const size_t row = i / cols, k = i % cols;
   const u32x4 v = ld16(h + i);
-  uint32_t hi[2], lo[2];
-  split_pair(u2f(v[0]), u2f(v[1]), hi[0], lo[0]);
-  split_pair(u2f(v[2]), u2f(v[3]), hi[1], lo[1]);
-  uint16_t* o = planes + row * 2 * cols + k;
-  *reinterpret_cast<u32x2*>(o) = u32x2{hi[0], hi[1]};
-  *reinterpret_cast<u32x2*>(o + cols) = u32x2{lo[0], lo[1]};
+  uint32_t t[3][4];
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    uint32_t b[3];
+    bf16_terms(u2f(v[j]), b);
+#pragma unroll
+    for (int a = 0; a < 3; a++) t[a][j] = b[a];
+  }
+  uint16_t* o = planes + row * 3 * cols + k;
+#pragma unroll
+  for (int a = 0; a < 3; a++)
+    *reinterpret_cast<u32x2*>(o + (size_t)a * cols) = u32x2{t[a][0] | (t[a][1] << 16), t[a][2] | (t[a][3] << 16)};
 }
 
 // ---------------------------------------------------------------- products
@@ -280,7 +296,8 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_int4_few(Int4Params P) {
 #pragma unroll
       for (int i = 0; i < TPQ; i++) {
         float v = tot[m][i * TERMS];
-        if constexpr (TERMS == 2) v += tot[m][i * 2 + 1];
+#pragma unroll
+        for (int a = 1; a < TERMS; a++) v += tot[m][i * TERMS + a];
         red[wave][m][g * TPQ + i][n] = v;
       }
     __syncthreads();
@@ -303,10 +320,11 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_int4_few(Int4Params P) {
         const size_t pair = perm ? perm[m0 + t] : first;
         const float h = ok ? silu_mul(v[0] * P.w[0].scale2[e], v[NMAT - 1] * P.w[1].scale2[e]) : 0.f;
         if (P.out_terms) {
-          const uint32_t hi = f2u(h) & 0xFFFF0000u;
-          uint16_t* out = (uint16_t*)P.y + pair * 2 * P.rows + r;
-          out[0] = (uint16_t)(hi >> 16);
-          out[P.rows] = (uint16_t)f32_bf16_rne_nan(h - u2f(hi));
+          uint32_t b[3];
+          bf16_terms(h, b);
+          uint16_t* out = (uint16_t*)P.y + pair * 3 * P.rows + r;
+#pragma unroll
+          for (int a = 0; a < 3; a++) out[(size_t)a * P.rows] = (uint16_t)b[a];
         } else {
           ((float*)P.y)[pair * P.rows + r] = h;
         }
@@ -353,10 +371,8 @@ hipError_t few_kind(int kind, const Int4Params& p, int items, hipStream_t s, con
       if (rows <= 4) return few<GP, 1, 1, I4_GATE_UP>(p, items, s, ev);
       if (rows <= 8) return few<GP, 1, 2, I4_GATE_UP>(p, items, s, ev);
       return few<GP, 1, 4, I4_GATE_UP>(p, items, s, ev);
-    case I4_DOWN_SUM: return few<GP, 2, 2, I4_DOWN_SUM>(p, items, s, ev);
-    case I4_DOWN_PART:
-      if (rows <= 4) return few<GP, 2, 2, I4_DOWN_PART>(p, items, s, ev);
-      return few<GP, 2, 4, I4_DOWN_PART>(p, items, s, ev);
+    case I4_DOWN_SUM: return few<GP, 3, 3, I4_DOWN_SUM>(p, items, s, ev);
+    case I4_DOWN_PART: return few<GP, 3, 3, I4_DOWN_PART>(p, items, s, ev);
   }
   return hipErrorInvalidValue;
 }

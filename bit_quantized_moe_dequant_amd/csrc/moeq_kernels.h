@@ -112,13 +112,13 @@ enum { FMT_INT8 = 9 };  // beside the FMT_* of moeq_device.h
 constexpr int INT4_FEW_T = 16;  // tokens of the linear that takes no workspace
 
 // Products of INT4 weights (moeq_int4.h) with rows of activations in bf16: tokens, or the
-// intermediate h as two terms (hi + lo) of each value.
+// intermediate h as three terms of each value, whose sum it is.
 enum { I4_LINEAR = 0, I4_GATE_UP = 1, I4_DOWN_SUM = 2, I4_DOWN_PART = 3 };
 struct Int4Params {
   int fmt;
   WeightRef w[2];       // gate and up, or one matrix
   int rows, cols;       // of the weight
-  const uint16_t* act;  // bf16 rows `pitch` values apart; the second term `term` values behind the first
+  const uint16_t* act;  // bf16 rows `pitch` values apart; their terms `term` values apart
   size_t pitch, term;
   int T, top_k, n_experts;
   int expert;           // I4_LINEAR: the one tensor
@@ -129,8 +129,24 @@ struct Int4Params {
   const float* bias;    // I4_LINEAR: [rows] or null
   void* y;              // linear [T][rows]; gate/up h [pairs][rows]; down [T][rows] or [pairs][rows]
   bool out_bf16;        // I4_LINEAR: y is bf16
-  bool out_terms;       // I4_GATE_UP: h as two bf16 planes, [pairs][2][rows]
+  bool out_terms;       // I4_GATE_UP: h as bf16 terms, [pairs][3][rows]
   uint32_t* err;
+};
+
+// The same for many rows, given as fp16 terms (launch_int4_rows): tokens [T][kpad], or h
+// [pairs][2][kpad], kpad = cols rounded up to 128. Experts' rows in the order of `route`.
+struct Int4Rows {
+  int fmt;
+  WeightRef w[2];
+  int rows, cols;
+  const uint16_t* act;
+  const float* act_scale;  // [rows of act]
+  int T, top_k, n_experts, expert;
+  RouteView route;
+  const float* rw;
+  const float* bias;
+  void* y;                 // as in Int4Params (no I4_DOWN_SUM)
+  bool out_bf16;
 };
 
 // 8-bit integer linear of one expert tensor.
@@ -272,8 +288,13 @@ hipError_t launch_pack_int4(int fmt, const uint8_t* codes, const uint16_t* scale
 hipError_t launch_dequant_int4(int fmt, const WeightRef& w, int rows, int cols, int expert, float* out, hipStream_t s);
 // Products for a few rows to an expert (any number is right, in tiles of up to 16 or 8 rows).
 hipError_t launch_int4_few(int kind, const Int4Params& p, int items, hipStream_t s, const LaunchEvents* ev = nullptr);
-// fp32 rows -> their two bf16 terms [n_rows][2][cols].
+// fp32 rows -> their three bf16 terms [n_rows][3][cols].
 hipError_t launch_int4_terms(const float* h, size_t n_rows, int cols, uint16_t* planes, hipStream_t s);
+bool int4_rows_fit(size_t n_rows, int terms, int cols);
+size_t int4_rows_bytes(size_t n_rows, int terms, int cols);
+// bf16 rows -> one fp16 term, fp32 rows -> two (see Int4Rows).
+hipError_t launch_int4_rows(bool in_f32, const void* x, size_t n_rows, int cols, uint16_t* out, float* scale, hipStream_t s);
+hipError_t launch_int4_tiled(int kind, const Int4Rows& p, hipStream_t s);
 
 // Chunk geometry: weights per 16-byte chunk; lanes per row and chunks per lane.
 int weights_per_chunk(int fmt);
