@@ -1,0 +1,312 @@
+// Products of INT4 weights with many activation rows (layout of the weights: moeq_int4.h).
+//
+//   y_tr = sum_g s_rg sum_{k in g} (q_rk - z_rg) x_tk
+//
+// on the fp16 matrix instruction (16 x 16 x 32). Codes become fp16 integers q - z, exact: the
+// nibble is laid into the mantissa of 1024 (or of 64, four bits higher) by a mask-and-or, and a
+// packed addition takes 1024 + z away, nine vector operations for eight values. Activations come
+// as fp16, every row times a power of two of its own (k_int4_rows): a bf16 value keeps all its
+// bits down to 2^-39 of its row's largest; the intermediate h, fp32, is two fp16 terms, 22 bits.
+// Sums are fp32. Two ways to the scale:
+//   exact   a group's sum, of exact products, is multiplied by its scale in fp32 and added up
+//           (a vector operation per output and group);
+//   SCALED  the scale is multiplied into the weight, rounded to fp16 (2^-12 relative on average
+//           at most, each weight for itself; 1e-4 of the result), for outputs that are rounded
+//           to bf16 (2^-9) anyway.
+//
+// Activations are operand A (its rows: tokens), so a lane's outputs belong to one weight row and
+// need one scale per group. A work-group's waves stand WM x WN, each with NM row tiles of weights
+// and 16 NT of its tokens, which lie in LDS in steps of 128 columns (three buffers; a row's 16-byte chunks at chunk ^ (row % 16), so that the sixteen rows
+// of an operand touch all banks once). Weights go from memory to registers, a step ahead.
+//
+// One barrier per step, before the products of its last 32 columns, whose operands are in
+// registers by then: behind it the step's buffer is free for the copy three steps on, and the
+// next step's first operands are read under those products. A wave decodes the next fragment of
+// weights between the products of one, as spread by the scheduling groups: left to the compiler,
+// the vector unit's and the matrix unit's work took turns.
+#pragma once
+#include "moeq_int4.h"
+#include "moeq_int8.h"
+#include "moeq_tiled.h"
+
+namespace moeq {
+
+namespace {
+
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+// ---------------------------------------------------------------- product
+
+__device__ __forceinline__ uint32_t pk_add(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, a) + __builtin_bit_cast(f16x2_t, b));
+}
+__device__ __forceinline__ uint32_t pk_mul(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, a) * __builtin_bit_cast(f16x2_t, b));
+}
+__device__ __forceinline__ uint32_t pk_half(float v) {
+  const uint32_t h = __builtin_bit_cast(uint16_t, (_Float16)v);
+  return h | (h << 16);
+}
+
+constexpr int I4_STAGES = 3;  // buffers of activations, and sets of weights in registers
+
+// Spread V vector operations among M matrix instructions, and R operand reads behind the first.
+template <int M, int V, int R, int I = 0>
+__device__ __forceinline__ void spread() {
+  if constexpr (I < M) {
+    constexpr int v = (I + 1) * V / M - I * V / M;
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (I < R) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    if constexpr (v > 0) __builtin_amdgcn_sched_group_barrier(0x002, v, 0);
+    spread<M, V, R, I + 1>();
+  }
+}
+
+template <int KIND, int GP, bool ZEROS, bool SCALED, int WM, int WN, int NM, int NT>
+__global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_int4_tiled(Int4Rows P) {
+  constexpr int TOK = 16 * NT * WN;            // activation rows of a work-group
+  constexpr int TERMS = KIND == I4_DOWN_PART ? 2 : 1, ROWS = TERMS * TOK, STAGE = ROWS * 256;
+  constexpr int COPIES = ROWS / 4 / (WM * WN);  // of a wave per step, four LDS rows each
+  static_assert(COPIES * 4 * WM * WN == ROWS, "whole copies");
+  constexpr int PAIRS = KIND == I4_GATE_UP ? 2 : 1;  // matrices side by side
+  constexpr int RT = NM / PAIRS;               // row tiles of a wave
+  __shared__ __attribute__((aligned(16))) uint8_t lds[I4_STAGES * STAGE];
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ktiles = int4_ktiles(P.cols), kpad = ktiles * 128, rtiles = int4_rtiles(P.rows);
+  const int nbm = (rtiles + WM * RT - 1) / (WM * RT);
+  const int wm = wave % WM, wn = wave / WM;
+
+  // tile of this work-group: row block bm, activation rows `first` .. + count
+  int bm, e, first, count;
+  const int32_t* perm = nullptr;
+  if constexpr (KIND == I4_LINEAR) {
+    int bn;
+    tile_of(blockIdx.x, nbm, (P.T + TOK - 1) / TOK, bm, bn);
+    first = bn * TOK;
+    count = min(TOK, P.T - first);
+    e = P.expert;
+  } else {
+    // the row blocks of a chunk of tokens on one XCD: they share the tokens in its L2
+    static_assert(TOK == PREFILL_MC, "chunks of the routing");
+    const int l = blockIdx.x / 8, q = l / nbm * 8 + (int)(blockIdx.x % 8);
+    bm = l % nbm;
+    if (q >= P.route.n_chunks()[0]) return;
+    e = P.route.chunk_e()[q];
+    const int p0 = P.route.offsets()[e], m0 = P.route.chunk_m0()[q];
+    count = min(TOK, P.route.offsets()[e + 1] - p0 - m0);
+    perm = P.route.perm() + p0 + m0;
+    first = 0;
+    if (e >= P.n_experts) {  // ids out of range
+      if constexpr (KIND == I4_DOWN_PART)
+        for (int i = threadIdx.x; i < count * 16 * WM * RT; i += 64 * WM * WN) {
+          const int r = bm * 16 * WM * RT + i % (16 * WM * RT);
+          if (r < P.rows) ((float*)P.y)[(size_t)perm[i / (16 * WM * RT)] * P.rows + r] = 0.f;
+        }
+      return;
+    }
+  }
+
+  // this lane's part of a wave's copies: LDS row 4 (COPIES wave + i) + lane / 16, term by term
+  const uint16_t* abase = P.act + (KIND == I4_LINEAR ? (size_t)first * kpad : 0);
+  int off[COPIES];
+#pragma unroll
+  for (int i = 0; i < COPIES; i++) {
+    const int row = 4 * (COPIES * wave + i) + (lane >> 4), term = row / TOK, t = min(row % TOK, count - 1);
+    int a = t;
+    if constexpr (KIND == I4_GATE_UP) a = perm[t] / P.top_k;
+    if constexpr (KIND == I4_DOWN_PART) a = perm[t];
+    off[i] = (a * TERMS + term) * kpad * 2 + 16 * ((lane & 15) ^ (row & 15));
+  }
+  auto copy = [&](int s, int to) {  // step s into buffer `to`
+    uint8_t* dst = lds + to * STAGE + 1024 * COPIES * wave;
+#pragma unroll
+    for (int i = 0; i < COPIES; i++) copy16(reinterpret_cast<const int8_t*>(abase), off[i], s * 256, dst + 1024 * i);
+  };
+
+  // row tiles of this wave; past the end the last one, whose outputs are not stored
+  const uint8_t* wp[NM];
+  const uint8_t* sp[NM];
+  const uint8_t* zp[NM];
+#pragma unroll
+  for (int m = 0; m < NM; m++) {
+    const WeightRef& w = P.w[PAIRS == 2 ? m / RT : 0];
+    const size_t tile = (size_t)min((bm * WM + wm) * RT + m % RT, rtiles - 1) * ktiles;
+    wp[m] = w.data + (size_t)e * w.estride + tile * 1024 + 16 * lane;
+    const uint8_t* s = w.scales + (size_t)e * w.sestride;
+    sp[m] = s + (tile * 16 + n) * GP * 2;
+    zp[m] = s + int4_zeros_at(P.fmt, P.rows, P.cols) + (tile * 16 + n) * GP;
+  }
+  struct Step {
+    u32x4 w[NM];
+    u32x2 s[NM];
+    uint32_t z[NM];
+  };
+  auto fetch = [&](int s, Step& v) {
+#pragma unroll
+    for (int m = 0; m < NM; m++) {
+      v.w[m] = ld16(wp[m] + (size_t)s * 1024);
+      const uint8_t* q = sp[m] + (size_t)s * 32 * GP;
+      if constexpr (GP == 1) v.s[m][0] = *reinterpret_cast<const uint16_t*>(q);
+      else if constexpr (GP == 2) v.s[m][0] = *reinterpret_cast<const uint32_t*>(q);
+      else v.s[m] = *reinterpret_cast<const u32x2*>(q);
+      if constexpr (ZEROS) {
+        const uint8_t* z = zp[m] + (size_t)s * 16 * GP;
+        if constexpr (GP == 1) v.z[m] = *z;
+        else if constexpr (GP == 2) v.z[m] = *reinterpret_cast<const uint16_t*>(z);
+        else v.z[m] = *reinterpret_cast<const uint32_t*>(z);
+      }
+    }
+  };
+
+  f32x4_t tot[NM][NT], acc[NM][NT];
+#pragma unroll
+  for (int m = 0; m < NM; m++)
+#pragma unroll
+    for (int t = 0; t < NT; t++) tot[m][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  // masks and the numbers whose mantissas take the nibbles, held in registers: one v_and_or each
+  uint32_t m0 = 0x000F000Fu, m1 = 0x00F000F0u, o0 = 0x64006400u, o1 = 0x54005400u;
+  asm volatile("" : "+s"(m0), "+s"(m1), "+v"(o0), "+v"(o1));
+  const int last = ktiles - 1;
+  Step w[I4_STAGES];
+  f16x8_t xv[2][TERMS][NT];  // operands of these 32 columns and the next
+  u32x4 d;                   // the next fragment of weights
+  auto read = [&](int buf, int j, int to) {
+    const uint8_t* x = lds + buf * STAGE + (wn * NT * 16 + n) * 256 + 16 * ((4 * j + g) ^ n);
+#pragma unroll
+    for (int a = 0; a < TERMS; a++)
+#pragma unroll
+      for (int t = 0; t < NT; t++) xv[to][a][t] = *reinterpret_cast<const f16x8_t*>(x + (a * TOK + t * 16) * 256);
+  };
+  auto decode = [&](const Step& v, int j, int m) {
+    const int gi = j * GP / 4;
+    const float z = ZEROS ? (float)(v.z[m] >> (8 * gi) & 255u) : 8.0f;
+    const uint32_t c0 = pk_half(-1024.0f - z), c1 = pk_half(-64.0f - z), lo = v.w[m][j], hi = lo >> 8;
+    d = u32x4{pk_add((lo & m0) | o0, c0), pk_add((lo & m1) | o1, c1), pk_add((hi & m0) | o0, c0), pk_add((hi & m1) | o1, c1)};
+    if constexpr (SCALED) {
+      const uint32_t sc = __builtin_amdgcn_perm(0u, v.s[m][gi / 2], gi & 1 ? 0x03020302u : 0x01000100u);
+#pragma unroll
+      for (int i = 0; i < 4; i++) d[i] = pk_mul(d[i], sc);
+    }
+  };
+  // Copies and fetches past the last step repeat it (into buffers that nobody reads), so that
+  // every wait counts the same.
+  fetch(0, w[0]);
+  asm volatile("" ::: "memory");
+  copy(0, 0);
+  copy(min(1, last), 1);
+  asm volatile("" ::: "memory");
+  fetch(min(1, last), w[1]);
+  asm volatile("" ::: "memory");
+  copy(min(2, last), 2);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * COPIES) : "memory");  // copy 0 (older than the second fetch too)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  read(0, 0, 0);
+  decode(w[0], 0, 0);
+  auto step = [&](int s, auto B) {  // B: s % I4_STAGES
+    constexpr int b = decltype(B)::value, nb = (b + 1) % I4_STAGES;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const bool begin = j % (4 / GP) == 0, end = (j + 1) % (4 / GP) == 0;
+      if (j < 3) {
+        read(b, j + 1, (j + 1) & 1);
+      } else {
+        // the next step's copies, and all reads of this one's; the copies of the one behind may be on their way
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(COPIES) : "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        fetch(min(s + 2, last), w[(b + 2) % I4_STAGES]);
+        asm volatile("" ::: "memory");
+        copy(min(s + 3, last), b);
+        read(nb, 0, 0);
+      }
+#pragma unroll
+      for (int m = 0; m < NM; m++) {
+        const f16x8_t now = __builtin_bit_cast(f16x8_t, d);
+        if (m + 1 < NM) decode(w[b], j, m + 1);
+        else if (j < 3) decode(w[b], j + 1, 0);
+        else decode(w[nb], 0, 0);
+#pragma unroll
+        for (int t = 0; t < NT; t++) {
+          f32x4_t c = SCALED ? tot[m][t] : begin ? f32x4_t{0.f, 0.f, 0.f, 0.f} : acc[m][t];
+          c = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv[j & 1][0][t], now, c, 0, 0, 0);
+          if constexpr (TERMS == 2) c = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv[j & 1][TERMS - 1][t], now, c, 0, 0, 0);
+          if constexpr (SCALED) tot[m][t] = c;
+          else acc[m][t] = c;
+        }
+        if (!SCALED && end) {
+          const float f = half_bits_f32(w[b].s[m][(j * GP / 4) / 2] >> (16 * (j * GP / 4 & 1)));
+#pragma unroll
+          for (int t = 0; t < NT; t++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) tot[m][t][r] = __builtin_fmaf(f, acc[m][t][r], tot[m][t][r]);
+        }
+      }
+      if (SCALED) spread<NM * NT * TERMS, NM * 15, TERMS * NT>();
+      else if (end) spread<NM * NT * TERMS, NM * (11 + 4 * NT), TERMS * NT>();
+      else spread<NM * NT * TERMS, NM * 11, TERMS * NT>();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  for (int s = 0; s < ktiles; s += I4_STAGES) {
+    step(s, Count<0>{});
+    if (s + 1 < ktiles) step(s + 1, Count<1>{});
+    if (s + 2 < ktiles) step(s + 2, Count<2>{});
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no copy outlives the work-group
+
+  // lane (n, g), register r of token tile t: token 16 t + 4 g + r, weight row n of the tile
+  const int t0 = wn * NT * 16 + 4 * g;
+#pragma unroll
+  for (int t = 0; t < NT; t++) {
+    float as[4];
+    size_t at[4];
+#pragma unroll
+    for (int r = 0; r < 4; r++) {
+      const int i = min(t0 + 16 * t + r, count - 1);
+      const size_t a = KIND == I4_LINEAR ? (size_t)(first + i) : (size_t)perm[i];
+      as[r] = P.act_scale[KIND == I4_GATE_UP ? a / P.top_k : a];
+      if constexpr (KIND == I4_DOWN_PART) as[r] *= P.rw[a];
+      at[r] = a * P.rows;
+    }
+    const float s0 = P.w[0].scale2[e], s1 = PAIRS == 2 ? P.w[1].scale2[e] : 0.f;
+#pragma unroll
+    for (int m = 0; m < RT; m++) {
+      const int row = ((bm * WM + wm) * RT + m) * 16 + n;
+      if (row >= P.rows) continue;
+      float bias = 0.f;
+      if constexpr (KIND == I4_LINEAR)
+        if (P.bias) bias = P.bias[row];
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        if (t0 + 16 * t + r >= count) continue;
+        float v = tot[m][t][r] * s0 * as[r];
+        if constexpr (PAIRS == 2) v = silu_mul(v, tot[RT + m][t][r] * s1 * as[r]);
+        if constexpr (KIND == I4_LINEAR) {
+          v += bias;
+          if (P.out_bf16) {
+            ((uint16_t*)P.y)[at[r] + row] = (uint16_t)f32_bf16_rne_nan(v);
+            continue;
+          }
+        }
+        ((float*)P.y)[at[r] + row] = v;
+      }
+    }
+  }
+}
+
+template <int KIND, int GP, bool SCALED, int WM, int WN, int NM, int NT>
+hipError_t tiled(const Int4Rows& p, long blocks, hipStream_t s) {
+  const dim3 g((unsigned)blocks), b(64 * WM * WN);
+  if (int4_zeros(p.fmt)) hipLaunchKernelGGL((k_int4_tiled<KIND, GP, true, SCALED, WM, WN, NM, NT>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((k_int4_tiled<KIND, GP, false, SCALED, WM, WN, NM, NT>), g, b, 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+}  // namespace moeq
