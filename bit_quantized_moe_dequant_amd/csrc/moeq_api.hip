@@ -153,7 +153,7 @@ WsLayout ws_layout(const moeq_layer* L, int T) {
   w.h = off;
   off += align_up(P * L->inter * 4, 256);
   w.partial = off;
-  off += T > 1 ? align_up(P * L->hidden * 4, 256) : 0;
+  off += T > 1 || is_int4(L->down.fmt) ? align_up(P * L->hidden * 4, 256) : 0;
   w.xq = w.xs = w.hq = w.hs = w.dq = w.ds = 0;
   w.err = nullptr;
   if (T > 1 && L->down.fmt == MOEQ_FMT_Q2_K && dn_q2k_g_fits(L->hidden, L->inter)) {
@@ -321,8 +321,9 @@ bool scales16(const moeq_weight& w) {
 #define MOEQ_INT4_DIRECT_MAX_T 4
 #endif
 bool gu_direct(const moeq_layer* L, int T) {
+  if (is_int4(L->gate.fmt))
+    return T <= MOEQ_INT4_DIRECT_MAX_T && !int4_many(L, T) && int4_one_fits(I4_GATE_UP, L->top_k, L->hidden);
   if (T == 1) return true;
-  if (is_int4(L->gate.fmt)) return T >= 1 && T <= MOEQ_INT4_DIRECT_MAX_T && !int4_many(L, T);
   if (L->gate.fmt == MOEQ_FMT_IQ2_XXS)  // the dequantize + GEMV over every pair
     return T >= 1 && L->up.fmt == MOEQ_FMT_IQ2_XXS && pairs_per_expert(L, T) < MOEQ_IQ2_DIRECT_BELOW;
   const int max_t = L->gate.fmt == MOEQ_FMT_MXFP4 ? MOEQ_FP4_DIRECT_MAX_T
@@ -332,9 +333,10 @@ bool gu_direct(const moeq_layer* L, int T) {
          scales16(L->gate) && scales16(L->up);
 }
 bool dn_direct(const moeq_layer* L, int T, const float* h) {
+  if (is_int4(L->down.fmt))
+    return T <= MOEQ_INT4_DIRECT_MAX_T && !int4_many(L, T) && int4_one_fits(I4_DOWN_SUM, L->top_k, L->inter);
   if (T == 1) return true;
   if (T < 1 || !aligned(h, 16)) return false;
-  if (is_int4(L->down.fmt)) return T <= MOEQ_INT4_DIRECT_MAX_T && !int4_many(L, T);
   if (L->down.fmt == MOEQ_FMT_MXFP4)
     return T <= MOEQ_FP4_DIRECT_MAX_T && down1_mx4_fits(L->hidden, L->inter, L->top_k) && scales16(L->down);
   if (L->down.fmt == MOEQ_FMT_Q2_K)
@@ -1050,7 +1052,7 @@ int forward(const moeq_layer* L, const void* x, const int32_t* ids, const float*
             const WsLayout& lay, hipStream_t s) {
   int rc;
   float* h = (float*)((uint8_t*)ws + lay.h);
-  if (T > 1 && !(gu_direct(L, T) && dn_direct(L, T, h))) {
+  if (!(gu_direct(L, T) && dn_direct(L, T, h))) {
     rc = hip_rc(launch_route(ids, T * L->top_k, L->n_experts, route_view(L, ws, lay), err_of(ws, lay), s));
     if (rc) return rc;
   }

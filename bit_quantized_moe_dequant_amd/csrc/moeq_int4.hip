@@ -20,6 +20,9 @@
 // (32 clocks) and one matrix instruction of 16.
 #include <hip/hip_ext.h>
 
+#include <algorithm>
+#include <type_traits>
+
 #include "moeq_int4.h"
 #include "moeq_int8.h"
 
@@ -150,239 +153,426 @@ __global__ __launch_bounds__(256) void k_int4_terms(const float* h, size_t n, in
 // ---------------------------------------------------------------- products
 
 constexpr int FEW_WAVES = 8;
-constexpr int FEW_DEPTH = 4;  // tiles of 128 columns whose loads a wave has in flight
 
-// A work-group: 16 weight rows (of the gate and of the up matrix for NMAT = 2), all of K, whose
-// tiles its waves take in turn; their sums meet in LDS and are added in the order of the waves.
-// GP: groups per 128 columns. TERMS: bf16 terms of an activation. NR: output registers in use,
-// so a tile holds 4 NR / TERMS tokens.
-template <int GP, int TERMS, int NR, int KIND>
-__global__ __launch_bounds__(64 * FEW_WAVES) void k_int4_few(Int4Params P) {
-  constexpr int NMAT = KIND == I4_GATE_UP ? 2 : 1, TPQ = NR / TERMS, TOK = 4 * TPQ;
+// A row's scales and zero points of one tile.
+template <int GP, bool ZEROS, int NMAT>
+struct Side {
+  u32x2 s[NMAT];
+  uint32_t z[NMAT];
+};
+
+// Tile `tile` of expert e: codes of this lane, and the side data of its row.
+template <int GP, bool ZEROS, int NMAT>
+__device__ __forceinline__ void int4_load(const Int4Params& P, int e, size_t tile, int lane, u32x4 (&w)[NMAT], Side<GP, ZEROS, NMAT>& side) {
+#pragma unroll
+  for (int m = 0; m < NMAT; m++) {
+    w[m] = ld16(P.w[m].data + (size_t)e * P.w[m].estride + tile * 1024 + 16 * lane);
+    const uint8_t* sp = P.w[m].scales + (size_t)e * P.w[m].sestride;
+    const size_t at = (tile * 16 + (lane & 15)) * GP;
+    if constexpr (GP == 1) side.s[m][0] = *reinterpret_cast<const uint16_t*>(sp + 2 * at);
+    else if constexpr (GP == 2) side.s[m][0] = *reinterpret_cast<const uint32_t*>(sp + 2 * at);
+    else side.s[m] = *reinterpret_cast<const u32x2*>(sp + 2 * at);
+    if constexpr (ZEROS) {
+      const uint8_t* zp = sp + int4_zeros_at(P.fmt, P.rows, P.cols) + at;
+      if constexpr (GP == 1) side.z[m] = *zp;
+      else if constexpr (GP == 2) side.z[m] = *reinterpret_cast<const uint16_t*>(zp);
+      else side.z[m] = *reinterpret_cast<const uint32_t*>(zp);
+    }
+  }
+}
+
+__device__ __forceinline__ f32x4_t mfma(u32x4 x, u32x4 w, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x), __builtin_bit_cast(bf16x8_t, w), c, 0, 0, 0);
+}
+__device__ __forceinline__ u32x4 ones() { return u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}; }
+
+// Keeps every register of the matrix instructions' results a and b until `v`, computed from them,
+// is there. Where only some of them are used, the compiler gives the others to vector operations
+// between the instruction and its end without the wait that this takes, and the result lands in them.
+__device__ __forceinline__ void hold(float& v, const f32x4_t& a, const f32x4_t& b) {
+  asm volatile("" : "+v"(v) : "v"(a), "v"(b));
+}
+
+// Eight codes as 16 + q in bf16.
+__device__ __forceinline__ u32x4 int4_operand(uint32_t w) {
+  return u32x4{((w << 3) & 0x00780078u) | 0x41804180u, ((w >> 1) & 0x00780078u) | 0x41804180u,
+               ((w >> 5) & 0x00780078u) | 0x41804180u, ((w >> 9) & 0x00780078u) | 0x41804180u};
+}
+
+// scale of group gi of a tile, and what is too much in its sum for every unit of sum x
+template <int GP, bool ZEROS, int NMAT>
+__device__ __forceinline__ float int4_scale(const Side<GP, ZEROS, NMAT>& side, int m, int gi) {
+  return half_bits_f32(side.s[m][gi / 2] >> (16 * (gi & 1)));
+}
+template <int GP, bool ZEROS, int NMAT>
+__device__ __forceinline__ float int4_offset(const Side<GP, ZEROS, NMAT>& side, int m, int gi) {
+  return ZEROS ? 16.0f + (float)(side.z[m] >> (8 * gi) & 255u) : 24.0f;
+}
+
+// What becomes of the sums v (one per matrix) of weight row r and activation row t of the tile:
+// `pair` is its (token, slot) pair, or the token.
+template <int KIND, int NMAT>
+__device__ __forceinline__ void int4_store(const Int4Params& P, int e, bool ok, size_t pair, int r, const float (&v)[NMAT]) {
+  if constexpr (KIND == I4_LINEAR) {
+    const size_t at = pair * P.rows + r;
+    float f = v[0] * P.w[0].scale2[e];
+    if (P.bias) f += P.bias[r];
+    if (P.out_bf16) ((uint16_t*)P.y)[at] = (uint16_t)f32_bf16_rne_nan(f);
+    else ((float*)P.y)[at] = f;
+  } else if constexpr (KIND == I4_GATE_UP) {
+    const float h = ok ? silu_mul(v[0] * P.w[0].scale2[e], v[NMAT - 1] * P.w[1].scale2[e]) : 0.f;
+    if (P.out_terms) {
+      uint32_t b[3];
+      bf16_terms(h, b);
+      uint16_t* out = (uint16_t*)P.y + pair * 3 * P.rows + r;
+#pragma unroll
+      for (int a = 0; a < 3; a++) out[(size_t)a * P.rows] = (uint16_t)b[a];
+    } else {
+      ((float*)P.y)[pair * P.rows + r] = h;
+    }
+  } else if constexpr (KIND == I4_DOWN_SUM) {
+    ((float*)P.y)[pair * P.rows + r] = v[0];
+  } else {
+    ((float*)P.y)[pair * P.rows + r] = ok ? v[0] * P.w[0].scale2[e] * P.rw[pair] : 0.f;
+  }
+}
+
+// One token (or pair; I4_DOWN_SUM: a token's pairs one behind the other) or up to four of a
+// linear, whose rows lie in LDS. A work-group: 16 weight rows (of the gate and of the up matrix),
+// all of K, whose tiles its waves take in turn, DEPTH of them with their loads in flight at once,
+// issued before the activations are waited for; the waves' sums meet in LDS and are added in the
+// order of the waves. TERMS: bf16 terms of an activation. The lanes of operand A's unused rows
+// read zeros.
+template <int GP, bool ZEROS, int TERMS, int KIND, int DEPTH>
+__global__ __launch_bounds__(64 * FEW_WAVES) void k_int4_one(Int4Params P) {
+  constexpr int NMAT = KIND == I4_GATE_UP ? 2 : 1, NR = TERMS, TOK = TERMS == 1 ? 4 : 1;
+  extern __shared__ __attribute__((aligned(16))) uint8_t xs[];  // 16 bytes of zeros, then the rows
   __shared__ float red[FEW_WAVES][NMAT][TOK][16];
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int rt = blockIdx.x, item = blockIdx.y, ktiles = int4_ktiles(P.cols);
+  const int parts = KIND == I4_DOWN_SUM ? P.top_k : 1, steps = parts * ktiles;
+  const int tok = KIND == I4_LINEAR ? P.T : 1;
 
-  // The rows of this work-group's activations: `count` of them, in tiles of TOK.
-  int e = 0, first = 0, count = 1;
-  const int32_t* perm = nullptr;
+  int e = KIND == I4_LINEAR ? P.expert : 0;
   bool ok = true;
-  if constexpr (KIND == I4_LINEAR) {
-    e = P.expert;
-    first = item * TOK;
-    count = min(TOK, P.T - first);
-  } else if constexpr (KIND != I4_DOWN_SUM) {
-    if (P.grouped) {
-      if (item >= P.route.n_slots()[0]) return;
-      e = P.route.slots()[item];
-      const int p0 = P.route.offsets()[e];
-      count = P.route.offsets()[e + 1] - p0;
-      perm = P.route.perm() + p0;
-    } else {
-      e = P.ids[item];
-      first = item;
-    }
+  if constexpr (KIND == I4_GATE_UP) {
+    e = P.ids[item];
     ok = e >= 0 && e < P.n_experts;
     if (!ok && rt == 0 && threadIdx.x == 0) atomicOr(P.err, 1u);
+    if (!ok) e = 0;
   }
-  const int steps = KIND == I4_DOWN_SUM ? P.top_k * ktiles : ktiles;
 
-  // this lane's row of operand A: token `ai` of the tile, term `at`
-  const int ai = (n & 3) / TERMS + (n >> 2) * TPQ, aterm = (n & 3) % TERMS;
-  const size_t tiles_at = (size_t)rt * ktiles;
-
-  for (int m0 = 0; m0 < count; m0 += TOK) {
-    const int here = min(TOK, count - m0);
-    float tot[NMAT][NR];
+  u32x4 wv[DEPTH][NMAT];
+  Side<GP, ZEROS, NMAT> side[DEPTH];
+  float fac[DEPTH];
+  bool live[DEPTH];
+  auto load = [&](int u0) {
 #pragma unroll
-    for (int m = 0; m < NMAT; m++)
-#pragma unroll
-      for (int r = 0; r < NR; r++) tot[m][r] = 0.f;
-    const bool a_on = (n & 3) < NR && ai < here;
-    size_t arow = 0;
-    if (a_on) {
-      if constexpr (KIND == I4_LINEAR) arow = first + ai;
-      else if constexpr (KIND == I4_DOWN_SUM) arow = (size_t)item * P.top_k;
-      else if constexpr (KIND == I4_GATE_UP) arow = (perm ? perm[m0 + ai] : first) / P.top_k;
-      else arow = perm ? perm[m0 + ai] : first;
+    for (int d = 0; d < DEPTH; d++) {
+      const int u = min(u0 + d * waves, steps - 1);
+      live[d] = u0 + d * waves < steps && ok;
+      int kt = u;
+      if constexpr (KIND == I4_DOWN_SUM) {
+        const int k = u / ktiles;
+        kt = u % ktiles;
+        e = P.ids[(size_t)item * P.top_k + k];
+        const bool good = e >= 0 && e < P.n_experts;
+        if (!good && rt == 0 && lane == 0 && kt == 0 && live[d]) atomicOr(P.err, 1u);
+        live[d] = live[d] && good;
+        e = good ? e : 0;
+        fac[d] = P.rw[(size_t)item * P.top_k + k] * P.w[0].scale2[e];
+      }
+      int4_load(P, e, (size_t)rt * ktiles + kt, lane, wv[d], side[d]);
     }
-    const uint16_t* ap = P.act + arow * P.pitch + aterm * P.term + 8 * g;
+  };
+  load(wave);
 
-    if (ok) {
-      for (int u0 = wave; u0 < steps; u0 += waves * FEW_DEPTH) {
-        u32x4 wv[FEW_DEPTH][NMAT], xv[FEW_DEPTH][4];
-        u32x2 sv[FEW_DEPTH][NMAT];
-        uint32_t zv[FEW_DEPTH][NMAT];
-        float fac[FEW_DEPTH];
-        bool live[FEW_DEPTH];
+  // the rows: token by token, or part by part and term by term, `pitch` bytes apart
+  const int kpad = ktiles * 128, pitch = kpad * 2 + 16, rows = KIND == I4_DOWN_SUM ? parts * TERMS : tok;
+  if (threadIdx.x < 4) reinterpret_cast<uint32_t*>(xs)[threadIdx.x] = 0;
+  for (int i = threadIdx.x; i < rows * (kpad / 8); i += blockDim.x) {
+    const int row = i / (kpad / 8), k = i % (kpad / 8) * 8;
+    const uint16_t* a = P.act;
+    if constexpr (KIND == I4_DOWN_SUM) a += ((size_t)item * P.top_k + row / TERMS) * P.pitch + row % TERMS * P.term;
+    else if constexpr (KIND == I4_GATE_UP) a += (size_t)(item / P.top_k) * P.pitch;
+    else a += (size_t)row * P.pitch;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (k < P.cols) v = ld16(a + k);
+    *reinterpret_cast<u32x4*>(xs + 16 + (size_t)row * pitch + 2 * k) = v;
+  }
+  __syncthreads();
+  // this lane's row of operand A: token n / 4 in row 0, 4, 8, 12, or term n
+  const bool a_on = TERMS == 1 ? (n & 3) == 0 && n / 4 < tok : n < TERMS;
+  const int a0 = a_on ? 16 + (TERMS == 1 ? n / 4 : n) * pitch + 16 * g : 0, a_step = a_on ? 1 : 0;
+
+  float tot[NMAT][NR];
 #pragma unroll
-        for (int d = 0; d < FEW_DEPTH; d++) {
-          const int u = min(u0 + d * waves, steps - 1);
-          const int kt = KIND == I4_DOWN_SUM ? u % ktiles : u;
-          int ee = e;
-          fac[d] = 1.f;
-          live[d] = u0 + d * waves < steps;
-          const uint16_t* a = ap;
-          if constexpr (KIND == I4_DOWN_SUM) {
-            const int k = u / ktiles;
-            ee = P.ids[(size_t)item * P.top_k + k];
-            const bool good = ee >= 0 && ee < P.n_experts;
-            if (!good && rt == 0 && lane == 0 && kt == 0) atomicOr(P.err, 1u);
-            ee = good ? ee : 0;
-            live[d] = live[d] && good;
-            fac[d] = P.rw[(size_t)item * P.top_k + k] * P.w[0].scale2[ee];
-            a += k * P.pitch;
-          }
-          const size_t tile = tiles_at + kt;
+  for (int m = 0; m < NMAT; m++)
+#pragma unroll
+    for (int r = 0; r < NR; r++) tot[m][r] = 0.f;
+  for (int u0 = wave; u0 < steps; u0 += waves * DEPTH) {
+    if (u0 != wave) load(u0);
+#pragma unroll
+    for (int d = 0; d < DEPTH; d++) {
+      if (!live[d]) continue;
+      const int u = u0 + d * waves, kt = KIND == I4_DOWN_SUM ? u % ktiles : u;
+      const uint8_t* x = xs + a0 + a_step * ((KIND == I4_DOWN_SUM ? u / ktiles * TERMS * pitch : 0) + kt * 256);
+      f32x4_t acc[NMAT], sx = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int m = 0; m < NMAT; m++) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const u32x4 xv = *reinterpret_cast<const u32x4*>(x + a_step * 64 * j);
+        sx = mfma(xv, ones(), sx);
+#pragma unroll
+        for (int m = 0; m < NMAT; m++) acc[m] = mfma(xv, int4_operand(wv[d][m][j]), acc[m]);
+        if ((j + 1) % (4 / GP) == 0) {  // a group's end
+          const int gi = j * GP / 4;
 #pragma unroll
           for (int m = 0; m < NMAT; m++) {
-            wv[d][m] = ld16(P.w[m].data + (size_t)ee * P.w[m].estride + tile * 1024 + 16 * lane);
-            const uint8_t* sp = P.w[m].scales + (size_t)ee * P.w[m].sestride;
-            const size_t at = tile * 16 * GP + n * GP;
-            if constexpr (GP == 1) sv[d][m][0] = *reinterpret_cast<const uint16_t*>(sp + 2 * at);
-            else if constexpr (GP == 2) sv[d][m][0] = *reinterpret_cast<const uint32_t*>(sp + 2 * at);
-            else sv[d][m] = *reinterpret_cast<const u32x2*>(sp + 2 * at);
-            zv[d][m] = 0x08080808u;
-            if (int4_zeros(P.fmt)) {
-              const uint8_t* zp = sp + int4_zeros_at(P.fmt, P.rows, P.cols) + at;
-              if constexpr (GP == 1) zv[d][m] = *zp;
-              else if constexpr (GP == 2) zv[d][m] = *reinterpret_cast<const uint16_t*>(zp);
-              else zv[d][m] = *reinterpret_cast<const uint32_t*>(zp);
-            }
+            float s = int4_scale(side[d], m, gi);
+            if constexpr (KIND == I4_DOWN_SUM) s *= fac[d];
+            const float c = int4_offset(side[d], m, gi);
+#pragma unroll
+            for (int r = 0; r < NR; r++) tot[m][r] = __builtin_fmaf(s, __builtin_fmaf(-c, sx[r], acc[m][r]), tot[m][r]);
+            hold(tot[m][NR - 1], acc[m], sx);
+            acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
           }
-#pragma unroll
-          for (int j = 0; j < 4; j++) {
-            xv[d][j] = u32x4{0u, 0u, 0u, 0u};
-            if (a_on && kt * 128 + 32 * j < P.cols) xv[d][j] = ld16(a + kt * 128 + 32 * j);
-          }
-        }
-#pragma unroll
-        for (int d = 0; d < FEW_DEPTH; d++) {
-          if (!live[d]) continue;
-          f32x4_t acc[NMAT], sx = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int m = 0; m < NMAT; m++) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int j = 0; j < 4; j++) {
-            const bf16x8_t x = __builtin_bit_cast(bf16x8_t, xv[d][j]);
-            sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                x, __builtin_bit_cast(bf16x8_t, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}), sx, 0, 0, 0);
-#pragma unroll
-            for (int m = 0; m < NMAT; m++) {
-              const uint32_t w = wv[d][m][j];
-              const u32x4 q = {((w << 3) & 0x00780078u) | 0x41804180u, ((w >> 1) & 0x00780078u) | 0x41804180u,
-                               ((w >> 5) & 0x00780078u) | 0x41804180u, ((w >> 9) & 0x00780078u) | 0x41804180u};
-              acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, __builtin_bit_cast(bf16x8_t, q), acc[m], 0, 0, 0);
-            }
-            if ((j + 1) % (4 / GP) == 0) {  // a group's end
-              const int gi = j * GP / 4;
-#pragma unroll
-              for (int m = 0; m < NMAT; m++) {
-                const float s = half_bits_f32(sv[d][m][gi / 2] >> (16 * (gi & 1))) * fac[d];
-                const float c = 16.0f + (float)(zv[d][m] >> (8 * gi) & 255u);
-#pragma unroll
-                for (int r = 0; r < NR; r++) tot[m][r] = __builtin_fmaf(s, __builtin_fmaf(-c, sx[r], acc[m][r]), tot[m][r]);
-                acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-              }
-              sx = f32x4_t{0.f, 0.f, 0.f, 0.f};
-            }
-          }
+          sx = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
       }
     }
+  }
 #pragma unroll
-    for (int m = 0; m < NMAT; m++)
+  for (int m = 0; m < NMAT; m++) {
+    float v = tot[m][0];
 #pragma unroll
-      for (int i = 0; i < TPQ; i++) {
-        float v = tot[m][i * TERMS];
+    for (int a = 1; a < TERMS; a++) v += tot[m][a];
+    if (g < TOK) red[wave][m][g][n] = v;
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < tok * 16) {
+    const int t = threadIdx.x >> 4, r = rt * 16 + n;
+    float v[NMAT];
 #pragma unroll
-        for (int a = 1; a < TERMS; a++) v += tot[m][i * TERMS + a];
-        red[wave][m][g * TPQ + i][n] = v;
-      }
-    __syncthreads();
-    for (int o = threadIdx.x; o < here * 16; o += blockDim.x) {
-      const int t = o >> 4, r = rt * 16 + (o & 15);
-      float v[NMAT];
-#pragma unroll
-      for (int m = 0; m < NMAT; m++) {
-        v[m] = 0.f;
-        for (int w = 0; w < waves; w++) v[m] += red[w][m][t][o & 15];
-      }
-      if (r >= P.rows) continue;
-      if constexpr (KIND == I4_LINEAR) {
-        const size_t at = (size_t)(first + t) * P.rows + r;
-        float f = v[0] * P.w[0].scale2[e];
-        if (P.bias) f += P.bias[r];
-        if (P.out_bf16) ((uint16_t*)P.y)[at] = (uint16_t)f32_bf16_rne_nan(f);
-        else ((float*)P.y)[at] = f;
-      } else if constexpr (KIND == I4_GATE_UP) {
-        const size_t pair = perm ? perm[m0 + t] : first;
-        const float h = ok ? silu_mul(v[0] * P.w[0].scale2[e], v[NMAT - 1] * P.w[1].scale2[e]) : 0.f;
-        if (P.out_terms) {
-          uint32_t b[3];
-          bf16_terms(h, b);
-          uint16_t* out = (uint16_t*)P.y + pair * 3 * P.rows + r;
-#pragma unroll
-          for (int a = 0; a < 3; a++) out[(size_t)a * P.rows] = (uint16_t)b[a];
-        } else {
-          ((float*)P.y)[pair * P.rows + r] = h;
-        }
-      } else if constexpr (KIND == I4_DOWN_SUM) {
-        ((float*)P.y)[(size_t)item * P.rows + r] = v[0];
-      } else {
-        const size_t pair = perm ? perm[m0 + t] : first;
-        ((float*)P.y)[pair * P.rows + r] = ok ? v[0] * P.w[0].scale2[e] * P.rw[pair] : 0.f;
-      }
+    for (int m = 0; m < NMAT; m++) {
+      v[m] = 0.f;
+      for (int w = 0; w < waves; w++) v[m] += red[w][m][t][n];
     }
-    __syncthreads();
+    if (r < P.rows) int4_store<KIND, NMAT>(P, e, ok, KIND == I4_LINEAR ? t : item, r, v);
   }
 }
 
-template <int GP, int TERMS, int NR, int KIND>
-hipError_t few(const Int4Params& p, int items, hipStream_t s, const LaunchEvents* ev) {
+// A few rows to an expert. A work-group takes `rb` row tiles of an expert, one after another; its
+// waves take the tiles of K in turn, KT of them at a time, whose activations (and, as
+// they do not change with the weight row, their sums for each group) stay in registers, so that
+// only weights move: the next row tile's are loaded as this one's are used up. The waves' sums
+// meet in LDS (two buffers, so one barrier to a row tile) and are added in the order of the waves.
+// NR: output registers in use, so a tile of operand A holds 4 NR / TERMS rows.
+template <int GP, bool ZEROS, int TERMS, int NR, int KIND, int KT>
+__device__ __forceinline__ void int4_few(const Int4Params& P, float* red, int e, int first, int count, const int32_t* perm,
+                                         bool ok, int rt0, int rt1) {
+  constexpr int NMAT = KIND == I4_GATE_UP ? 2 : 1, TPQ = NR / TERMS, TOK = 4 * TPQ;
+  constexpr int RED = FEW_WAVES * NMAT * TOK * 16;
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ktiles = int4_ktiles(P.cols), rounds = (ktiles + FEW_WAVES * KT - 1) / (FEW_WAVES * KT);
+  // this lane's row of operand A: token `ai` of the tile, term `aterm`
+  const int ai = (n & 3) / TERMS + (n >> 2) * TPQ, aterm = (n & 3) % TERMS;
+
+  for (int m0 = 0; m0 < count; m0 += TOK) {
+    const int here = min(TOK, count - m0);
+    const bool a_on = (n & 3) < NR && ai < here;
+    size_t arow = 0;
+    if (a_on) {
+      arow = perm ? perm[m0 + ai] : first + m0 + ai;
+      if constexpr (KIND == I4_GATE_UP) arow /= P.top_k;
+    }
+    const uint16_t* ap = P.act + arow * P.pitch + aterm * P.term + 8 * g;
+    u32x4 wv[KT][NMAT], xv[KT][4];
+    Side<GP, ZEROS, NMAT> side[KT];
+    f32x4_t sx[KT][GP];
+    auto load = [&](int rt, int round, int i) {
+      const int kt = min((round * KT + i) * FEW_WAVES + wave, ktiles - 1);
+      int4_load(P, e, (size_t)rt * ktiles + kt, lane, wv[i], side[i]);
+    };
+    if (ok) {
+#pragma unroll
+      for (int i = 0; i < KT; i++) load(rt0, 0, i);
+    }
+    int buf = 0;
+    for (int rt = rt0; rt < rt1; rt++, buf ^= 1) {
+      float tot[NMAT][NR];
+#pragma unroll
+      for (int m = 0; m < NMAT; m++)
+#pragma unroll
+        for (int r = 0; r < NR; r++) tot[m][r] = 0.f;
+      if (ok) {
+        for (int round = 0; round < rounds; round++) {
+          if (rt == rt0 || rounds > 1) {
+#pragma unroll
+            for (int i = 0; i < KT; i++) {
+              const int k0 = ((round * KT + i) * FEW_WAVES + wave) * 128;
+#pragma unroll
+              for (int j = 0; j < 4; j++) {  // zeros past the end, and so for tiles past it
+                xv[i][j] = u32x4{0u, 0u, 0u, 0u};
+                if (a_on && k0 + 32 * j < P.cols) xv[i][j] = ld16(ap + k0 + 32 * j);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < KT; i++)
+#pragma unroll
+              for (int q = 0; q < GP; q++) {
+                f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = q * (4 / GP); j < (q + 1) * (4 / GP); j++) v = mfma(xv[i][j], ones(), v);
+                sx[i][q] = v;
+              }
+          }
+#pragma unroll
+          for (int i = 0; i < KT; i++) {
+            if ((round * KT + i) * FEW_WAVES + wave < ktiles) {
+#pragma unroll
+              for (int q = 0; q < GP; q++)
+#pragma unroll
+                for (int m = 0; m < NMAT; m++) {
+                  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                  for (int j = q * (4 / GP); j < (q + 1) * (4 / GP); j++) acc = mfma(xv[i][j], int4_operand(wv[i][m][j]), acc);
+                  const float s = int4_scale(side[i], m, q), c = int4_offset(side[i], m, q);
+#pragma unroll
+                  for (int r = 0; r < NR; r++) tot[m][r] = __builtin_fmaf(s, __builtin_fmaf(-c, sx[i][q][r], acc[r]), tot[m][r]);
+                  hold(tot[m][NR - 1], acc, sx[i][q]);
+                }
+            }
+            if (round + 1 < rounds) load(rt, round + 1, i);
+            else if (rt + 1 < rt1) load(rt + 1, 0, i);
+          }
+        }
+      }
+      float* rd = red + buf * RED;
+#pragma unroll
+      for (int m = 0; m < NMAT; m++)
+#pragma unroll
+        for (int i = 0; i < TPQ; i++) {
+          float v = tot[m][i * TERMS];
+#pragma unroll
+          for (int a = 1; a < TERMS; a++) v += tot[m][i * TERMS + a];
+          rd[((wave * NMAT + m) * TOK + g * TPQ + i) * 16 + n] = v;
+        }
+      __syncthreads();
+      const int t = threadIdx.x >> 4, r = rt * 16 + n;
+      if (t < here) {
+        float v[NMAT];
+#pragma unroll
+        for (int m = 0; m < NMAT; m++) {
+          v[m] = 0.f;
+#pragma unroll
+          for (int w = 0; w < FEW_WAVES; w++) v[m] += rd[((w * NMAT + m) * TOK + t) * 16 + n];
+        }
+        if (r < P.rows) int4_store<KIND, NMAT>(P, e, ok, perm ? perm[m0 + t] : first + m0 + t, r, v);
+      }
+    }
+    __syncthreads();  // the buffers are free again
+  }
+}
+
+template <int GP, bool ZEROS, int KIND, int KT>
+__global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_int4_few(Int4Params P, int rb) {
+  __shared__ float red[2 * FEW_WAVES * (KIND == I4_GATE_UP ? 2 : 1) * 16 * 16];
+  const int rt0 = blockIdx.x * rb, rt1 = min(rt0 + rb, int4_rtiles(P.rows)), item = blockIdx.y;
+  int e = P.expert, first = item * 16, count = min(16, P.T - first);
+  const int32_t* perm = nullptr;
+  bool ok = true;
+  if constexpr (KIND != I4_LINEAR) {
+    if (item >= P.route.n_slots()[0]) return;
+    e = P.route.slots()[item];
+    const int p0 = P.route.offsets()[e];
+    count = P.route.offsets()[e + 1] - p0;
+    perm = P.route.perm() + p0;
+    first = 0;
+    ok = e < P.n_experts;  // ids out of range have set the error bit when they were sorted
+  }
+  if constexpr (KIND == I4_DOWN_PART) {
+    int4_few<GP, ZEROS, 3, 3, KIND, KT>(P, red, e, first, count, perm, ok, rt0, rt1);
+  } else if (count <= 4) {
+    int4_few<GP, ZEROS, 1, 1, KIND, KT>(P, red, e, first, count, perm, ok, rt0, rt1);
+  } else if (count <= 8 || KIND == I4_GATE_UP) {  // two matrices and sixteen rows do not fit the registers
+    int4_few<GP, ZEROS, 1, 2, KIND, KT>(P, red, e, first, count, perm, ok, rt0, rt1);
+  } else if constexpr (KIND != I4_GATE_UP) {
+    int4_few<GP, ZEROS, 1, 4, KIND, KT>(P, red, e, first, count, perm, ok, rt0, rt1);
+  }
+}
+
+// LDS of k_int4_one's rows; more than this and the other kernel takes them.
+constexpr size_t ONE_LDS = 96 << 10;
+size_t one_lds(int rows, int cols) { return 16 + (size_t)rows * (int4_ktiles(cols) * 256 + 16); }
+
+template <int GP, int TERMS, int KIND, int DEPTH>
+hipError_t one(const Int4Params& p, int items, int rows, hipStream_t s, const LaunchEvents* ev) {
   const int steps = int4_ktiles(p.cols) * (KIND == I4_DOWN_SUM ? p.top_k : 1);
   const dim3 g((unsigned)int4_rtiles(p.rows), (unsigned)items), b(64 * (steps < FEW_WAVES ? steps : FEW_WAVES));
-  if (ev) hipExtLaunchKernelGGL((k_int4_few<GP, TERMS, NR, KIND>), g, b, 0, s, ev->start, ev->stop, 0, p);
-  else hipLaunchKernelGGL((k_int4_few<GP, TERMS, NR, KIND>), g, b, 0, s, p);
-  return hipGetLastError();
+  const unsigned lds = (unsigned)one_lds(rows, p.cols);
+  auto go = [&](auto k) {
+    if (ev) hipExtLaunchKernelGGL(k, g, b, lds, s, ev->start, ev->stop, 0, p);
+    else hipLaunchKernelGGL(k, g, b, lds, s, p);
+    return hipGetLastError();
+  };
+  return int4_zeros(p.fmt) ? go(k_int4_one<GP, true, TERMS, KIND, DEPTH>) : go(k_int4_one<GP, false, TERMS, KIND, DEPTH>);
+}
+
+// Row tiles of a work-group: few enough that every CU has two of them, at most 16.
+#ifndef MOEQ_I4_FEW_WGS
+#define MOEQ_I4_FEW_WGS 768
+#endif
+template <int GP, int KIND>
+hipError_t few(const Int4Params& p, int items, hipStream_t s, const LaunchEvents* ev) {
+  const long rt = int4_rtiles(p.rows);
+  const int rb = (int)std::min(16l, std::max(1l, rt * items / MOEQ_I4_FEW_WGS));
+  const dim3 g((unsigned)((rt + rb - 1) / rb), (unsigned)items), b(64 * FEW_WAVES);
+  const int kt = (int4_ktiles(p.cols) + FEW_WAVES - 1) / FEW_WAVES;
+  auto go = [&](auto k) {
+    if (ev) hipExtLaunchKernelGGL(k, g, b, 0, s, ev->start, ev->stop, 0, p, rb);
+    else hipLaunchKernelGGL(k, g, b, 0, s, p, rb);
+    return hipGetLastError();
+  };
+  auto by_k = [&](auto z) {
+    constexpr bool Z = decltype(z)::value;
+    if (kt <= 1) return go(k_int4_few<GP, Z, KIND, 1>);
+    if (kt <= 2) return go(k_int4_few<GP, Z, KIND, 2>);
+    return go(k_int4_few<GP, Z, KIND, 4>);
+  };
+  return int4_zeros(p.fmt) ? by_k(std::true_type()) : by_k(std::false_type());
 }
 
 template <int GP>
 hipError_t few_kind(int kind, const Int4Params& p, int items, hipStream_t s, const LaunchEvents* ev) {
-  // Tokens of a tile: as many as one item can hold.
-  const int rows = kind == I4_LINEAR ? p.T : p.grouped ? p.T : 1;
   switch (kind) {
-    case I4_LINEAR: {
-      if (rows <= 4) return few<GP, 1, 1, I4_LINEAR>(p, 1, s, ev);
-      if (rows <= 8) return few<GP, 1, 2, I4_LINEAR>(p, 1, s, ev);
-      Int4Params q = p;
-      for (long t0 = 0; t0 < p.T; t0 += 16L * 65535) {  // grid rows
-        const int n = (int)(p.T - t0 < 16L * 65535 ? p.T - t0 : 16L * 65535);
-        q.T = n;
-        q.act = p.act + (size_t)t0 * p.pitch;
-        q.y = (uint8_t*)p.y + (size_t)t0 * p.rows * (p.out_bf16 ? 2 : 4);
-        const hipError_t e = few<GP, 1, 4, I4_LINEAR>(q, (n + 15) / 16, s, ev);
-        if (e != hipSuccess) return e;
-      }
-      return hipSuccess;
-    }
+    case I4_LINEAR:
+      if (p.T <= 4 && one_lds(p.T, p.cols) <= ONE_LDS) return one<GP, 1, I4_LINEAR, 4>(p, 1, p.T, s, ev);
+      return few<GP, I4_LINEAR>(p, (p.T + 15) / 16, s, ev);
     case I4_GATE_UP:
-      if (rows <= 4) return few<GP, 1, 1, I4_GATE_UP>(p, items, s, ev);
-      if (rows <= 8) return few<GP, 1, 2, I4_GATE_UP>(p, items, s, ev);
-      return few<GP, 1, 4, I4_GATE_UP>(p, items, s, ev);
-    case I4_DOWN_SUM: return few<GP, 3, 3, I4_DOWN_SUM>(p, items, s, ev);
-    case I4_DOWN_PART: return few<GP, 3, 3, I4_DOWN_PART>(p, items, s, ev);
+      return p.grouped ? few<GP, I4_GATE_UP>(p, items, s, ev) : one<GP, 1, I4_GATE_UP, 4>(p, items, 1, s, ev);
+    case I4_DOWN_SUM: return one<GP, 3, I4_DOWN_SUM, 12>(p, items, 3 * p.top_k, s, ev);
+    case I4_DOWN_PART: return few<GP, I4_DOWN_PART>(p, items, s, ev);
   }
   return hipErrorInvalidValue;
 }
 
 }  // namespace
 
+bool int4_one_fits(int kind, int top_k, int cols) {
+  return one_lds(kind == I4_DOWN_SUM ? 3 * top_k : 1, cols) <= ONE_LDS;
+}
+
 hipError_t launch_int4_few(int kind, const Int4Params& p, int items, hipStream_t s, const LaunchEvents* ev) {
   if (!is_int4(p.fmt) || p.T < 1 || items < 1 || items > 65535 || p.rows < 1 || p.rows > INT4_MAX_ROWS || p.cols < 32 ||
       p.cols > INT4_MAX_COLS || p.cols % int4_group(p.fmt) || p.pitch % 8 || p.term % 8)
     return hipErrorInvalidValue;
+  if ((kind == I4_DOWN_SUM || (kind == I4_GATE_UP && !p.grouped)) && !int4_one_fits(kind, p.top_k, p.cols))
+    return hipErrorInvalidValue;
+  if (kind == I4_LINEAR && p.T > INT4_FEW_T) return hipErrorInvalidValue;
   switch (int4_group(p.fmt)) {
     case 32: return few_kind<4>(kind, p, items, s, ev);
     case 64: return few_kind<2>(kind, p, items, s, ev);

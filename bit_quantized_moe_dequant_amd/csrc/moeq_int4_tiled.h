@@ -64,64 +64,37 @@ __device__ __forceinline__ void spread() {
   }
 }
 
+// One work-group's tile: row block bm of expert e, activation rows first .. + count (LINEAR), or
+// the pairs perm[0 .. count); count at most 16 NT WN.
 template <int KIND, int GP, bool ZEROS, bool SCALED, int WM, int WN, int NM, int NT>
-__global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_int4_tiled(Int4Rows P) {
-  constexpr int TOK = 16 * NT * WN;            // activation rows of a work-group
+__device__ __forceinline__ void int4_tile(const Int4Rows& P, uint8_t* lds, int bm, int e, int first, int count,
+                                          const int32_t* perm) {
+  constexpr int TOK = 16 * NT * WN;
   constexpr int TERMS = KIND == I4_DOWN_PART ? 2 : 1, ROWS = TERMS * TOK, STAGE = ROWS * 256;
-  constexpr int COPIES = ROWS / 4 / (WM * WN);  // of a wave per step, four LDS rows each
-  static_assert(COPIES * 4 * WM * WN == ROWS, "whole copies");
+  // copies of a wave per step, four LDS rows each (the waves past the last row repeat the first)
+  constexpr int COPIES = (ROWS / 4 + WM * WN - 1) / (WM * WN);
+  static_assert(ROWS % (4 * COPIES) == 0, "no copy passes the end");
   constexpr int PAIRS = KIND == I4_GATE_UP ? 2 : 1;  // matrices side by side
   constexpr int RT = NM / PAIRS;               // row tiles of a wave
-  __shared__ __attribute__((aligned(16))) uint8_t lds[I4_STAGES * STAGE];
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ktiles = int4_ktiles(P.cols), kpad = ktiles * 128, rtiles = int4_rtiles(P.rows);
-  const int nbm = (rtiles + WM * RT - 1) / (WM * RT);
   const int wm = wave % WM, wn = wave / WM;
+  const int row0 = 4 * COPIES * wave % ROWS;
 
-  // tile of this work-group: row block bm, activation rows `first` .. + count
-  int bm, e, first, count;
-  const int32_t* perm = nullptr;
-  if constexpr (KIND == I4_LINEAR) {
-    int bn;
-    tile_of(blockIdx.x, nbm, (P.T + TOK - 1) / TOK, bm, bn);
-    first = bn * TOK;
-    count = min(TOK, P.T - first);
-    e = P.expert;
-  } else {
-    // the row blocks of a chunk of tokens on one XCD: they share the tokens in its L2
-    static_assert(TOK == PREFILL_MC, "chunks of the routing");
-    const int l = blockIdx.x / 8, q = l / nbm * 8 + (int)(blockIdx.x % 8);
-    bm = l % nbm;
-    if (q >= P.route.n_chunks()[0]) return;
-    e = P.route.chunk_e()[q];
-    const int p0 = P.route.offsets()[e], m0 = P.route.chunk_m0()[q];
-    count = min(TOK, P.route.offsets()[e + 1] - p0 - m0);
-    perm = P.route.perm() + p0 + m0;
-    first = 0;
-    if (e >= P.n_experts) {  // ids out of range
-      if constexpr (KIND == I4_DOWN_PART)
-        for (int i = threadIdx.x; i < count * 16 * WM * RT; i += 64 * WM * WN) {
-          const int r = bm * 16 * WM * RT + i % (16 * WM * RT);
-          if (r < P.rows) ((float*)P.y)[(size_t)perm[i / (16 * WM * RT)] * P.rows + r] = 0.f;
-        }
-      return;
-    }
-  }
-
-  // this lane's part of a wave's copies: LDS row 4 (COPIES wave + i) + lane / 16, term by term
+  // this lane's part of a wave's copies: LDS row row0 + 4 i + lane / 16, term by term
   const uint16_t* abase = P.act + (KIND == I4_LINEAR ? (size_t)first * kpad : 0);
   int off[COPIES];
 #pragma unroll
   for (int i = 0; i < COPIES; i++) {
-    const int row = 4 * (COPIES * wave + i) + (lane >> 4), term = row / TOK, t = min(row % TOK, count - 1);
+    const int row = row0 + 4 * i + (lane >> 4), term = row / TOK, t = min(row % TOK, count - 1);
     int a = t;
     if constexpr (KIND == I4_GATE_UP) a = perm[t] / P.top_k;
     if constexpr (KIND == I4_DOWN_PART) a = perm[t];
     off[i] = (a * TERMS + term) * kpad * 2 + 16 * ((lane & 15) ^ (row & 15));
   }
   auto copy = [&](int s, int to) {  // step s into buffer `to`
-    uint8_t* dst = lds + to * STAGE + 1024 * COPIES * wave;
+    uint8_t* dst = lds + to * STAGE + 256 * row0;
 #pragma unroll
     for (int i = 0; i < COPIES; i++) copy16(reinterpret_cast<const int8_t*>(abase), off[i], s * 256, dst + 1024 * i);
   };
@@ -299,11 +272,62 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_int4_tiled(Int4Ro
   }
 }
 
-template <int KIND, int GP, bool SCALED, int WM, int WN, int NM, int NT>
-hipError_t tiled(const Int4Rows& p, long blocks, hipStream_t s) {
-  const dim3 g((unsigned)blocks), b(64 * WM * WN);
-  if (int4_zeros(p.fmt)) hipLaunchKernelGGL((k_int4_tiled<KIND, GP, true, SCALED, WM, WN, NM, NT>), g, b, 0, s, p);
-  else hipLaunchKernelGGL((k_int4_tiled<KIND, GP, false, SCALED, WM, WN, NM, NT>), g, b, 0, s, p);
+template <int GP, bool ZEROS, bool SCALED, int WM, int WN, int NM, int NT>
+__global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_int4_linear(Int4Rows P) {
+  constexpr int TOK = 16 * NT * WN;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[I4_STAGES * TOK * 256];
+  int bm, bn;
+  tile_of(blockIdx.x, (int4_rtiles(P.rows) + WM * NM - 1) / (WM * NM), (P.T + TOK - 1) / TOK, bm, bn);
+  int4_tile<I4_LINEAR, GP, ZEROS, SCALED, WM, WN, NM, NT>(P, lds, bm, P.expert, bn * TOK, min(TOK, P.T - bn * TOK), nullptr);
+}
+
+// NT: token tiles of a work-group at most; as many are multiplied as its pairs need.
+template <int KIND, int GP, bool ZEROS, int NM, int NT>
+__global__ __launch_bounds__(512, 2) void k_int4_experts(Int4Rows P) {
+  constexpr int TOK = 16 * NT, RT = NM / (KIND == I4_GATE_UP ? 2 : 1), PARTS = PREFILL_MC / TOK;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[I4_STAGES * (KIND == I4_DOWN_PART ? 2 : 1) * TOK * 256];
+  const int nbm = (int4_rtiles(P.rows) + 8 * RT - 1) / (8 * RT);
+  // the row blocks of a chunk of tokens on one XCD: they share the tokens in its L2
+  const int l = blockIdx.x / 8, q = l / nbm * 8 + (int)(blockIdx.x % 8), bm = l % nbm, chunk = q / PARTS;
+  if (chunk >= P.route.n_chunks()[0]) return;
+  const int e = P.route.chunk_e()[chunk];
+  const int p0 = P.route.offsets()[e], m0 = P.route.chunk_m0()[chunk] + q % PARTS * TOK;
+  const int count = min(TOK, P.route.offsets()[e + 1] - p0 - m0);
+  if (count <= 0) return;
+  const int32_t* perm = P.route.perm() + p0 + m0;
+  if (e >= P.n_experts) {  // ids out of range
+    if constexpr (KIND == I4_DOWN_PART)
+      for (int i = threadIdx.x; i < count * 128 * RT; i += 512) {
+        const int r = bm * 128 * RT + i % (128 * RT);
+        if (r < P.rows) ((float*)P.y)[(size_t)perm[i / (128 * RT)] * P.rows + r] = 0.f;
+      }
+    return;
+  }
+  if (NT == 1 || count <= 16) return int4_tile<KIND, GP, ZEROS, false, 8, 1, NM, 1>(P, lds, bm, e, 0, count, perm);
+  if constexpr (NT >= 2)
+    if (NT == 2 || count <= 32) return int4_tile<KIND, GP, ZEROS, false, 8, 1, NM, 2>(P, lds, bm, e, 0, count, perm);
+  if constexpr (NT >= 4) {
+    if (count <= 48) return int4_tile<KIND, GP, ZEROS, false, 8, 1, NM, 3>(P, lds, bm, e, 0, count, perm);
+    int4_tile<KIND, GP, ZEROS, false, 8, 1, NM, 4>(P, lds, bm, e, 0, count, perm);
+  }
+}
+
+template <int GP, bool SCALED, int WM, int WN, int NM, int NT>
+hipError_t linear(const Int4Rows& p, hipStream_t s) {
+  const long rows = 16 * WM * NM, tok = 16 * WN * NT;
+  const dim3 g((unsigned)((p.rows + rows - 1) / rows * ((p.T + tok - 1) / tok))), b(64 * WM * WN);
+  if (int4_zeros(p.fmt)) hipLaunchKernelGGL((k_int4_linear<GP, true, SCALED, WM, WN, NM, NT>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((k_int4_linear<GP, false, SCALED, WM, WN, NM, NT>), g, b, 0, s, p);
+  return hipGetLastError();
+}
+
+template <int KIND, int GP, int NM, int NT>
+hipError_t experts(const Int4Rows& p, hipStream_t s) {
+  constexpr int RT = NM / (KIND == I4_GATE_UP ? 2 : 1);
+  const long items = (long)RouteView::max_chunks(p.n_experts, p.T * p.top_k) * (PREFILL_MC / (16 * NT));
+  const dim3 g((unsigned)((int4_rtiles(p.rows) + 8 * RT - 1) / (8 * RT) * ((items + 7) / 8 * 8)));
+  if (int4_zeros(p.fmt)) hipLaunchKernelGGL((k_int4_experts<KIND, GP, true, NM, NT>), g, dim3(512), 0, s, p);
+  else hipLaunchKernelGGL((k_int4_experts<KIND, GP, false, NM, NT>), g, dim3(512), 0, s, p);
   return hipGetLastError();
 }
 

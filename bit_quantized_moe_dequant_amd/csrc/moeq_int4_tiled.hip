@@ -68,20 +68,21 @@ __global__ __launch_bounds__(256) void k_int4_rows(const void* x, int cols, int 
   }
 }
 
+#ifndef MOEQ_I4_WIDE
+#define MOEQ_I4_WIDE 8
+#endif
 template <int GP>
 hipError_t tiled_kind(int kind, const Int4Rows& p, hipStream_t s) {
-  const long rt = int4_rtiles(p.rows);
-  auto blocks = [&](int rows, int tok) { return (16 * rt + rows - 1) / rows * ((p.T + tok - 1) / tok); };
+  auto blocks = [&](int rows, int tok) { return (p.rows + (long)rows - 1) / rows * ((p.T + tok - 1) / tok); };
   if (kind == I4_LINEAR) {
-    if (p.out_bf16 && blocks(256, 128) >= 192) return launch_int4_scaled(p, blocks(256, 128), s);
-    if (blocks(256, 64) >= 192) return tiled<I4_LINEAR, GP, false, 8, 1, 2, 4>(p, blocks(256, 64), s);
-    if (p.T > 32) return tiled<I4_LINEAR, GP, false, 4, 1, 1, 4>(p, blocks(64, 64), s);
-    return tiled<I4_LINEAR, GP, false, 4, 1, 1, 2>(p, blocks(64, 32), s);
+    if (p.out_bf16 && blocks(256, 128) >= 192) return launch_int4_scaled(p, s);
+    if (blocks(256, 64) >= 192) return linear<GP, false, 8, 1, 2, 4>(p, s);
+    if (p.T > 32) return linear<GP, false, 4, 1, 1, 4>(p, s);
+    return linear<GP, false, 4, 1, 1, 2>(p, s);
   }
-  const int pairs = p.T * p.top_k;
-  const long chunks = (RouteView::max_chunks(p.n_experts, pairs) + 7) / 8 * 8;
-  if (kind == I4_GATE_UP) return tiled<I4_GATE_UP, GP, false, 8, 1, 2, 4>(p, (rt + 7) / 8 * chunks, s);
-  return tiled<I4_DOWN_PART, GP, false, 8, 1, 2, 4>(p, (rt + 15) / 16 * chunks, s);
+  const bool wide = (long)p.T * p.top_k >= (long)MOEQ_I4_WIDE * p.n_experts;
+  if (kind == I4_GATE_UP) return wide ? experts<I4_GATE_UP, GP, 2, 4>(p, s) : experts<I4_GATE_UP, GP, 2, 1>(p, s);
+  return wide ? experts<I4_DOWN_PART, GP, 2, 4>(p, s) : experts<I4_DOWN_PART, GP, 2, 1>(p, s);
 }
 
 }  // namespace

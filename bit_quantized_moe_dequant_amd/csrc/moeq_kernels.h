@@ -286,7 +286,9 @@ hipError_t launch_dequant_int8(const int8_t* w, const float* ws, int rows, int c
 hipError_t launch_pack_int4(int fmt, const uint8_t* codes, const uint16_t* scales, bool scales_bf16, const uint8_t* zeros,
                             int rows, int cols, int n, uint8_t* data, uint8_t* out_scales, float* scale2, hipStream_t s);
 hipError_t launch_dequant_int4(int fmt, const WeightRef& w, int rows, int cols, int expert, float* out, hipStream_t s);
-// Products for a few rows to an expert (any number is right, in tiles of up to 16 or 8 rows).
+// Products for a few rows to an expert (any number is right, in tiles of up to 16 or 4 rows). One
+// token or pair at a time (I4_DOWN_SUM, I4_GATE_UP unless `grouped`) has to fit: int4_one_fits.
+bool int4_one_fits(int kind, int top_k, int cols);
 hipError_t launch_int4_few(int kind, const Int4Params& p, int items, hipStream_t s, const LaunchEvents* ev = nullptr);
 // fp32 rows -> their three bf16 terms [n_rows][3][cols].
 hipError_t launch_int4_terms(const float* h, size_t n_rows, int cols, uint16_t* planes, hipStream_t s);
@@ -294,7 +296,7 @@ bool int4_rows_fit(size_t n_rows, int terms, int cols);
 size_t int4_rows_bytes(size_t n_rows, int terms, int cols);
 // bf16 rows -> one fp16 term, fp32 rows -> two (see Int4Rows).
 hipError_t launch_int4_rows(bool in_f32, const void* x, size_t n_rows, int cols, uint16_t* out, float* scale, hipStream_t s);
-hipError_t launch_int4_scaled(const Int4Rows& p, long blocks, hipStream_t s);  // of 256 rows x 128 tokens
+hipError_t launch_int4_scaled(const Int4Rows& p, hipStream_t s);  // bf16 linear in tiles of 256 rows x 128 tokens
 hipError_t launch_int4_tiled(int kind, const Int4Rows& p, hipStream_t s);
 
 // Chunk geometry: weights per 16-byte chunk; lanes per row and chunks per lane.
