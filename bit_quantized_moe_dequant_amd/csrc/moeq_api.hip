@@ -127,15 +127,22 @@ bool prefill_buffers(const moeq_layer* L, int T) {
   return T >= PREFILL_MIN_T && (L->gate.fmt == MOEQ_FMT_MXFP4 || L->down.fmt == MOEQ_FMT_MXFP4);
 }
 
-// INT4: from this many pairs per expert on (and while 32-bit offsets reach every row) as a
-// tiled product over each expert's tokens.
-#ifndef MOEQ_INT4_TILED_FROM
-#define MOEQ_INT4_TILED_FROM 8.0
+double touched_experts(const moeq_layer* L, int T);
+
+// INT4 projections pair by pair (each pair's expert read for itself, h in one launch more) or
+// tiled over each expert's tokens (four launches more): pair by pair while what is read twice
+// takes less than those launches. MOEQ_INT4_DIRECT_US at 4.5 TB/s; 4096 x 2048 experts, 6 of 256:
+// 1 / 2 / 4 / 8 tokens 24 / 36 / 64 / 130 us so, tiled 8 / 12 / 16 tokens 149 / 178 / 227.
+#ifndef MOEQ_INT4_DIRECT_US
+#define MOEQ_INT4_DIRECT_US 15.0
 #endif
-bool int4_many(const moeq_layer* L, int T) {
-  const size_t P = (size_t)T * L->top_k;
-  return T > 1 && P >= MOEQ_INT4_TILED_FROM * L->n_experts && int4_rows_fit(T, 1, L->hidden) && int4_rows_fit(P, 2, L->inter);
+bool int4_direct(const moeq_layer* L, int T) {
+  if (T == 1) return true;
+  const double extra = (double)T * L->top_k - touched_experts(L, T);
+  return (long)T * L->top_k <= 65535 && extra * 1.6 * L->hidden * L->inter < MOEQ_INT4_DIRECT_US * 4.5e6;
 }
+bool int4_gu_direct(const moeq_layer* L, int T) { return int4_direct(L, T) && int4_one_fits(I4_GATE_UP, L->top_k, L->hidden); }
+bool int4_dn_direct(const moeq_layer* L, int T) { return int4_direct(L, T) && int4_one_fits(I4_DOWN_SUM, L->top_k, L->inter); }
 
 struct WsLayout {
   size_t route, h, partial, xq, xs, hq, hs, dq, ds, h4, xr, xrs, hr, hrs, total;
@@ -153,7 +160,7 @@ WsLayout ws_layout(const moeq_layer* L, int T) {
   w.h = off;
   off += align_up(P * L->inter * 4, 256);
   w.partial = off;
-  off += T > 1 || is_int4(L->down.fmt) ? align_up(P * L->hidden * 4, 256) : 0;
+  off += T > 1 || (is_int4(L->down.fmt) && !int4_dn_direct(L, T)) ? align_up(P * L->hidden * 4, 256) : 0;
   w.xq = w.xs = w.hq = w.hs = w.dq = w.ds = 0;
   w.err = nullptr;
   if (T > 1 && L->down.fmt == MOEQ_FMT_Q2_K && dn_q2k_g_fits(L->hidden, L->inter)) {
@@ -164,14 +171,13 @@ WsLayout ws_layout(const moeq_layer* L, int T) {
     off += align_up(dn_q2k_g_scale_bytes((long)P, L->inter), 256);
   }
   w.h4 = w.xr = w.xrs = w.hr = w.hrs = 0;
-  const bool many = int4_many(L, T);
-  if (is_int4(L->gate.fmt) && many) {  // the tokens' fp16 rows and their scales
+  if (is_int4(L->gate.fmt) && !int4_gu_direct(L, T)) {  // the tokens' fp16 rows and their scales
     w.xr = off;
     off += align_up(int4_rows_bytes(T, 1, L->hidden), 256);
     w.xrs = off;
     off += align_up((size_t)T * 4, 256);
   }
-  if (is_int4(L->down.fmt) && many) {  // and those of h
+  if (is_int4(L->down.fmt) && !int4_dn_direct(L, T)) {  // and those of h
     w.hr = off;
     off += align_up(int4_rows_bytes(P, 2, L->inter), 256);
     w.hrs = off;
@@ -239,10 +245,13 @@ GemvParams gemv_params(const moeq_layer* L, const moeq_weight& a, const moeq_wei
 #ifndef MOEQ_GROUPED_WIDE_FROM
 #define MOEQ_GROUPED_WIDE_FROM 2.5
 #endif
-double pairs_per_expert(const moeq_layer* L, int T) {
+double touched_experts(const moeq_layer* L, int T) {
   const double E = L->n_experts, K = L->top_k;
-  const double touched = E * (1.0 - std::pow(1.0 - K / E, (double)T));
-  return (double)T * K / (touched > 1.0 ? touched : 1.0);
+  return E * (1.0 - std::pow(1.0 - K / E, (double)T));
+}
+double pairs_per_expert(const moeq_layer* L, int T) {
+  const double touched = touched_experts(L, T);
+  return (double)T * L->top_k / (touched > 1.0 ? touched : 1.0);
 }
 bool grouped_wide(const moeq_layer* L, int T) { return pairs_per_expert(L, T) >= MOEQ_GROUPED_WIDE_FROM; }
 
@@ -316,13 +325,8 @@ bool scales16(const moeq_weight& w) {
 #ifndef MOEQ_Q2K_DIRECT_BELOW
 #define MOEQ_Q2K_DIRECT_BELOW 1.06
 #endif
-// INT4: pair by pair up to this many tokens.
-#ifndef MOEQ_INT4_DIRECT_MAX_T
-#define MOEQ_INT4_DIRECT_MAX_T 4
-#endif
 bool gu_direct(const moeq_layer* L, int T) {
-  if (is_int4(L->gate.fmt))
-    return T <= MOEQ_INT4_DIRECT_MAX_T && !int4_many(L, T) && int4_one_fits(I4_GATE_UP, L->top_k, L->hidden);
+  if (is_int4(L->gate.fmt)) return int4_gu_direct(L, T);
   if (T == 1) return true;
   if (L->gate.fmt == MOEQ_FMT_IQ2_XXS)  // the dequantize + GEMV over every pair
     return T >= 1 && L->up.fmt == MOEQ_FMT_IQ2_XXS && pairs_per_expert(L, T) < MOEQ_IQ2_DIRECT_BELOW;
@@ -333,8 +337,7 @@ bool gu_direct(const moeq_layer* L, int T) {
          scales16(L->gate) && scales16(L->up);
 }
 bool dn_direct(const moeq_layer* L, int T, const float* h) {
-  if (is_int4(L->down.fmt))
-    return T <= MOEQ_INT4_DIRECT_MAX_T && !int4_many(L, T) && int4_one_fits(I4_DOWN_SUM, L->top_k, L->inter);
+  if (is_int4(L->down.fmt)) return int4_dn_direct(L, T);
   if (T == 1) return true;
   if (T < 1 || !aligned(h, 16)) return false;
   if (L->down.fmt == MOEQ_FMT_MXFP4)
@@ -342,11 +345,6 @@ bool dn_direct(const moeq_layer* L, int T, const float* h) {
   if (L->down.fmt == MOEQ_FMT_Q2_K)
     return pairs_per_expert(L, T) < MOEQ_Q2K_DIRECT_BELOW && down1_q2k_fits(L->hidden, L->inter, L->top_k);
   return false;
-}
-
-int route_slots(const moeq_layer* L, int T) {
-  const int pairs = T * L->top_k;
-  return (pairs < L->n_experts ? pairs : L->n_experts) + 1;
 }
 
 Int4Params int4_params(const moeq_weight& w, const void* act, size_t pitch, size_t term, int T, void* y) {
@@ -382,14 +380,20 @@ Int4Rows int4_rows(const moeq_weight& w, const moeq_layer* L, int T, const uint1
   return p;
 }
 
-// out_terms: h as bf16 terms, for run_down_int4, instead of fp32.
+// The stages of one token need no moeq_route before them; where one is tiled all the same (more
+// columns than a work-group holds), it sorts the token's pairs itself.
+int route_one(const moeq_layer* L, const int32_t* ids, void* ws, const WsLayout& lay, hipStream_t s) {
+  return hip_rc(launch_route(ids, L->top_k, L->n_experts, route_view(L, ws, lay), err_of(ws, lay), s));
+}
+
+// out_terms: h as bf16 terms, for run_down_int4_direct, instead of fp32.
 int run_gate_up_int4(const moeq_layer* L, const void* x, const int32_t* ids, int T, void* h, bool out_terms, void* ws,
                      const WsLayout& lay, hipStream_t s, const LaunchEvents* ev = nullptr) {
   if (lay.xr) {
     uint16_t* xr = (uint16_t*)((uint8_t*)ws + lay.xr);
     float* xrs = (float*)((uint8_t*)ws + lay.xrs);
-    const int rc = hip_rc(launch_int4_rows(false, x, T, L->hidden, xr, xrs, s));
-    if (rc) return rc;
+    int rc = T == 1 ? route_one(L, ids, ws, lay, s) : MOEQ_OK;
+    if (rc || (rc = hip_rc(launch_int4_rows(false, x, T, L->hidden, xr, xrs, s)))) return rc;
     Int4Rows p = int4_rows(L->gate, L, T, xr, xrs, h);
     p.w[1] = ref_of(L->up);
     p.route = route_view(L, ws, lay);
@@ -399,30 +403,22 @@ int run_gate_up_int4(const moeq_layer* L, const void* x, const int32_t* ids, int
   p.w[1] = ref_of(L->up);
   p.top_k = L->top_k;
   p.n_experts = L->n_experts;
-  p.grouped = !gu_direct(L, T);
   p.ids = ids;
-  p.route = route_view(L, ws, lay);
   p.out_terms = out_terms;
   p.err = err_of(ws, lay);
-  return hip_rc(launch_int4_few(I4_GATE_UP, p, p.grouped ? route_slots(L, T) : T * L->top_k, s, ev));
+  return hip_rc(launch_int4_few(I4_GATE_UP, p, T * L->top_k, s, ev));
 }
 
 // h: bf16 terms, [pairs][3][inter].
-int run_down_int4(const moeq_layer* L, const uint16_t* h, bool direct, const int32_t* ids, const float* rw, int T, float* y,
-                  void* ws, const WsLayout& lay, hipStream_t s) {
-  float* partial = (float*)((uint8_t*)ws + lay.partial);
-  Int4Params p = int4_params(L->down, h, (size_t)3 * L->inter, L->inter, T, direct ? y : partial);
+int run_down_int4_direct(const moeq_layer* L, const uint16_t* h, const int32_t* ids, const float* rw, int T, float* y, void* ws,
+                         const WsLayout& lay, hipStream_t s) {
+  Int4Params p = int4_params(L->down, h, (size_t)3 * L->inter, L->inter, T, y);
   p.top_k = L->top_k;
   p.n_experts = L->n_experts;
-  p.grouped = !direct;
   p.ids = ids;
   p.rw = rw;
-  p.route = route_view(L, ws, lay);
   p.err = err_of(ws, lay);
-  if (direct) return hip_rc(launch_int4_few(I4_DOWN_SUM, p, T, s));
-  const int rc = hip_rc(launch_int4_few(I4_DOWN_PART, p, route_slots(L, T), s));
-  if (rc) return rc;
-  return hip_rc(launch_combine(partial, T, L->top_k, L->hidden, y, s));
+  return hip_rc(launch_int4_few(I4_DOWN_SUM, p, T, s));
 }
 
 int run_gate_up(const moeq_layer* L, const void* x, const int32_t* ids, int T, float* h, void* ws, const WsLayout& lay,
@@ -473,8 +469,8 @@ int run_down(const moeq_layer* L, const float* h, const int32_t* ids, const floa
     uint16_t* hr = (uint16_t*)((uint8_t*)ws + lay.hr);
     float* hrs = (float*)((uint8_t*)ws + lay.hrs);
     float* partial = (float*)((uint8_t*)ws + lay.partial);
-    int rc = hip_rc(launch_int4_rows(true, h, (size_t)T * L->top_k, L->inter, hr, hrs, s));
-    if (rc) return rc;
+    int rc = T == 1 ? route_one(L, ids, ws, lay, s) : MOEQ_OK;
+    if (rc || (rc = hip_rc(launch_int4_rows(true, h, (size_t)T * L->top_k, L->inter, hr, hrs, s)))) return rc;
     Int4Rows p = int4_rows(L->down, L, T, hr, hrs, partial);
     p.route = route_view(L, ws, lay);
     p.rw = rw;
@@ -484,7 +480,7 @@ int run_down(const moeq_layer* L, const float* h, const int32_t* ids, const floa
   if (is_int4(L->down.fmt)) {
     uint16_t* terms = (uint16_t*)((uint8_t*)ws + lay.h4);
     const int rc = hip_rc(launch_int4_terms(h, (size_t)T * L->top_k, L->inter, terms, s));
-    return rc ? rc : run_down_int4(L, terms, dn_direct(L, T, h), ids, rw, T, y, ws, lay, s);
+    return rc ? rc : run_down_int4_direct(L, terms, ids, rw, T, y, ws, lay, s);
   }
   if (dn_direct(L, T, h)) {
     Down1Params d = down1_params(L, h, ids, rw, T, err_of(ws, lay));
@@ -1052,7 +1048,7 @@ int forward(const moeq_layer* L, const void* x, const int32_t* ids, const float*
             const WsLayout& lay, hipStream_t s) {
   int rc;
   float* h = (float*)((uint8_t*)ws + lay.h);
-  if (!(gu_direct(L, T) && dn_direct(L, T, h))) {
+  if (T > 1 && !(gu_direct(L, T) && dn_direct(L, T, h))) {
     rc = hip_rc(launch_route(ids, T * L->top_k, L->n_experts, route_view(L, ws, lay), err_of(ws, lay), s));
     if (rc) return rc;
   }
@@ -1063,10 +1059,10 @@ int forward(const moeq_layer* L, const void* x, const int32_t* ids, const float*
   uint8_t* xs = (uint8_t*)ws + lay.xs;
   uint8_t* hq = (uint8_t*)ws + lay.hq;
   uint8_t* hs = (uint8_t*)ws + lay.hs;
-  if (is_int4(L->gate.fmt) && is_int4(L->down.fmt) && lay.h4) {
+  if (is_int4(L->gate.fmt) && is_int4(L->down.fmt) && !lay.xr && !lay.hr) {
     uint16_t* terms = (uint16_t*)((uint8_t*)ws + lay.h4);
     if ((rc = run_gate_up_int4(L, x, ids, T, terms, true, ws, lay, s))) return rc;
-    return run_down_int4(L, terms, dn_direct(L, T, h), ids, rw, T, y, ws, lay, s);
+    return run_down_int4_direct(L, terms, ids, rw, T, y, ws, lay, s);
   }
   if (gu_pf) {  // W4A8: MXFP8 x; fp32 h too when the down projection needs it
     if ((rc = hip_rc(launch_quant_mxfp8(0, x, T, L->hidden, xq, xs, s)))) return rc;

@@ -230,332 +230,308 @@ __device__ __forceinline__ void int4_store(const Int4Params& P, int e, bool ok, 
     } else {
       ((float*)P.y)[pair * P.rows + r] = h;
     }
-  } else if constexpr (KIND == I4_DOWN_SUM) {
-    ((float*)P.y)[pair * P.rows + r] = v[0];
   } else {
-    ((float*)P.y)[pair * P.rows + r] = ok ? v[0] * P.w[0].scale2[e] * P.rw[pair] : 0.f;
+    ((float*)P.y)[pair * P.rows + r] = v[0];
   }
 }
 
-// One token (or pair; I4_DOWN_SUM: a token's pairs one behind the other) or up to four of a
-// linear, whose rows lie in LDS. A work-group: 16 weight rows (of the gate and of the up matrix),
-// all of K, whose tiles its waves take in turn, DEPTH of them with their loads in flight at once,
-// issued before the activations are waited for; the waves' sums meet in LDS and are added in the
-// order of the waves. TERMS: bf16 terms of an activation. The lanes of operand A's unused rows
-// read zeros.
+// Waves of a work-group of k_int4_one: a token's down has no more work-groups than row tiles.
+constexpr int one_waves(int kind) { return kind == I4_DOWN_SUM ? 16 : FEW_WAVES; }
+
+// One token or pair (I4_DOWN_SUM: a token's pairs one behind the other), or up to four tokens of a
+// linear, in LDS. A work-group takes rb tiles of 16 weight rows (of the gate and of
+// the up matrix), one after another, and all of K, whose tiles its waves take in turn; the waves'
+// sums meet in LDS (two buffers, one barrier to a row tile) and are added in the order of the waves.
+// A wave's next DEPTH tiles are always on their way, those of the next row tile among them; the
+// first are asked for behind the activations' loads and before these are waited for. TERMS: bf16
+// terms of an activation. The lanes of operand A's unused rows read zeros.
 template <int GP, bool ZEROS, int TERMS, int KIND, int DEPTH>
-__global__ __launch_bounds__(64 * FEW_WAVES) void k_int4_one(Int4Params P) {
-  constexpr int NMAT = KIND == I4_GATE_UP ? 2 : 1, NR = TERMS, TOK = TERMS == 1 ? 4 : 1;
+__global__ __launch_bounds__(64 * one_waves(KIND)) void k_int4_one(Int4Params P, int rb) {
+  constexpr int NMAT = KIND == I4_GATE_UP ? 2 : 1, NR = TERMS, TOK = KIND == I4_DOWN_SUM ? 1 : 4;
+  constexpr int STAGE = KIND == I4_DOWN_SUM ? 5 : KIND == I4_LINEAR ? 4 : 1;  // 16-byte pieces of the rows to a thread
   extern __shared__ __attribute__((aligned(16))) uint8_t xs[];  // 16 bytes of zeros, then the rows
-  __shared__ float red[FEW_WAVES][NMAT][TOK][16];
+  __shared__ float red[2][one_waves(KIND)][NMAT][TOK][16];
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-  const int rt = blockIdx.x, item = blockIdx.y, ktiles = int4_ktiles(P.cols);
+  const int rt0 = blockIdx.x * rb, rt1 = min(rt0 + rb, int4_rtiles(P.rows));
+  const int item = blockIdx.y, ktiles = int4_ktiles(P.cols);
   const int parts = KIND == I4_DOWN_SUM ? P.top_k : 1, steps = parts * ktiles;
-  const int tok = KIND == I4_LINEAR ? P.T : 1;
 
+  const int here = KIND == I4_LINEAR ? P.T : 1;
+
+  // the rows, token by token or part by part, and term by term, `pitch` bytes apart
+  const int kpad = ktiles * 128, pitch = kpad * 2 + 16;
+  const int chunks = (KIND == I4_DOWN_SUM ? parts : here) * TERMS * (kpad / 8);
+  auto get = [&](int i) {
+    i = min(i, chunks - 1);
+    const int row = i / (kpad / 8), k = i % (kpad / 8) * 8;
+    size_t a = row / TERMS;
+    if constexpr (KIND == I4_DOWN_SUM) a += (size_t)item * P.top_k;
+    if constexpr (KIND == I4_GATE_UP) a = item / P.top_k;
+    u32x4 v = ld16(P.act + a * P.pitch + row % TERMS * P.term + min(k, P.cols - 8));
+    if (k >= P.cols) v = u32x4{0u, 0u, 0u, 0u};
+    return v;
+  };
+  auto put = [&](int i, u32x4 v) {
+    i = min(i, chunks - 1);
+    *reinterpret_cast<u32x4*>(xs + 16 + (size_t)(i / (kpad / 8)) * pitch + i % (kpad / 8) * 16) = v;
+  };
+  u32x4 rv[STAGE];
+#pragma unroll
+  for (int q = 0; q < STAGE; q++) rv[q] = get(threadIdx.x + q * blockDim.x);
+  if (threadIdx.x < 4) reinterpret_cast<uint32_t*>(xs)[threadIdx.x] = 0;
+  __builtin_amdgcn_sched_barrier(0);
+
+  // the expert; I4_DOWN_SUM: lane k holds part k's, and the factor of its sums (-1: skipped)
   int e = KIND == I4_LINEAR ? P.expert : 0;
+  float fac = 0.f;
   bool ok = true;
   if constexpr (KIND == I4_GATE_UP) {
     e = P.ids[item];
     ok = e >= 0 && e < P.n_experts;
-    if (!ok && rt == 0 && threadIdx.x == 0) atomicOr(P.err, 1u);
+    if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(P.err, 1u);
     if (!ok) e = 0;
   }
-
-  u32x4 wv[DEPTH][NMAT];
-  Side<GP, ZEROS, NMAT> side[DEPTH];
-  float fac[DEPTH];
-  bool live[DEPTH];
-  auto load = [&](int u0) {
-#pragma unroll
-    for (int d = 0; d < DEPTH; d++) {
-      const int u = min(u0 + d * waves, steps - 1);
-      live[d] = u0 + d * waves < steps && ok;
-      int kt = u;
-      if constexpr (KIND == I4_DOWN_SUM) {
-        const int k = u / ktiles;
-        kt = u % ktiles;
-        e = P.ids[(size_t)item * P.top_k + k];
-        const bool good = e >= 0 && e < P.n_experts;
-        if (!good && rt == 0 && lane == 0 && kt == 0 && live[d]) atomicOr(P.err, 1u);
-        live[d] = live[d] && good;
-        e = good ? e : 0;
-        fac[d] = P.rw[(size_t)item * P.top_k + k] * P.w[0].scale2[e];
+  if constexpr (KIND == I4_DOWN_SUM) {
+    e = -1;
+    if (lane < parts) {
+      e = P.ids[(size_t)item * P.top_k + lane];
+      if (e < 0 || e >= P.n_experts) {
+        if (blockIdx.x == 0 && wave == 0) atomicOr(P.err, 1u);
+        e = -1;
+      } else {
+        fac = P.rw[(size_t)item * P.top_k + lane] * P.w[0].scale2[e];
       }
-      int4_load(P, e, (size_t)rt * ktiles + kt, lane, wv[d], side[d]);
+    }
+  }
+
+  // A wave's tiles: row tile by row tile, step wave, wave + waves, ... of each
+  struct At {
+    int rt, u;
+  };
+  auto step = [&](At& a) {
+    a.u += waves;
+    if (a.u >= steps) {
+      a.u = wave;
+      a.rt++;
     }
   };
-  load(wave);
-
-  // the rows: token by token, or part by part and term by term, `pitch` bytes apart
-  const int kpad = ktiles * 128, pitch = kpad * 2 + 16, rows = KIND == I4_DOWN_SUM ? parts * TERMS : tok;
-  if (threadIdx.x < 4) reinterpret_cast<uint32_t*>(xs)[threadIdx.x] = 0;
-  for (int i = threadIdx.x; i < rows * (kpad / 8); i += blockDim.x) {
-    const int row = i / (kpad / 8), k = i % (kpad / 8) * 8;
-    const uint16_t* a = P.act;
-    if constexpr (KIND == I4_DOWN_SUM) a += ((size_t)item * P.top_k + row / TERMS) * P.pitch + row % TERMS * P.term;
-    else if constexpr (KIND == I4_GATE_UP) a += (size_t)(item / P.top_k) * P.pitch;
-    else a += (size_t)row * P.pitch;
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (k < P.cols) v = ld16(a + k);
-    *reinterpret_cast<u32x4*>(xs + 16 + (size_t)row * pitch + 2 * k) = v;
+  u32x4 wv[DEPTH][NMAT];
+  Side<GP, ZEROS, NMAT> side[DEPTH];
+  auto load = [&](At a, int d) {
+    if (a.rt >= rt1) return;
+    int kt = a.u, ex = e;
+    if constexpr (KIND == I4_DOWN_SUM) {
+      const int k = a.u / ktiles;
+      kt = a.u % ktiles;
+      ex = max(__builtin_amdgcn_readlane(e, k), 0);
+    }
+    int4_load(P, ex, (size_t)a.rt * ktiles + kt, lane, wv[d], side[d]);
+  };
+  At ahead = {rt0, wave}, at = {rt0, wave};
+  if (wave >= steps) ahead.rt = at.rt = rt1;  // (a wave without tiles keeps the barriers)
+#pragma unroll
+  for (int d = 0; d < DEPTH; d++) {
+    load(ahead, d);
+    step(ahead);
   }
-  __syncthreads();
-  // this lane's row of operand A: token n / 4 in row 0, 4, 8, 12, or term n
-  const bool a_on = TERMS == 1 ? (n & 3) == 0 && n / 4 < tok : n < TERMS;
-  const int a0 = a_on ? 16 + (TERMS == 1 ? n / 4 : n) * pitch + 16 * g : 0, a_step = a_on ? 1 : 0;
+  __builtin_amdgcn_sched_barrier(0);
 
+#pragma unroll
+  for (int q = 0; q < STAGE; q++) put(threadIdx.x + q * blockDim.x, rv[q]);
+  for (int i = threadIdx.x + STAGE * blockDim.x; i < chunks; i += blockDim.x) put(i, get(i));
+  __syncthreads();
+  // this lane's row of operand A: row 4 i + a holds term a of token i
+  const bool a_on = (n & 3) < TERMS && n / 4 < here;
+  const int a0 = a_on ? 16 + (n / 4 * TERMS + (n & 3)) * pitch + 16 * g : 0, a_step = a_on ? 1 : 0;
+
+  int buf = 0;
   float tot[NMAT][NR];
 #pragma unroll
   for (int m = 0; m < NMAT; m++)
 #pragma unroll
     for (int r = 0; r < NR; r++) tot[m][r] = 0.f;
-  for (int u0 = wave; u0 < steps; u0 += waves * DEPTH) {
-    if (u0 != wave) load(u0);
-#pragma unroll
-    for (int d = 0; d < DEPTH; d++) {
-      if (!live[d]) continue;
-      const int u = u0 + d * waves, kt = KIND == I4_DOWN_SUM ? u % ktiles : u;
-      const uint8_t* x = xs + a0 + a_step * ((KIND == I4_DOWN_SUM ? u / ktiles * TERMS * pitch : 0) + kt * 256);
-      f32x4_t acc[NMAT], sx = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int m = 0; m < NMAT; m++) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const u32x4 xv = *reinterpret_cast<const u32x4*>(x + a_step * 64 * j);
-        sx = mfma(xv, ones(), sx);
-#pragma unroll
-        for (int m = 0; m < NMAT; m++) acc[m] = mfma(xv, int4_operand(wv[d][m][j]), acc[m]);
-        if ((j + 1) % (4 / GP) == 0) {  // a group's end
-          const int gi = j * GP / 4;
-#pragma unroll
-          for (int m = 0; m < NMAT; m++) {
-            float s = int4_scale(side[d], m, gi);
-            if constexpr (KIND == I4_DOWN_SUM) s *= fac[d];
-            const float c = int4_offset(side[d], m, gi);
-#pragma unroll
-            for (int r = 0; r < NR; r++) tot[m][r] = __builtin_fmaf(s, __builtin_fmaf(-c, sx[r], acc[m][r]), tot[m][r]);
-            hold(tot[m][NR - 1], acc[m], sx);
-            acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-          }
-          sx = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int m = 0; m < NMAT; m++) {
-    float v = tot[m][0];
-#pragma unroll
-    for (int a = 1; a < TERMS; a++) v += tot[m][a];
-    if (g < TOK) red[wave][m][g][n] = v;
-  }
-  __syncthreads();
-  if ((int)threadIdx.x < tok * 16) {
-    const int t = threadIdx.x >> 4, r = rt * 16 + n;
-    float v[NMAT];
+  auto finish = [&](int rt) {  // a row tile's end
 #pragma unroll
     for (int m = 0; m < NMAT; m++) {
-      v[m] = 0.f;
-      for (int w = 0; w < waves; w++) v[m] += red[w][m][t][n];
+      float v = tot[m][0];
+#pragma unroll
+      for (int a = 1; a < TERMS; a++) v += tot[m][a];
+      if (g < TOK) red[buf][wave][m][g][n] = v;
+#pragma unroll
+      for (int r = 0; r < NR; r++) tot[m][r] = 0.f;
     }
-    if (r < P.rows) int4_store<KIND, NMAT>(P, e, ok, KIND == I4_LINEAR ? t : item, r, v);
+    __syncthreads();
+    if ((int)threadIdx.x < here * 16) {
+      const int t = threadIdx.x >> 4, r = rt * 16 + n;
+      float v[NMAT];
+#pragma unroll
+      for (int m = 0; m < NMAT; m++) {
+        v[m] = 0.f;
+        for (int w = 0; w < waves; w++) v[m] += red[buf][w][m][t][n];
+      }
+      if (r < P.rows) int4_store<KIND, NMAT>(P, e, ok, KIND == I4_LINEAR ? t : item, r, v);
+    }
+    buf ^= 1;
+  };
+  while (at.rt < rt1) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; d++) {
+      if (at.rt >= rt1) break;
+      bool live = ok;
+      float f = 1.f;
+      int k = 0, kt = at.u;
+      if constexpr (KIND == I4_DOWN_SUM) {
+        k = at.u / ktiles;
+        kt = at.u % ktiles;
+        live = __builtin_amdgcn_readlane(e, k) >= 0;
+        f = u2f((uint32_t)__builtin_amdgcn_readlane((int)f2u(fac), k));
+      }
+      if (live) {
+        const uint8_t* x = xs + a0 + a_step * (k * TERMS * pitch + kt * 256);
+        f32x4_t acc[NMAT], sx = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int m = 0; m < NMAT; m++) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const u32x4 xv = *reinterpret_cast<const u32x4*>(x + a_step * 64 * j);
+          sx = mfma(xv, ones(), sx);
+#pragma unroll
+          for (int m = 0; m < NMAT; m++) acc[m] = mfma(xv, int4_operand(wv[d][m][j]), acc[m]);
+          if ((j + 1) % (4 / GP) == 0) {  // a group's end
+            const int gi = j * GP / 4;
+#pragma unroll
+            for (int m = 0; m < NMAT; m++) {
+              float s = int4_scale(side[d], m, gi);
+              if constexpr (KIND == I4_DOWN_SUM) s *= f;
+              const float c = int4_offset(side[d], m, gi);
+#pragma unroll
+              for (int r = 0; r < NR; r++) tot[m][r] = __builtin_fmaf(s, __builtin_fmaf(-c, sx[r], acc[m][r]), tot[m][r]);
+              hold(tot[m][NR - 1], acc[m], sx);
+              acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            }
+            sx = f32x4_t{0.f, 0.f, 0.f, 0.f};
+          }
+        }
+      }
+      load(ahead, d);
+      step(ahead);
+      const int rt = at.rt;
+      step(at);
+      if (at.rt != rt) finish(rt);
+    }
   }
+  if (wave >= steps)
+    for (int rt = rt0; rt < rt1; rt++) finish(rt);
 }
 
-// A few rows to an expert. A work-group takes `rb` row tiles of an expert, one after another; its
-// waves take the tiles of K in turn, KT of them at a time, whose activations (and, as
-// they do not change with the weight row, their sums for each group) stay in registers, so that
-// only weights move: the next row tile's are loaded as this one's are used up. The waves' sums
-// meet in LDS (two buffers, so one barrier to a row tile) and are added in the order of the waves.
-// NR: output registers in use, so a tile of operand A holds 4 NR / TERMS rows.
-template <int GP, bool ZEROS, int TERMS, int NR, int KIND, int KT>
-__device__ __forceinline__ void int4_few(const Int4Params& P, float* red, int e, int first, int count, const int32_t* perm,
-                                         bool ok, int rt0, int rt1) {
-  constexpr int NMAT = KIND == I4_GATE_UP ? 2 : 1, TPQ = NR / TERMS, TOK = 4 * TPQ;
-  constexpr int RED = FEW_WAVES * NMAT * TOK * 16;
+// Five to sixteen tokens of a linear (or fewer, with more columns than fit k_int4_one's LDS). A
+// work-group: 16 weight rows and all of K, whose tiles its waves take in turn, KT of them at a
+// time, with their activations in registers; the waves' sums meet in LDS and are added in the
+// order of the waves. NR: output registers in use, so a tile of operand A holds 4 NR tokens.
+template <int GP, bool ZEROS, int NR, int KT>
+__global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_int4_few(Int4Params P) {
+  constexpr int TOK = 4 * NR;
+  __shared__ float red[FEW_WAVES][TOK][16];
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int ktiles = int4_ktiles(P.cols), rounds = (ktiles + FEW_WAVES * KT - 1) / (FEW_WAVES * KT);
-  // this lane's row of operand A: token `ai` of the tile, term `aterm`
-  const int ai = (n & 3) / TERMS + (n >> 2) * TPQ, aterm = (n & 3) % TERMS;
-
-  for (int m0 = 0; m0 < count; m0 += TOK) {
-    const int here = min(TOK, count - m0);
-    const bool a_on = (n & 3) < NR && ai < here;
-    size_t arow = 0;
-    if (a_on) {
-      arow = perm ? perm[m0 + ai] : first + m0 + ai;
-      if constexpr (KIND == I4_GATE_UP) arow /= P.top_k;
-    }
-    const uint16_t* ap = P.act + arow * P.pitch + aterm * P.term + 8 * g;
-    u32x4 wv[KT][NMAT], xv[KT][4];
-    Side<GP, ZEROS, NMAT> side[KT];
-    f32x4_t sx[KT][GP];
-    auto load = [&](int rt, int round, int i) {
-      const int kt = min((round * KT + i) * FEW_WAVES + wave, ktiles - 1);
-      int4_load(P, e, (size_t)rt * ktiles + kt, lane, wv[i], side[i]);
-    };
-    if (ok) {
+  const int rt = blockIdx.x, ktiles = int4_ktiles(P.cols);
+  // this lane's row of operand A: token `ai`
+  const int ai = (n & 3) + (n >> 2) * NR;
+  const bool a_on = (n & 3) < NR && ai < P.T;
+  const uint16_t* ap = P.act + (size_t)(a_on ? ai : 0) * P.pitch + 8 * g;
+  float tot[NR];
 #pragma unroll
-      for (int i = 0; i < KT; i++) load(rt0, 0, i);
-    }
-    int buf = 0;
-    for (int rt = rt0; rt < rt1; rt++, buf ^= 1) {
-      float tot[NMAT][NR];
+  for (int r = 0; r < NR; r++) tot[r] = 0.f;
+  for (int k1 = wave; k1 < ktiles; k1 += FEW_WAVES * KT) {
+    u32x4 wv[KT][1], xv[KT][4];
+    Side<GP, ZEROS, 1> side[KT];
 #pragma unroll
-      for (int m = 0; m < NMAT; m++)
+    for (int i = 0; i < KT; i++)
+      int4_load(P, P.expert, (size_t)rt * ktiles + min(k1 + i * FEW_WAVES, ktiles - 1), lane, wv[i], side[i]);
 #pragma unroll
-        for (int r = 0; r < NR; r++) tot[m][r] = 0.f;
-      if (ok) {
-        for (int round = 0; round < rounds; round++) {
-          if (rt == rt0 || rounds > 1) {
+    for (int i = 0; i < KT; i++) {
+      const int k0 = (k1 + i * FEW_WAVES) * 128;
 #pragma unroll
-            for (int i = 0; i < KT; i++) {
-              const int k0 = ((round * KT + i) * FEW_WAVES + wave) * 128;
-#pragma unroll
-              for (int j = 0; j < 4; j++) {  // zeros past the end, and so for tiles past it
-                xv[i][j] = u32x4{0u, 0u, 0u, 0u};
-                if (a_on && k0 + 32 * j < P.cols) xv[i][j] = ld16(ap + k0 + 32 * j);
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < KT; i++)
-#pragma unroll
-              for (int q = 0; q < GP; q++) {
-                f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int j = q * (4 / GP); j < (q + 1) * (4 / GP); j++) v = mfma(xv[i][j], ones(), v);
-                sx[i][q] = v;
-              }
-          }
-#pragma unroll
-          for (int i = 0; i < KT; i++) {
-            if ((round * KT + i) * FEW_WAVES + wave < ktiles) {
-#pragma unroll
-              for (int q = 0; q < GP; q++)
-#pragma unroll
-                for (int m = 0; m < NMAT; m++) {
-                  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                  for (int j = q * (4 / GP); j < (q + 1) * (4 / GP); j++) acc = mfma(xv[i][j], int4_operand(wv[i][m][j]), acc);
-                  const float s = int4_scale(side[i], m, q), c = int4_offset(side[i], m, q);
-#pragma unroll
-                  for (int r = 0; r < NR; r++) tot[m][r] = __builtin_fmaf(s, __builtin_fmaf(-c, sx[i][q][r], acc[r]), tot[m][r]);
-                  hold(tot[m][NR - 1], acc, sx[i][q]);
-                }
-            }
-            if (round + 1 < rounds) load(rt, round + 1, i);
-            else if (rt + 1 < rt1) load(rt + 1, 0, i);
-          }
-        }
-      }
-      float* rd = red + buf * RED;
-#pragma unroll
-      for (int m = 0; m < NMAT; m++)
-#pragma unroll
-        for (int i = 0; i < TPQ; i++) {
-          float v = tot[m][i * TERMS];
-#pragma unroll
-          for (int a = 1; a < TERMS; a++) v += tot[m][i * TERMS + a];
-          rd[((wave * NMAT + m) * TOK + g * TPQ + i) * 16 + n] = v;
-        }
-      __syncthreads();
-      const int t = threadIdx.x >> 4, r = rt * 16 + n;
-      if (t < here) {
-        float v[NMAT];
-#pragma unroll
-        for (int m = 0; m < NMAT; m++) {
-          v[m] = 0.f;
-#pragma unroll
-          for (int w = 0; w < FEW_WAVES; w++) v[m] += rd[((w * NMAT + m) * TOK + t) * 16 + n];
-        }
-        if (r < P.rows) int4_store<KIND, NMAT>(P, e, ok, perm ? perm[m0 + t] : first + m0 + t, r, v);
+      for (int j = 0; j < 4; j++) {
+        xv[i][j] = u32x4{0u, 0u, 0u, 0u};
+        if (a_on && k0 + 32 * j < P.cols) xv[i][j] = ld16(ap + k0 + 32 * j);
       }
     }
-    __syncthreads();  // the buffers are free again
+#pragma unroll
+    for (int i = 0; i < KT; i++) {
+      if (k1 + i * FEW_WAVES >= ktiles) break;
+#pragma unroll
+      for (int q = 0; q < GP; q++) {
+        f32x4_t acc = {0.f, 0.f, 0.f, 0.f}, sx = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = q * (4 / GP); j < (q + 1) * (4 / GP); j++) {
+          sx = mfma(xv[i][j], ones(), sx);
+          acc = mfma(xv[i][j], int4_operand(wv[i][0][j]), acc);
+        }
+        const float s = int4_scale(side[i], 0, q), c = int4_offset(side[i], 0, q);
+#pragma unroll
+        for (int r = 0; r < NR; r++) tot[r] = __builtin_fmaf(s, __builtin_fmaf(-c, sx[r], acc[r]), tot[r]);
+        hold(tot[NR - 1], acc, sx);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < NR; r++) red[wave][g * NR + r][n] = tot[r];
+  __syncthreads();
+  const int t = threadIdx.x >> 4, r = rt * 16 + n;
+  if (t < P.T && r < P.rows) {
+    float v[1] = {0.f};
+#pragma unroll
+    for (int w = 0; w < FEW_WAVES; w++) v[0] += red[w][t][n];
+    int4_store<I4_LINEAR, 1>(P, P.expert, true, t, r, v);
   }
 }
 
-template <int GP, bool ZEROS, int KIND, int KT>
-__global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_int4_few(Int4Params P, int rb) {
-  __shared__ float red[2 * FEW_WAVES * (KIND == I4_GATE_UP ? 2 : 1) * 16 * 16];
-  const int rt0 = blockIdx.x * rb, rt1 = min(rt0 + rb, int4_rtiles(P.rows)), item = blockIdx.y;
-  int e = P.expert, first = item * 16, count = min(16, P.T - first);
-  const int32_t* perm = nullptr;
-  bool ok = true;
-  if constexpr (KIND != I4_LINEAR) {
-    if (item >= P.route.n_slots()[0]) return;
-    e = P.route.slots()[item];
-    const int p0 = P.route.offsets()[e];
-    count = P.route.offsets()[e + 1] - p0;
-    perm = P.route.perm() + p0;
-    first = 0;
-    ok = e < P.n_experts;  // ids out of range have set the error bit when they were sorted
-  }
-  if constexpr (KIND == I4_DOWN_PART) {
-    int4_few<GP, ZEROS, 3, 3, KIND, KT>(P, red, e, first, count, perm, ok, rt0, rt1);
-  } else if (count <= 4) {
-    int4_few<GP, ZEROS, 1, 1, KIND, KT>(P, red, e, first, count, perm, ok, rt0, rt1);
-  } else if (count <= 8 || KIND == I4_GATE_UP) {  // two matrices and sixteen rows do not fit the registers
-    int4_few<GP, ZEROS, 1, 2, KIND, KT>(P, red, e, first, count, perm, ok, rt0, rt1);
-  } else if constexpr (KIND != I4_GATE_UP) {
-    int4_few<GP, ZEROS, 1, 4, KIND, KT>(P, red, e, first, count, perm, ok, rt0, rt1);
-  }
-}
-
-// LDS of k_int4_one's rows; more than this and the other kernel takes them.
+// LDS of k_int4_one's rows (each term one); more than this and the other kernel takes them.
 constexpr size_t ONE_LDS = 96 << 10;
 size_t one_lds(int rows, int cols) { return 16 + (size_t)rows * (int4_ktiles(cols) * 256 + 16); }
 
 template <int GP, int TERMS, int KIND, int DEPTH>
 hipError_t one(const Int4Params& p, int items, int rows, hipStream_t s, const LaunchEvents* ev) {
   const int steps = int4_ktiles(p.cols) * (KIND == I4_DOWN_SUM ? p.top_k : 1);
-  const dim3 g((unsigned)int4_rtiles(p.rows), (unsigned)items), b(64 * (steps < FEW_WAVES ? steps : FEW_WAVES));
+  // Row tiles of a work-group: one while every CU has up to three work-groups, then more (at most
+  // 16), which saves their beginnings: 8 tokens of 4096 x 2048 experts (6 of 256) 130 us, 169 with
+  // one each. (With 512, 1024 and 1536 work-groups instead of 768: 140, 147 and 138.)
+  const long rt = int4_rtiles(p.rows);
+  const int rb = (int)std::min(16l, std::max(1l, rt * items / 768));
+  const dim3 g((unsigned)((rt + rb - 1) / rb), (unsigned)items), b(64 * std::min(steps, one_waves(KIND)));
   const unsigned lds = (unsigned)one_lds(rows, p.cols);
   auto go = [&](auto k) {
-    if (ev) hipExtLaunchKernelGGL(k, g, b, lds, s, ev->start, ev->stop, 0, p);
-    else hipLaunchKernelGGL(k, g, b, lds, s, p);
+    if (ev) hipExtLaunchKernelGGL(k, g, b, lds, s, ev->start, ev->stop, 0, p, rb);
+    else hipLaunchKernelGGL(k, g, b, lds, s, p, rb);
     return hipGetLastError();
   };
   return int4_zeros(p.fmt) ? go(k_int4_one<GP, true, TERMS, KIND, DEPTH>) : go(k_int4_one<GP, false, TERMS, KIND, DEPTH>);
 }
 
-// Row tiles of a work-group: few enough that every CU has two of them, at most 16.
-#ifndef MOEQ_I4_FEW_WGS
-#define MOEQ_I4_FEW_WGS 768
-#endif
-template <int GP, int KIND>
-hipError_t few(const Int4Params& p, int items, hipStream_t s, const LaunchEvents* ev) {
-  const long rt = int4_rtiles(p.rows);
-  const int rb = (int)std::min(16l, std::max(1l, rt * items / MOEQ_I4_FEW_WGS));
-  const dim3 g((unsigned)((rt + rb - 1) / rb), (unsigned)items), b(64 * FEW_WAVES);
+template <int GP, int NR>
+hipError_t few(const Int4Params& p, hipStream_t s) {
+  const dim3 g((unsigned)int4_rtiles(p.rows)), b(64 * FEW_WAVES);
   const int kt = (int4_ktiles(p.cols) + FEW_WAVES - 1) / FEW_WAVES;
   auto go = [&](auto k) {
-    if (ev) hipExtLaunchKernelGGL(k, g, b, 0, s, ev->start, ev->stop, 0, p, rb);
-    else hipLaunchKernelGGL(k, g, b, 0, s, p, rb);
+    hipLaunchKernelGGL(k, g, b, 0, s, p);
     return hipGetLastError();
   };
-  auto by_k = [&](auto z) {
-    constexpr bool Z = decltype(z)::value;
-    if (kt <= 1) return go(k_int4_few<GP, Z, KIND, 1>);
-    if (kt <= 2) return go(k_int4_few<GP, Z, KIND, 2>);
-    return go(k_int4_few<GP, Z, KIND, 4>);
-  };
-  return int4_zeros(p.fmt) ? by_k(std::true_type()) : by_k(std::false_type());
+  if (int4_zeros(p.fmt)) return kt <= 2 ? go(k_int4_few<GP, true, NR, 2>) : go(k_int4_few<GP, true, NR, 4>);
+  return kt <= 2 ? go(k_int4_few<GP, false, NR, 2>) : go(k_int4_few<GP, false, NR, 4>);
 }
 
+// DEPTH: fewer tiles on their way leave more waves on a CU, which counts for more (gate/up of one
+// token, two against four: 12.4 and 15.6 us).
 template <int GP>
 hipError_t few_kind(int kind, const Int4Params& p, int items, hipStream_t s, const LaunchEvents* ev) {
   switch (kind) {
     case I4_LINEAR:
       if (p.T <= 4 && one_lds(p.T, p.cols) <= ONE_LDS) return one<GP, 1, I4_LINEAR, 4>(p, 1, p.T, s, ev);
-      return few<GP, I4_LINEAR>(p, (p.T + 15) / 16, s, ev);
-    case I4_GATE_UP:
-      return p.grouped ? few<GP, I4_GATE_UP>(p, items, s, ev) : one<GP, 1, I4_GATE_UP, 4>(p, items, 1, s, ev);
-    case I4_DOWN_SUM: return one<GP, 3, I4_DOWN_SUM, 12>(p, items, 3 * p.top_k, s, ev);
-    case I4_DOWN_PART: return few<GP, I4_DOWN_PART>(p, items, s, ev);
+      return p.T <= 8 ? few<GP, 2>(p, s) : few<GP, 4>(p, s);
+    case I4_GATE_UP: return one<GP, 1, I4_GATE_UP, 2>(p, items, 1, s, ev);
+    case I4_DOWN_SUM: return one<GP, 3, I4_DOWN_SUM, 3>(p, items, 3 * p.top_k, s, ev);
   }
   return hipErrorInvalidValue;
 }
@@ -570,8 +546,7 @@ hipError_t launch_int4_few(int kind, const Int4Params& p, int items, hipStream_t
   if (!is_int4(p.fmt) || p.T < 1 || items < 1 || items > 65535 || p.rows < 1 || p.rows > INT4_MAX_ROWS || p.cols < 32 ||
       p.cols > INT4_MAX_COLS || p.cols % int4_group(p.fmt) || p.pitch % 8 || p.term % 8)
     return hipErrorInvalidValue;
-  if ((kind == I4_DOWN_SUM || (kind == I4_GATE_UP && !p.grouped)) && !int4_one_fits(kind, p.top_k, p.cols))
-    return hipErrorInvalidValue;
+  if (kind != I4_LINEAR && !int4_one_fits(kind, p.top_k, p.cols)) return hipErrorInvalidValue;
   if (kind == I4_LINEAR && p.T > INT4_FEW_T) return hipErrorInvalidValue;
   switch (int4_group(p.fmt)) {
     case 32: return few_kind<4>(kind, p, items, s, ev);

@@ -83,20 +83,29 @@ __device__ __forceinline__ void int4_tile(const Int4Rows& P, uint8_t* lds, int b
   const int row0 = 4 * COPIES * wave % ROWS;
 
   // this lane's part of a wave's copies: LDS row row0 + 4 i + lane / 16, term by term
-  const uint16_t* abase = P.act + (KIND == I4_LINEAR ? (size_t)first * kpad : 0);
+  const uint16_t* abase = P.act + (size_t)first * kpad;  // LINEAR
   int off[COPIES];
+  const uint8_t* from[COPIES];
 #pragma unroll
   for (int i = 0; i < COPIES; i++) {
     const int row = row0 + 4 * i + (lane >> 4), term = row / TOK, t = min(row % TOK, count - 1);
-    int a = t;
-    if constexpr (KIND == I4_GATE_UP) a = perm[t] / P.top_k;
-    if constexpr (KIND == I4_DOWN_PART) a = perm[t];
-    off[i] = (a * TERMS + term) * kpad * 2 + 16 * ((lane & 15) ^ (row & 15));
+    const int chunk = 16 * ((lane & 15) ^ (row & 15));
+    if constexpr (KIND == I4_LINEAR) {
+      off[i] = t * kpad * 2 + chunk;
+    } else {
+      const size_t a = KIND == I4_GATE_UP ? perm[t] / P.top_k : perm[t];
+      from[i] = reinterpret_cast<const uint8_t*>(P.act + (a * TERMS + term) * kpad) + chunk;
+    }
   }
   auto copy = [&](int s, int to) {  // step s into buffer `to`
     uint8_t* dst = lds + to * STAGE + 256 * row0;
 #pragma unroll
-    for (int i = 0; i < COPIES; i++) copy16(reinterpret_cast<const int8_t*>(abase), off[i], s * 256, dst + 1024 * i);
+    for (int i = 0; i < COPIES; i++) {
+      if constexpr (KIND == I4_LINEAR) copy16(reinterpret_cast<const int8_t*>(abase), off[i], s * 256, dst + 1024 * i);
+      else
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from[i] + (size_t)s * 256),
+                                         (__attribute__((address_space(3))) void*)(dst + 1024 * i), 16, 0, 0);
+    }
   };
 
   // row tiles of this wave; past the end the last one, whose outputs are not stored
@@ -281,19 +290,19 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_int4_linear(Int4R
   int4_tile<I4_LINEAR, GP, ZEROS, SCALED, WM, WN, NM, NT>(P, lds, bm, P.expert, bn * TOK, min(TOK, P.T - bn * TOK), nullptr);
 }
 
-// NT: token tiles of a work-group at most; as many are multiplied as its pairs need.
-template <int KIND, int GP, bool ZEROS, int NM, int NT>
-__global__ __launch_bounds__(512, 2) void k_int4_experts(Int4Rows P) {
-  constexpr int TOK = 16 * NT, RT = NM / (KIND == I4_GATE_UP ? 2 : 1), PARTS = PREFILL_MC / TOK;
+// A chunk of up to PREFILL_MC pairs of an expert, 16 NT of them at a time; as many token tiles are
+// multiplied as there are. WAVES: to a SIMD.
+template <int KIND, int GP, bool ZEROS, int NM, int NT, int WAVES>
+__global__ __launch_bounds__(512, WAVES) void k_int4_experts(Int4Rows P) {
+  constexpr int TOK = 16 * NT, RT = NM / (KIND == I4_GATE_UP ? 2 : 1);
   __shared__ __attribute__((aligned(16))) uint8_t lds[I4_STAGES * (KIND == I4_DOWN_PART ? 2 : 1) * TOK * 256];
   const int nbm = (int4_rtiles(P.rows) + 8 * RT - 1) / (8 * RT);
   // the row blocks of a chunk of tokens on one XCD: they share the tokens in its L2
-  const int l = blockIdx.x / 8, q = l / nbm * 8 + (int)(blockIdx.x % 8), bm = l % nbm, chunk = q / PARTS;
-  if (chunk >= P.route.n_chunks()[0]) return;
-  const int e = P.route.chunk_e()[chunk];
-  const int p0 = P.route.offsets()[e], m0 = P.route.chunk_m0()[chunk] + q % PARTS * TOK;
-  const int count = min(TOK, P.route.offsets()[e + 1] - p0 - m0);
-  if (count <= 0) return;
+  const int l = blockIdx.x / 8, q = l / nbm * 8 + (int)(blockIdx.x % 8), bm = l % nbm;
+  if (q >= P.route.n_chunks()[0]) return;
+  const int e = P.route.chunk_e()[q];
+  const int p0 = P.route.offsets()[e], m0 = P.route.chunk_m0()[q];
+  const int count = min(PREFILL_MC, P.route.offsets()[e + 1] - p0 - m0);
   const int32_t* perm = P.route.perm() + p0 + m0;
   if (e >= P.n_experts) {  // ids out of range
     if constexpr (KIND == I4_DOWN_PART)
@@ -303,12 +312,13 @@ __global__ __launch_bounds__(512, 2) void k_int4_experts(Int4Rows P) {
       }
     return;
   }
-  if (NT == 1 || count <= 16) return int4_tile<KIND, GP, ZEROS, false, 8, 1, NM, 1>(P, lds, bm, e, 0, count, perm);
-  if constexpr (NT >= 2)
-    if (NT == 2 || count <= 32) return int4_tile<KIND, GP, ZEROS, false, 8, 1, NM, 2>(P, lds, bm, e, 0, count, perm);
-  if constexpr (NT >= 4) {
-    if (count <= 48) return int4_tile<KIND, GP, ZEROS, false, 8, 1, NM, 3>(P, lds, bm, e, 0, count, perm);
-    int4_tile<KIND, GP, ZEROS, false, 8, 1, NM, 4>(P, lds, bm, e, 0, count, perm);
+  for (int m = 0; m < count; m += TOK) {
+    const int here = min(TOK, count - m);
+    if (m > 0) __syncthreads();  // the tile before has been read
+    if (NT == 1 || here <= 16) int4_tile<KIND, GP, ZEROS, false, 8, 1, NM, 1>(P, lds, bm, e, 0, here, perm + m);
+    else if (NT == 2 || here <= 32) int4_tile<KIND, GP, ZEROS, false, 8, 1, NM, NT < 2 ? 1 : 2>(P, lds, bm, e, 0, here, perm + m);
+    else if (here <= 48) int4_tile<KIND, GP, ZEROS, false, 8, 1, NM, NT < 4 ? 1 : 3>(P, lds, bm, e, 0, here, perm + m);
+    else int4_tile<KIND, GP, ZEROS, false, 8, 1, NM, NT < 4 ? 1 : 4>(P, lds, bm, e, 0, here, perm + m);
   }
 }
 
@@ -321,13 +331,13 @@ hipError_t linear(const Int4Rows& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int KIND, int GP, int NM, int NT>
+template <int KIND, int GP, int NM, int NT, int WAVES>
 hipError_t experts(const Int4Rows& p, hipStream_t s) {
   constexpr int RT = NM / (KIND == I4_GATE_UP ? 2 : 1);
-  const long items = (long)RouteView::max_chunks(p.n_experts, p.T * p.top_k) * (PREFILL_MC / (16 * NT));
+  const long items = RouteView::max_chunks(p.n_experts, p.T * p.top_k);
   const dim3 g((unsigned)((int4_rtiles(p.rows) + 8 * RT - 1) / (8 * RT) * ((items + 7) / 8 * 8)));
-  if (int4_zeros(p.fmt)) hipLaunchKernelGGL((k_int4_experts<KIND, GP, true, NM, NT>), g, dim3(512), 0, s, p);
-  else hipLaunchKernelGGL((k_int4_experts<KIND, GP, false, NM, NT>), g, dim3(512), 0, s, p);
+  if (int4_zeros(p.fmt)) hipLaunchKernelGGL((k_int4_experts<KIND, GP, true, NM, NT, WAVES>), g, dim3(512), 0, s, p);
+  else hipLaunchKernelGGL((k_int4_experts<KIND, GP, false, NM, NT, WAVES>), g, dim3(512), 0, s, p);
   return hipGetLastError();
 }
 

@@ -69,7 +69,10 @@ __global__ __launch_bounds__(256) void k_int4_rows(const void* x, int cols, int 
 }
 
 #ifndef MOEQ_I4_WIDE
-#define MOEQ_I4_WIDE 8
+#define MOEQ_I4_WIDE 12
+#endif
+#ifndef MOEQ_I4_NT
+#define MOEQ_I4_NT 1
 #endif
 template <int GP>
 hipError_t tiled_kind(int kind, const Int4Rows& p, hipStream_t s) {
@@ -81,14 +84,11 @@ hipError_t tiled_kind(int kind, const Int4Rows& p, hipStream_t s) {
     return linear<GP, false, 4, 1, 1, 2>(p, s);
   }
   const bool wide = (long)p.T * p.top_k >= (long)MOEQ_I4_WIDE * p.n_experts;
-  if (kind == I4_GATE_UP) return wide ? experts<I4_GATE_UP, GP, 2, 4>(p, s) : experts<I4_GATE_UP, GP, 2, 1>(p, s);
-  return wide ? experts<I4_DOWN_PART, GP, 2, 4>(p, s) : experts<I4_DOWN_PART, GP, 2, 1>(p, s);
+  if (kind == I4_GATE_UP) return wide ? experts<I4_GATE_UP, GP, 2, 4, 2>(p, s) : experts<I4_GATE_UP, GP, 2, MOEQ_I4_NT, 4>(p, s);
+  return wide ? experts<I4_DOWN_PART, GP, 2, 4, 2>(p, s) : experts<I4_DOWN_PART, GP, 2, MOEQ_I4_NT, 4>(p, s);
 }
 
 }  // namespace
-
-// Byte offsets of gathered rows are 32-bit.
-bool int4_rows_fit(size_t n_rows, int terms, int cols) { return n_rows * terms * int4_ktiles(cols) * 256 < (size_t)1 << 31; }
 
 size_t int4_rows_bytes(size_t n_rows, int terms, int cols) { return n_rows * terms * int4_ktiles(cols) * 256; }
 
@@ -110,8 +110,6 @@ hipError_t launch_int4_rows(bool in_f32, const void* x, size_t n_rows, int cols,
 hipError_t launch_int4_tiled(int kind, const Int4Rows& p, hipStream_t s) {
   if (!is_int4(p.fmt) || p.T < 1 || p.rows < 1 || p.rows > INT4_MAX_ROWS || p.cols < 32 || p.cols > INT4_MAX_COLS ||
       p.cols % int4_group(p.fmt))
-    return hipErrorInvalidValue;
-  if (kind != I4_LINEAR && !int4_rows_fit((size_t)p.T * (kind == I4_DOWN_PART ? p.top_k : 1), kind == I4_DOWN_PART ? 2 : 1, p.cols))
     return hipErrorInvalidValue;
   auto run = [&](const Int4Rows& q) {
     switch (int4_group(q.fmt)) {

@@ -112,7 +112,8 @@ enum { FMT_INT8 = 9 };  // beside the FMT_* of moeq_device.h
 constexpr int INT4_FEW_T = 16;  // tokens of the linear that takes no workspace
 
 // Products of INT4 weights (moeq_int4.h) with rows of activations in bf16: tokens, or the
-// intermediate h as three terms of each value, whose sum it is.
+// intermediate h as three terms of each value, whose sum it is. I4_GATE_UP and I4_DOWN_SUM go
+// pair by pair and token by token.
 enum { I4_LINEAR = 0, I4_GATE_UP = 1, I4_DOWN_SUM = 2, I4_DOWN_PART = 3 };
 struct Int4Params {
   int fmt;
@@ -122,12 +123,10 @@ struct Int4Params {
   size_t pitch, term;
   int T, top_k, n_experts;
   int expert;           // I4_LINEAR: the one tensor
-  bool grouped;         // experts in the order of `route`; else pair by pair (ids)
   const int32_t* ids;
-  RouteView route;
   const float* rw;      // route weights [T][top_k]
   const float* bias;    // I4_LINEAR: [rows] or null
-  void* y;              // linear [T][rows]; gate/up h [pairs][rows]; down [T][rows] or [pairs][rows]
+  void* y;              // linear, down [T][rows]; gate/up h [pairs][rows]
   bool out_bf16;        // I4_LINEAR: y is bf16
   bool out_terms;       // I4_GATE_UP: h as bf16 terms, [pairs][3][rows]
   uint32_t* err;
@@ -145,7 +144,7 @@ struct Int4Rows {
   RouteView route;
   const float* rw;
   const float* bias;
-  void* y;                 // as in Int4Params (no I4_DOWN_SUM)
+  void* y;                 // as in Int4Params; I4_DOWN_PART: route-weighted parts [pairs][rows]
   bool out_bf16;
 };
 
@@ -286,13 +285,12 @@ hipError_t launch_dequant_int8(const int8_t* w, const float* ws, int rows, int c
 hipError_t launch_pack_int4(int fmt, const uint8_t* codes, const uint16_t* scales, bool scales_bf16, const uint8_t* zeros,
                             int rows, int cols, int n, uint8_t* data, uint8_t* out_scales, float* scale2, hipStream_t s);
 hipError_t launch_dequant_int4(int fmt, const WeightRef& w, int rows, int cols, int expert, float* out, hipStream_t s);
-// Products for a few rows to an expert (any number is right, in tiles of up to 16 or 4 rows). One
-// token or pair at a time (I4_DOWN_SUM, I4_GATE_UP unless `grouped`) has to fit: int4_one_fits.
+// items: pairs (I4_GATE_UP) or tokens (I4_DOWN_SUM), whose activations have to fit a work-group
+// (int4_one_fits); I4_LINEAR: up to INT4_FEW_T tokens.
 bool int4_one_fits(int kind, int top_k, int cols);
 hipError_t launch_int4_few(int kind, const Int4Params& p, int items, hipStream_t s, const LaunchEvents* ev = nullptr);
 // fp32 rows -> their three bf16 terms [n_rows][3][cols].
 hipError_t launch_int4_terms(const float* h, size_t n_rows, int cols, uint16_t* planes, hipStream_t s);
-bool int4_rows_fit(size_t n_rows, int terms, int cols);
 size_t int4_rows_bytes(size_t n_rows, int terms, int cols);
 // bf16 rows -> one fp16 term, fp32 rows -> two (see Int4Rows).
 hipError_t launch_int4_rows(bool in_f32, const void* x, size_t n_rows, int cols, uint16_t* out, float* scale, hipStream_t s);
