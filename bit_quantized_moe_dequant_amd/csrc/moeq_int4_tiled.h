@@ -16,8 +16,9 @@
 //
 // Activations are operand A (its rows: tokens), so a lane's outputs belong to one weight row and
 // need one scale per group. A work-group's waves stand WM x WN, each with NM row tiles of weights
-// and 16 NT of its tokens, which lie in LDS in steps of 128 columns (three buffers; a row's 16-byte chunks at chunk ^ (row % 16), so that the sixteen rows
-// of an operand touch all banks once). Weights go from memory to registers, a step ahead.
+// and 16 NT of its tokens, which lie in LDS in steps of 128 columns (three buffers; a row's 16-byte
+// chunks at chunk ^ (row % 16), so that the sixteen rows of an operand touch all banks once).
+// Weights go from memory to registers, a step ahead.
 //
 // One barrier per step, before the products of its last 32 columns, whose operands are in
 // registers by then: behind it the step's buffer is free for the copy three steps on, and the
@@ -39,6 +40,8 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------- product
 
+constexpr int I4_STAGES = 3;  // buffers of activations, and sets of weights in registers
+
 __device__ __forceinline__ uint32_t pk_add(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, a) + __builtin_bit_cast(f16x2_t, b));
 }
@@ -49,8 +52,6 @@ __device__ __forceinline__ uint32_t pk_half(float v) {
   const uint32_t h = __builtin_bit_cast(uint16_t, (_Float16)v);
   return h | (h << 16);
 }
-
-constexpr int I4_STAGES = 3;  // buffers of activations, and sets of weights in registers
 
 // Spread V vector operations among M matrix instructions, and R operand reads behind the first.
 template <int M, int V, int R, int I = 0>
@@ -65,22 +66,26 @@ __device__ __forceinline__ void spread() {
 }
 
 // One work-group's tile: row block bm of expert e, activation rows first .. + count (LINEAR), or
-// the pairs perm[0 .. count); count at most 16 NT WN.
-template <int KIND, int GP, bool ZEROS, bool SCALED, int WM, int WN, int NM, int NT>
+// the pairs perm[0 .. count); count at most 16 NT WN. WK: waves that share an output, each with
+// every WK-th step of columns; a step below is then WK of those, and the first wave adds up.
+template <int KIND, int GP, bool ZEROS, bool SCALED, int WM, int WN, int NM, int NT, int WK = 1>
 __device__ __forceinline__ void int4_tile(const Int4Rows& P, uint8_t* lds, int bm, int e, int first, int count,
                                           const int32_t* perm) {
   constexpr int TOK = 16 * NT * WN;
-  constexpr int TERMS = KIND == I4_DOWN_PART ? 2 : 1, ROWS = TERMS * TOK, STAGE = ROWS * 256;
+  constexpr int TERMS = KIND == I4_DOWN_PART ? 2 : 1, ROWS = WK * TERMS * TOK, STAGE = ROWS * 256;
+  constexpr int WAVES = WM * WN * WK;
+  static_assert(WK == 1 || (KIND == I4_LINEAR && !SCALED), "steps shared by waves");
   // copies of a wave per step, four LDS rows each (the waves past the last row repeat the first)
-  constexpr int COPIES = (ROWS / 4 + WM * WN - 1) / (WM * WN);
+  constexpr int COPIES = (ROWS / 4 + WAVES - 1) / WAVES;
   static_assert(ROWS % (4 * COPIES) == 0, "no copy passes the end");
   constexpr int PAIRS = KIND == I4_GATE_UP ? 2 : 1;  // matrices side by side
   constexpr int RT = NM / PAIRS;               // row tiles of a wave
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ktiles = int4_ktiles(P.cols), kpad = ktiles * 128, rtiles = int4_rtiles(P.rows);
-  const int wm = wave % WM, wn = wave / WM;
+  const int wm = wave % WM, wn = wave / WM % WN, wk = wave / (WM * WN);
   const int row0 = 4 * COPIES * wave % ROWS;
+  const int steps = (ktiles + WK - 1) / WK, last = steps - 1;
 
   // this lane's part of a wave's copies: LDS row row0 + 4 i + lane / 16, term by term
   const uint16_t* abase = P.act + (size_t)first * kpad;  // LINEAR
@@ -88,7 +93,7 @@ __device__ __forceinline__ void int4_tile(const Int4Rows& P, uint8_t* lds, int b
   const uint8_t* from[COPIES];
 #pragma unroll
   for (int i = 0; i < COPIES; i++) {
-    const int row = row0 + 4 * i + (lane >> 4), term = row / TOK, t = min(row % TOK, count - 1);
+    const int row = row0 + 4 * i + (lane >> 4), term = row / TOK % TERMS, t = min(row % TOK, count - 1);
     const int chunk = 16 * ((lane & 15) ^ (row & 15));
     if constexpr (KIND == I4_LINEAR) {
       off[i] = t * kpad * 2 + chunk;
@@ -97,11 +102,13 @@ __device__ __forceinline__ void int4_tile(const Int4Rows& P, uint8_t* lds, int b
       from[i] = reinterpret_cast<const uint8_t*>(P.act + (a * TERMS + term) * kpad) + chunk;
     }
   }
+  auto column = [&](int k, int s) { return WK == 1 ? s : min(s * WK + k, ktiles - 1); };  // in tiles of 128
   auto copy = [&](int s, int to) {  // step s into buffer `to`
     uint8_t* dst = lds + to * STAGE + 256 * row0;
 #pragma unroll
     for (int i = 0; i < COPIES; i++) {
-      if constexpr (KIND == I4_LINEAR) copy16(reinterpret_cast<const int8_t*>(abase), off[i], s * 256, dst + 1024 * i);
+      if constexpr (KIND == I4_LINEAR)
+        copy16(reinterpret_cast<const int8_t*>(abase), off[i], column((row0 + 4 * i) / TOK, s) * 256, dst + 1024 * i);
       else
         __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from[i] + (size_t)s * 256),
                                          (__attribute__((address_space(3))) void*)(dst + 1024 * i), 16, 0, 0);
@@ -126,7 +133,8 @@ __device__ __forceinline__ void int4_tile(const Int4Rows& P, uint8_t* lds, int b
     u32x2 s[NM];
     uint32_t z[NM];
   };
-  auto fetch = [&](int s, Step& v) {
+  auto fetch = [&](int step, Step& v) {
+    const int s = column(wk, step);
 #pragma unroll
     for (int m = 0; m < NM; m++) {
       v.w[m] = ld16(wp[m] + (size_t)s * 1024);
@@ -152,12 +160,11 @@ __device__ __forceinline__ void int4_tile(const Int4Rows& P, uint8_t* lds, int b
   // masks and the numbers whose mantissas take the nibbles, held in registers: one v_and_or each
   uint32_t m0 = 0x000F000Fu, m1 = 0x00F000F0u, o0 = 0x64006400u, o1 = 0x54005400u;
   asm volatile("" : "+s"(m0), "+s"(m1), "+v"(o0), "+v"(o1));
-  const int last = ktiles - 1;
   Step w[I4_STAGES];
   f16x8_t xv[2][TERMS][NT];  // operands of these 32 columns and the next
   u32x4 d;                   // the next fragment of weights
   auto read = [&](int buf, int j, int to) {
-    const uint8_t* x = lds + buf * STAGE + (wn * NT * 16 + n) * 256 + 16 * ((4 * j + g) ^ n);
+    const uint8_t* x = lds + buf * STAGE + (wk * TOK + wn * NT * 16 + n) * 256 + 16 * ((4 * j + g) ^ n);
 #pragma unroll
     for (int a = 0; a < TERMS; a++)
 #pragma unroll
@@ -175,16 +182,15 @@ __device__ __forceinline__ void int4_tile(const Int4Rows& P, uint8_t* lds, int b
     }
   };
   // Copies and fetches past the last step repeat it (into buffers that nobody reads), so that
-  // every wait counts the same.
-  fetch(0, w[0]);
-  asm volatile("" ::: "memory");
-  copy(0, 0);
-  copy(min(1, last), 1);
-  asm volatile("" ::: "memory");
-  fetch(min(1, last), w[1]);
-  asm volatile("" ::: "memory");
-  copy(min(2, last), 2);
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * COPIES) : "memory");  // copy 0 (older than the second fetch too)
+  // every wait counts the same. Waits for copies count the copies behind them alone.
+#pragma unroll
+  for (int i = 0; i < I4_STAGES; i++) {
+    if (i < I4_STAGES - 1) fetch(min(i, last), w[i]);
+    asm volatile("" ::: "memory");
+    copy(min(i, last), i);
+    asm volatile("" ::: "memory");
+  }
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * COPIES) : "memory");  // copy 0
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   read(0, 0, 0);
@@ -197,7 +203,7 @@ __device__ __forceinline__ void int4_tile(const Int4Rows& P, uint8_t* lds, int b
       if (j < 3) {
         read(b, j + 1, (j + 1) & 1);
       } else {
-        // the next step's copies, and all reads of this one's; the copies of the one behind may be on their way
+        // the next step's copies, and all reads of this one's; the copies behind may be on their way
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(COPIES) : "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
@@ -221,7 +227,8 @@ __device__ __forceinline__ void int4_tile(const Int4Rows& P, uint8_t* lds, int b
           else acc[m][t] = c;
         }
         if (!SCALED && end) {
-          const float f = half_bits_f32(w[b].s[m][(j * GP / 4) / 2] >> (16 * (j * GP / 4 & 1)));
+          float f = half_bits_f32(w[b].s[m][(j * GP / 4) / 2] >> (16 * (j * GP / 4 & 1)));
+          if (WK > 1 && s * WK + wk >= ktiles) f = 0.f;  // past the end: the last step again
 #pragma unroll
           for (int t = 0; t < NT; t++)
 #pragma unroll
@@ -234,12 +241,32 @@ __device__ __forceinline__ void int4_tile(const Int4Rows& P, uint8_t* lds, int b
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  for (int s = 0; s < ktiles; s += I4_STAGES) {
+  for (int s = 0; s < steps; s += I4_STAGES) {
     step(s, Count<0>{});
-    if (s + 1 < ktiles) step(s + 1, Count<1>{});
-    if (s + 2 < ktiles) step(s + 2, Count<2>{});
+    if (s + 1 < steps) step(s + 1, Count<1>{});
+    if (s + 2 < steps) step(s + 2, Count<2>{});
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no copy outlives the work-group
+  if constexpr (WK > 1) {
+    static_assert((WK - 1) * WM * WN * NM * NT * 1024 <= I4_STAGES * STAGE, "the other waves' sums");
+    auto sums = [&](int k, int m, int t) {
+      return reinterpret_cast<f32x4_t*>(lds) + ((((k - 1) * WN * WM + wn * WM + wm) * NM + m) * NT + t) * 64 + lane;
+    };
+    __syncthreads();
+    if (wk > 0)
+#pragma unroll
+      for (int m = 0; m < NM; m++)
+#pragma unroll
+        for (int t = 0; t < NT; t++) *sums(wk, m, t) = tot[m][t];
+    __syncthreads();
+    if (wk > 0) return;
+#pragma unroll
+    for (int k = 1; k < WK; k++)
+#pragma unroll
+      for (int m = 0; m < NM; m++)
+#pragma unroll
+        for (int t = 0; t < NT; t++) tot[m][t] += *sums(k, m, t);
+  }
 
   // lane (n, g), register r of token tile t: token 16 t + 4 g + r, weight row n of the tile
   const int t0 = wn * NT * 16 + 4 * g;
@@ -281,22 +308,23 @@ __device__ __forceinline__ void int4_tile(const Int4Rows& P, uint8_t* lds, int b
   }
 }
 
-template <int GP, bool ZEROS, bool SCALED, int WM, int WN, int NM, int NT>
-__global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_int4_linear(Int4Rows P) {
+template <int GP, bool ZEROS, bool SCALED, int WM, int WN, int NM, int NT, int WK>
+__global__ __launch_bounds__(64 * WM * WN * WK, WM * WN * WK / 4) void k_int4_linear(Int4Rows P) {
   constexpr int TOK = 16 * NT * WN;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[I4_STAGES * TOK * 256];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[I4_STAGES * WK * TOK * 256];
   int bm, bn;
   tile_of(blockIdx.x, (int4_rtiles(P.rows) + WM * NM - 1) / (WM * NM), (P.T + TOK - 1) / TOK, bm, bn);
-  int4_tile<I4_LINEAR, GP, ZEROS, SCALED, WM, WN, NM, NT>(P, lds, bm, P.expert, bn * TOK, min(TOK, P.T - bn * TOK), nullptr);
+  int4_tile<I4_LINEAR, GP, ZEROS, SCALED, WM, WN, NM, NT, WK>(P, lds, bm, P.expert, bn * TOK, min(TOK, P.T - bn * TOK), nullptr);
 }
 
 // A chunk of up to PREFILL_MC pairs of an expert, 16 NT of them at a time; as many token tiles are
 // multiplied as there are. WAVES: to a SIMD.
-template <int KIND, int GP, bool ZEROS, int NM, int NT, int WAVES>
-__global__ __launch_bounds__(512, WAVES) void k_int4_experts(Int4Rows P) {
+template <int KIND, int GP, bool ZEROS, int WM, int NM, int NT, int WAVES>
+__global__ __launch_bounds__(64 * WM, WAVES) void k_int4_experts(Int4Rows P) {
+  static_assert(NT == 1 || NT == 2 || NT == 4, "token tiles below");
   constexpr int TOK = 16 * NT, RT = NM / (KIND == I4_GATE_UP ? 2 : 1);
   __shared__ __attribute__((aligned(16))) uint8_t lds[I4_STAGES * (KIND == I4_DOWN_PART ? 2 : 1) * TOK * 256];
-  const int nbm = (int4_rtiles(P.rows) + 8 * RT - 1) / (8 * RT);
+  const int nbm = (int4_rtiles(P.rows) + WM * RT - 1) / (WM * RT);
   // the row blocks of a chunk of tokens on one XCD: they share the tokens in its L2
   const int l = blockIdx.x / 8, q = l / nbm * 8 + (int)(blockIdx.x % 8), bm = l % nbm;
   if (q >= P.route.n_chunks()[0]) return;
@@ -306,38 +334,38 @@ __global__ __launch_bounds__(512, WAVES) void k_int4_experts(Int4Rows P) {
   const int32_t* perm = P.route.perm() + p0 + m0;
   if (e >= P.n_experts) {  // ids out of range
     if constexpr (KIND == I4_DOWN_PART)
-      for (int i = threadIdx.x; i < count * 128 * RT; i += 512) {
-        const int r = bm * 128 * RT + i % (128 * RT);
-        if (r < P.rows) ((float*)P.y)[(size_t)perm[i / (128 * RT)] * P.rows + r] = 0.f;
+      for (int i = threadIdx.x; i < count * 16 * WM * RT; i += 64 * WM) {
+        const int r = bm * 16 * WM * RT + i % (16 * WM * RT);
+        if (r < P.rows) ((float*)P.y)[(size_t)perm[i / (16 * WM * RT)] * P.rows + r] = 0.f;
       }
     return;
   }
   for (int m = 0; m < count; m += TOK) {
     const int here = min(TOK, count - m);
     if (m > 0) __syncthreads();  // the tile before has been read
-    if (NT == 1 || here <= 16) int4_tile<KIND, GP, ZEROS, false, 8, 1, NM, 1>(P, lds, bm, e, 0, here, perm + m);
-    else if (NT == 2 || here <= 32) int4_tile<KIND, GP, ZEROS, false, 8, 1, NM, NT < 2 ? 1 : 2>(P, lds, bm, e, 0, here, perm + m);
-    else if (here <= 48) int4_tile<KIND, GP, ZEROS, false, 8, 1, NM, NT < 4 ? 1 : 3>(P, lds, bm, e, 0, here, perm + m);
-    else int4_tile<KIND, GP, ZEROS, false, 8, 1, NM, NT < 4 ? 1 : 4>(P, lds, bm, e, 0, here, perm + m);
+    if (NT == 1 || here <= 16) int4_tile<KIND, GP, ZEROS, false, WM, 1, NM, 1>(P, lds, bm, e, 0, here, perm + m);
+    else if (NT == 2 || here <= 32) int4_tile<KIND, GP, ZEROS, false, WM, 1, NM, NT == 1 ? 1 : 2>(P, lds, bm, e, 0, here, perm + m);
+    else if (here <= 48) int4_tile<KIND, GP, ZEROS, false, WM, 1, NM, NT == 4 ? 3 : 1>(P, lds, bm, e, 0, here, perm + m);
+    else int4_tile<KIND, GP, ZEROS, false, WM, 1, NM, NT>(P, lds, bm, e, 0, here, perm + m);
   }
 }
 
-template <int GP, bool SCALED, int WM, int WN, int NM, int NT>
+template <int GP, bool SCALED, int WM, int WN, int NM, int NT, int WK = 1>
 hipError_t linear(const Int4Rows& p, hipStream_t s) {
   const long rows = 16 * WM * NM, tok = 16 * WN * NT;
-  const dim3 g((unsigned)((p.rows + rows - 1) / rows * ((p.T + tok - 1) / tok))), b(64 * WM * WN);
-  if (int4_zeros(p.fmt)) hipLaunchKernelGGL((k_int4_linear<GP, true, SCALED, WM, WN, NM, NT>), g, b, 0, s, p);
-  else hipLaunchKernelGGL((k_int4_linear<GP, false, SCALED, WM, WN, NM, NT>), g, b, 0, s, p);
+  const dim3 g((unsigned)((p.rows + rows - 1) / rows * ((p.T + tok - 1) / tok))), b(64 * WM * WN * WK);
+  if (int4_zeros(p.fmt)) hipLaunchKernelGGL((k_int4_linear<GP, true, SCALED, WM, WN, NM, NT, WK>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((k_int4_linear<GP, false, SCALED, WM, WN, NM, NT, WK>), g, b, 0, s, p);
   return hipGetLastError();
 }
 
-template <int KIND, int GP, int NM, int NT, int WAVES>
+template <int KIND, int GP, int WM, int NM, int NT, int WAVES>
 hipError_t experts(const Int4Rows& p, hipStream_t s) {
   constexpr int RT = NM / (KIND == I4_GATE_UP ? 2 : 1);
   const long items = RouteView::max_chunks(p.n_experts, p.T * p.top_k);
-  const dim3 g((unsigned)((int4_rtiles(p.rows) + 8 * RT - 1) / (8 * RT) * ((items + 7) / 8 * 8)));
-  if (int4_zeros(p.fmt)) hipLaunchKernelGGL((k_int4_experts<KIND, GP, true, NM, NT, WAVES>), g, dim3(512), 0, s, p);
-  else hipLaunchKernelGGL((k_int4_experts<KIND, GP, false, NM, NT, WAVES>), g, dim3(512), 0, s, p);
+  const dim3 g((unsigned)((int4_rtiles(p.rows) + WM * RT - 1) / (WM * RT) * ((items + 7) / 8 * 8)));
+  if (int4_zeros(p.fmt)) hipLaunchKernelGGL((k_int4_experts<KIND, GP, true, WM, NM, NT, WAVES>), g, dim3(64 * WM), 0, s, p);
+  else hipLaunchKernelGGL((k_int4_experts<KIND, GP, false, WM, NM, NT, WAVES>), g, dim3(64 * WM), 0, s, p);
   return hipGetLastError();
 }
 

@@ -68,24 +68,37 @@ __global__ __launch_bounds__(256) void k_int4_rows(const void* x, int cols, int 
   }
 }
 
-#ifndef MOEQ_I4_WIDE
-#define MOEQ_I4_WIDE 12
-#endif
-#ifndef MOEQ_I4_NT
-#define MOEQ_I4_NT 1
-#endif
+// Pairs to an expert, on average, from which gate/up takes tiles of 64 pairs with three waves to a
+// SIMD (weights are decoded once for up to 64) instead of 32 with four. Kernel times in us (256
+// experts, 4096 columns, 2048 rows of gate and up, groups of 128), 32 | 64: 12 pairs 437 | 456,
+// 18 452 | 483, 24 511 | 521, 30 620 | 549, 48 947 | 693. Eight waves to a work-group instead of four
+// took 864 at 48 pairs. With 16 pairs or fewer both multiply one tile of tokens.
+constexpr long WIDE_PAIRS = 27;
+// And those from which down (4096 rows, 2048 columns, two terms to a value) takes 32 pairs instead
+// of 16, whose buffers of LDS are half as large: 0.4 pairs 81 (16) | 93 (32), 3 pairs 221 | 230,
+// 9 pairs 247 | 255, 12 pairs 273 | 261, 48 pairs 800 | 615; tiles of 64 are no faster there.
+constexpr long MID_PAIRS = 10;
+
 template <int GP>
 hipError_t tiled_kind(int kind, const Int4Rows& p, hipStream_t s) {
   auto blocks = [&](int rows, int tok) { return (p.rows + (long)rows - 1) / rows * ((p.T + tok - 1) / tok); };
   if (kind == I4_LINEAR) {
     if (p.out_bf16 && blocks(256, 128) >= 192) return launch_int4_scaled(p, s);
     if (blocks(256, 64) >= 192) return linear<GP, false, 8, 1, 2, 4>(p, s);
-    if (p.T > 32) return linear<GP, false, 4, 1, 1, 4>(p, s);
-    return linear<GP, false, 4, 1, 1, 2>(p, s);
+    // Too few tiles of 256 rows x 64 tokens to fill the chip: 64 x 32, with two waves to an output,
+    // or four where all tokens lie in one tile. us, against one wave and tiles of 64 tokens (of 32):
+    // 100 tokens x 5003 x 4128, groups of 32, 21.0 (25.6); 256 x 4096 x 4096, groups of 128, 18.6
+    // (22.0); 24 x 2048 x 4096 11.4 (14.3). More buffers in place of waves changed nothing: what
+    // binds a step is the vector unit (four waves to a CU or eight alike), not memory.
+    if (p.T > 32) return linear<GP, false, 4, 1, 1, 2, 2>(p, s);
+    return linear<GP, false, 4, 1, 1, 2, 4>(p, s);
   }
-  const bool wide = (long)p.T * p.top_k >= (long)MOEQ_I4_WIDE * p.n_experts;
-  if (kind == I4_GATE_UP) return wide ? experts<I4_GATE_UP, GP, 2, 4, 2>(p, s) : experts<I4_GATE_UP, GP, 2, MOEQ_I4_NT, 4>(p, s);
-  return wide ? experts<I4_DOWN_PART, GP, 2, 4, 2>(p, s) : experts<I4_DOWN_PART, GP, 2, MOEQ_I4_NT, 4>(p, s);
+  const long pairs = (long)p.T * p.top_k;
+  if (kind == I4_GATE_UP)
+    return pairs >= WIDE_PAIRS * p.n_experts ? experts<I4_GATE_UP, GP, 4, 2, 4, 3>(p, s)
+                                             : experts<I4_GATE_UP, GP, 4, 2, 2, 4>(p, s);
+  return pairs >= MID_PAIRS * p.n_experts ? experts<I4_DOWN_PART, GP, 8, 2, 2, 4>(p, s)
+                                          : experts<I4_DOWN_PART, GP, 8, 2, 1, 4>(p, s);
 }
 
 }  // namespace
