@@ -25,7 +25,9 @@
  * thread, second post). The decode paths agree with the exact layer to the
  * documented tolerance, the prefill path with the same layer on MXFP8
  * activations; which path runs depends only on formats, shapes, T and
- * alignment, never on the data.
+ * alignment, never on the data. INT4 projections (codes as exact operands of the bf16
+ * or fp16 matrix instruction, group scales on fp32 sums) run pair by pair while that
+ * reads few weights twice, and grouped by expert beyond.
  *
  * Conventions for every entry point:
  *  - Pointers named *_host are host memory; every other buffer pointer is device
@@ -395,12 +397,15 @@ int moeq_linear_int8_dynamic(const moeq_weight* w, int expert, const void* x, in
 int moeq_pack_int4(int fmt, const void* codes, const void* scales, int scale_type, const uint8_t* zeros, int rows, int cols,
                    int n, void* data, void* scales_out, float* scale2, void* stream);
 
-/* y[t][r] = sum_k W[r][k] x[t][k] (+ bias[r]) for expert `expert` of an INT4 weight. Products
- * are exact, sums are fp32 with the scales applied to them, one rounding to the output type.
+/* y[t][r] = sum_k W[r][k] x[t][k] (+ bias[r]) for expert `expert` of an INT4 weight. Sums of
+ * exact products in fp32, scales applied to each group's sum, one rounding to the output type;
+ * beyond 16 tokens a value below 2^-39 of its token's largest loses low bits. bf16 outputs of
+ * large batches come from weights (the scale in them) rounded to fp16, 2^-11 each at most. Which
+ * of these depends on shapes and out_type alone.
  * x bf16 [T][cols], 16-byte aligned; bias fp32 [rows] or NULL; y [T][rows] overwritten, fp32
  * or bf16 (MOEQ_OUT_*), aligned to its element. A token that holds an infinity or a NaN
- * gives NaN, and nobody else's outputs change. Sums over a group have to stay inside fp32's
- * range, which |x| < 2^112 ensures. ws: moeq_linear_int4_workspace_bytes(T, cols) bytes,
+ * gives NaN, and nobody else's outputs change. Up to 16 tokens, sums over a group have to stay
+ * inside fp32's range, which |x| < 2^112 ensures. ws: moeq_linear_int4_workspace_bytes(T, cols) bytes,
  * 256-byte aligned, contents arbitrary, not shared with an overlapping call; NULL for up to
  * 16 tokens. Any T; T == 0 is a no-op. */
 size_t moeq_linear_int4_workspace_bytes(int T, int cols);
