@@ -57,12 +57,10 @@ __device__ __forceinline__ uint64_t order_of(double k) {
 // Lanes to a group of experts: the largest power of two that leaves every group its own.
 __device__ __forceinline__ int group_lanes(int n_groups) { return 1 << (31 - __builtin_clz(64 / n_groups)); }
 
-// Which groups of experts a wave's token keeps. Lanes gl q .. gl q + gl - 1 (gl =
-// group_lanes()) hold the two largest biased scores of their parts of group q, a NaN as
-// -inf; the result's bit gl q is set where q is kept. Groups past the last take part with
-// lanes of their own that hold -inf and are never counted.
-__device__ __forceinline__ uint64_t keep_groups(double a, double b, int n_groups, int top_groups, bool top2, int lane) {
-  const int gl = group_lanes(n_groups);
+// The merit of a group, as an integer of its order, from the two largest biased scores of its
+// parts, which lie in lanes gl q .. gl q + gl - 1 for group q (gl = group_lanes(); a NaN as -inf);
+// in each of these lanes. Lanes past the last group take part with numbers that nobody counts.
+__device__ __forceinline__ uint64_t group_merit(double a, double b, int gl, bool top2) {
   for (int o = 1; o < gl; o <<= 1) {
     const double c = __shfl_xor(a, o, 64), d = __shfl_xor(b, o, 64);
     const double low = a < c ? a : c;
@@ -70,12 +68,20 @@ __device__ __forceinline__ uint64_t keep_groups(double a, double b, int n_groups
     b = b > d ? b : d;
     b = b > low ? b : low;
   }
-  const uint64_t mine = order_of(top2 && b > -__builtin_inf() ? a + b : top2 ? -__builtin_inf() : a);
-  const int q = lane / gl;
+  return order_of(top2 && b > -__builtin_inf() ? a + b : top2 ? -__builtin_inf() : a);
+}
+__device__ __forceinline__ uint64_t read_lane(uint64_t v, int lane) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane) |
+         ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane) << 32);
+}
+
+// Which groups of experts a wave's token keeps: bit gl q of the result for group q.
+__device__ __forceinline__ uint64_t keep_groups(double a, double b, int n_groups, int top_groups, bool top2, int lane) {
+  const int gl = group_lanes(n_groups), q = lane / gl;
+  const uint64_t mine = group_merit(a, b, gl, top2);
   int rank = 0;
   for (int o = 0; o < n_groups; o++) {
-    const uint64_t v = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)mine, o * gl) |
-                       ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(mine >> 32), o * gl) << 32);
+    const uint64_t v = read_lane(mine, o * gl);
     rank += v > mine || (v == mine && o < q);
   }
   return __ballot(q < n_groups && lane % gl == 0 && rank < top_groups);

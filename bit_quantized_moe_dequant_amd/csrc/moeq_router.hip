@@ -98,6 +98,11 @@ __global__ __launch_bounds__(256) void k_router_choose(RouterParams P) {
 //      chosen. (Each costs 1 to 2 us, one after another: experts whose logits are equal, not
 //      known from the norms and more than a few would be slow.)
 //
+// Groups: between 1. and 2. the same bounds and lower ones give every group's merit from above and
+// below; while that leaves the kept groups open, an exact logit at a time closes it (a token in
+// ten, a few logits each). Experts of other groups then drop out. 2048 tokens, 4096 x 256 in 8
+// groups: k_router_pick 44 us.
+//
 // The bound d_e = router_unit() |W_e| |x| + 2^-100: moeq_router_bound.h.
 //
 // Measured at 2048 tokens, 4096 x 256, 6 of them: 38 us (13 and 26) against 92 with all logits
@@ -177,6 +182,20 @@ __device__ __forceinline__ float score_above(int scoring, float v) {
   return __builtin_sqrtf(p + 2.0f * p * slack) + 1e-18f;
 }
 
+// The other end: a number not above the score of any logit that is not below v.
+__device__ __forceinline__ float score_below(int scoring, float v) {
+  v = v - __builtin_fabsf(v) * 0x1p-23f;
+  const float slack = 0x1p-17f + __builtin_fminf(__builtin_fabsf(v), 1e6f) * 0x1p-22f;
+  if (scoring == SCORE_SIGMOID) {
+    const float p = __fdividef(1.0f, 1.0f + __expf(-v));
+    return __builtin_fmaxf(p - p * slack - 1e-18f, 0.f);
+  }
+  const float e = __expf(-__builtin_fabsf(v));
+  const float l = e < 0.015625f ? e * (1.0f - e * (0.5f - e * 0.33333334f)) : __logf(1.0f + e);
+  const float p = __builtin_fmaxf(v, 0.f) + l;
+  return __builtin_fmaxf(__builtin_sqrtf(__builtin_fmaxf(p - 2.0f * p * slack, 0.f)) - 1e-18f, 0.f);
+}
+
 // The lane that holds the largest (value, then lowest id) and that value; by every lane.
 __device__ __forceinline__ int lane_of_max(uint64_t v, uint32_t id, uint64_t& top) {
   const uint32_t mh = wave_max((uint32_t)(v >> 32));
@@ -197,10 +216,12 @@ constexpr int RP_SEG = 4096;  // values of a token held at a time (64 to a lane)
 
 // Two waves to a SIMD at least: left free, the compiler hoists conversions and constants
 // until a SIMD holds one.
-template <int N>
+template <int N, bool GROUPS>
 __global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_count) {
+  __shared__ double ends[GROUPS ? 4 : 1][2][GROUPS ? 64 * N : 1];  // GROUPS: a wave's keys, from above and from below
   const int lane = threadIdx.x & 63;
-  const int t = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = blockIdx.x * 4 + wave;
   if (t >= P.T) return;
   const uint16_t* x = P.x + (size_t)t * P.hidden;
   const int chunks = P.hidden / 8, E = P.n_experts, K = P.top_k;
@@ -305,6 +326,14 @@ __global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_co
       double k = z[i] + (router_unit() * size + 0x1p-100);
       if (!soft) k = (double)score_above(P.scoring, (float)k);
       if (P.bias) k += (double)P.bias[e];
+      if constexpr (GROUPS) {  // never a softmax
+        double l = (double)score_below(P.scoring, (float)(z[i] - (router_unit() * size + 0x1p-100)));
+        if (P.bias) l += (double)P.bias[e];
+        const bool open = !(__builtin_fabs(z[i]) < __builtin_inf() && k == k && l == l);
+        const bool out = P.bias && P.bias[e] != P.bias[e];
+        ends[wave][0][e] = out ? -__builtin_inf() : open ? __builtin_inf() : k;
+        ends[wave][1][e] = out || open ? -__builtin_inf() : l;
+      }
       // nothing is known of a sum that left fp32's range: its exact logit is needed
       bound[i] = __builtin_fabs(z[i]) < __builtin_inf() && k == k ? order_of(k) : ~0ull;
       if (P.bias && P.bias[e] != P.bias[e]) bound[i] = order_of(-__builtin_inf());
@@ -325,8 +354,61 @@ __global__ __launch_bounds__(256, 2) void k_router_pick(RouterParams P, int z_co
     for (int i = 0; i < N; i++)
       if (known >> i & 1) {
         const double s = z[i] == 0.0 ? s0 : z[i];
-        bound[i] = order_of(P.bias ? s + (double)P.bias[lane + 64 * i] : s);
+        const double k = P.bias ? s + (double)P.bias[lane + 64 * i] : s;
+        bound[i] = order_of(k);
+        if constexpr (GROUPS) ends[wave][0][lane + 64 * i] = ends[wave][1][lane + 64 * i] = k == k ? k : -__builtin_inf();
       }
+  }
+  if constexpr (GROUPS) {
+    const int size = E / P.n_groups, gl = group_lanes(P.n_groups), q = lane / gl;
+    const bool top2 = P.group_top2 && size > 1;
+    double* up = ends[wave][0];
+    double* down = ends[wave][1];
+    uint64_t kept;
+    for (;;) {  // each time around one more expert's ends meet, until the groups are told apart
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // what other lanes wrote
+      double a[2] = {-__builtin_inf(), -__builtin_inf()}, b[2] = {-__builtin_inf(), -__builtin_inf()};
+      double most = -__builtin_inf();  // of this lane's experts whose ends lie apart the highest
+      int at = -1;
+      if (q < P.n_groups)
+        for (int i = lane % gl; i < size; i += gl) {
+          const int e = q * size + i;
+          const double v[2] = {up[e], down[e]};
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            const double low = a[h] < v[h] ? a[h] : v[h];
+            a[h] = a[h] > v[h] ? a[h] : v[h];
+            b[h] = b[h] > low ? b[h] : low;
+          }
+          if (v[0] > v[1] && (at < 0 || v[0] > most)) {
+            most = v[0];
+            at = e;
+          }
+        }
+      const uint64_t above = group_merit(a[0], b[0], gl, top2), below = group_merit(a[1], b[1], gl, top2);
+      int maybe = 0, surely = 0;  // groups that may come before this one, and that must
+      for (int o = 0; o < P.n_groups; o++) {
+        const uint64_t oa = read_lane(above, o * gl), ob = read_lane(below, o * gl);
+        if (o == q) continue;
+        maybe += o < q ? oa >= below : oa > below;
+        surely += o < q ? ob >= above : ob > above;
+      }
+      kept = __ballot(q < P.n_groups && lane % gl == 0 && maybe < P.top_groups);
+      const bool open = q < P.n_groups && maybe >= P.top_groups && surely < P.top_groups;
+      if (__ballot(open) == 0) break;
+      // the highest such expert of a group whose merit is not known: an undecided group's, else any's
+      uint64_t from = __ballot(open && above > below && at >= 0);
+      if (from == 0) from = __ballot(above > below && at >= 0);
+      if (from == 0) break;  // not reached: merits that are known tell the groups apart
+      uint64_t top;
+      const bool in = from >> lane & 1;
+      const int e = __builtin_amdgcn_readlane(at, lane_of_max(in ? order_of(most) : 0ull, in ? (uint32_t)at : 0xFFFFFFFFu, top));
+      const double s = score(logit(e)), k = P.bias ? s + (double)P.bias[e] : s;
+      if (lane == 0) up[e] = down[e] = k == k ? k : -__builtin_inf();
+    }
+#pragma unroll
+    for (int i = 0; i < N; i++)
+      if (!(kept >> ((lane + 64 * i) / size * gl & 63) & 1)) bound[i] = 0;
   }
   const bool mine = lane < K;  // lane k < K: an expert of the best K so far, its exact logit and key
   int id = 0;
@@ -438,7 +520,12 @@ hipError_t launch_router(const RouterParams& p, hipStream_t s) {
   // The denominator of a softmax takes all logits, and fp32 ones would be off by up to
   // 274 x 2^-23 |W_e| |x| each. It cancels where the K weights are normalised, unless a bias makes
   // the choice depend on it.
-  if (!groups && (p.scoring != SCORE_SOFTMAX || (p.normalize && !p.bias))) {
+  // With groups a softmax's merits depend on it too; and there the keys' ends and the undecided
+  // groups' exact logits cost more, so that few logits are sooner all taken in fp64. us, bounds |
+  // fp64, experts in 8 groups: 512 tokens x 4096 x 256 47 | 33, 1024 49 | 54, 1536 59 | 75, 2048 57 | 95;
+  // 2048 x 4096 x 64 45 | 34; 512 x 4096 x 1024 79 | 105; 1024 x 8192 x 512 90 | 180.
+  const bool many = (double)p.T * p.n_experts * p.hidden >= 0x1p30;
+  if (groups ? many && p.scoring != SCORE_SOFTMAX : p.scoring != SCORE_SOFTMAX || (p.normalize && !p.bias)) {
     for (long t0 = 0; t0 < p.T; t0 += ROUTER_TOKENS) {
       RouterParams q = p;
       q.T = (int)(p.T - t0 < ROUTER_TOKENS ? p.T - t0 : ROUTER_TOKENS);
@@ -450,9 +537,13 @@ hipError_t launch_router(const RouterParams& p, hipStream_t s) {
       const int z_bytes = (2 * q.hidden / z + 127) / 128 * 128;
       hipLaunchKernelGGL(k_router_mm, dim3((unsigned)(tiles * z + (q.n_experts + 3) / 4)), dim3(256), 0, s, q, z, z_bytes, tiles);
       const dim3 g((unsigned)((q.T + 3) / 4)), b(256);
-      if (q.n_experts <= 256) hipLaunchKernelGGL(k_router_pick<4>, g, b, 0, s, q, z);
-      else if (q.n_experts <= 512) hipLaunchKernelGGL(k_router_pick<8>, g, b, 0, s, q, z);
-      else hipLaunchKernelGGL(k_router_pick<16>, g, b, 0, s, q, z);
+      auto pick = [&](auto n) {
+        if (groups) hipLaunchKernelGGL((k_router_pick<decltype(n)::value, true>), g, b, 0, s, q, z);
+        else hipLaunchKernelGGL((k_router_pick<decltype(n)::value, false>), g, b, 0, s, q, z);
+      };
+      if (q.n_experts <= 256) pick(Count<4>{});
+      else if (q.n_experts <= 512) pick(Count<8>{});
+      else pick(Count<16>{});
     }
     return hipGetLastError();
   }

@@ -140,6 +140,65 @@ def test_all_groups_kept_is_the_router_without_groups():
             assert torch.equal(got[0], plain[0]) and torch.equal(got[1], plain[1])
 
 
+MANY = [  # 2^30 products and more: logits with bounds, and exact ones of those that matter
+    (2100, 2048, 256, 6, 8, 4), (1100, 4096, 240, 8, 5, 2), (280, 4104, 960, 16, 30, 7), (700, 4096, 400, 6, 50, 9),
+    (4200, 4096, 64, 3, 64, 7), (9000, 520, 240, 4, 3, 1), (140, 8200, 1000, 8, 8, 3),
+]
+
+
+@pytest.mark.parametrize("case", MANY)
+@pytest.mark.parametrize("kind,by", list(itertools.product(("sigmoid", "sqrtsoftplus"), ("top2", "max"))))
+def test_groups_of_many_logits(case, kind, by):
+    test_groups(case, kind, by)
+
+
+@pytest.mark.parametrize("by", ["top2", "max"])
+def test_ties_among_many_logits(by):
+    """Equal groups, equal experts, tokens of zeros, and merits that differ by a few parts in 1e8."""
+    say("groups many ties", by)
+    T, H = 4200, 4096
+    x, w, _ = make(T, H, 16, 1)
+    x[::3] = 0
+    same = w.repeat(4, 1)
+    for kind in ("sigmoid", "sqrtsoftplus"):
+        r = mq.Router(same, 4, scoring=kind, n_groups=4, top_groups=2, group_score=by)
+        ids = mq.router_topk(r, x)[0].cpu().numpy()
+        assert np.array_equal(ids, groups_ref(host(x), host(same), 4, kind, False, 1.0, None, 4, 2, by)[0]) and ids.max() < 32
+        flat = mq.Router(w[:1].repeat(64, 1), 5, scoring=kind, n_groups=8, top_groups=3, group_score=by)
+        assert mq.router_topk(flat, x)[0].cpu().tolist() == [[0, 1, 2, 3, 4]] * T
+    x, w, _ = make(T, H, 64, 5)
+    w[32:] = w[:32]
+    w[32:, 100] = (w[:32, 100].float() * (1 + 2.0 ** -8)).to(torch.bfloat16)
+    x[:, 100] = 2.0 ** -14
+    ref = groups_ref(host(x), host(w), 6, "sigmoid", True, 1.0, None, 8, 3, by)
+    dm, dk = (np.abs(np.diff(np.sort(a, axis=1), axis=1)) for a in (ref[2][1], ref[2][0]))
+    apart = ((dm == 0) | (dm > 1e-12)).all(axis=1) & ((dk == 0) | (dk > 1e-13)).all(axis=1)
+    assert apart.any() and (np.where(dm == 0, 1.0, dm).min(axis=1)[apart] < 1e-6).any()
+    r = mq.Router(w, 6, scoring="sigmoid", normalize=True, n_groups=8, top_groups=3, group_score=by)
+    assert np.array_equal(mq.router_topk(r, x)[0].cpu().numpy()[apart], ref[0][apart])
+
+
+@pytest.mark.parametrize("by", ["top2", "max"])
+def test_masks_among_many_logits(by):
+    say("groups many masks", by)
+    T, H = 5600, 4096
+    x, w, b = make(T, H, 48, 7)
+    b[:8], b[8:15], b[20] = -np.inf, -np.inf, np.nan
+    w[30, 3] = float("nan")
+    w[33] = 0
+    w[40, 5] = float("inf")
+    x[T - 1, 9] = float("nan")
+    x[7] = 0
+    for kind in ("sigmoid", "sqrtsoftplus"):
+        r = mq.Router(w, 6, scoring=kind, bias=b, n_groups=6, top_groups=2, group_score=by)
+        ids, rw = mq.router_topk(r, x)
+        ref = groups_ref(host(x), host(w), 6, kind, False, 1.0, host(b), 6, 2, by)
+        ok = clear((None, None, tuple(np.where(np.isfinite(a), a, 1e3 * np.arange(1, a.shape[1] + 1)) for a in ref[2])), T)
+        assert ok.mean() > 0.9
+        assert np.array_equal(ids.cpu().numpy()[ok], ref[0][ok])
+        assert np.allclose(rw.cpu().numpy()[ok], ref[1][ok], rtol=2.0 ** -23, atol=0, equal_nan=True)
+
+
 @pytest.mark.parametrize("T", [2, 64, 150])
 def test_graph_and_streams(T):
     say("groups graph", T)
