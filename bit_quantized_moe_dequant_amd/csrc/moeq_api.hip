@@ -131,15 +131,13 @@ double touched_experts(const moeq_layer* L, int T);
 
 // INT4 projections pair by pair (each pair's expert read for itself, h in one launch more) or
 // tiled over each expert's tokens (four launches more): pair by pair while what is read twice
-// takes less than those launches. MOEQ_INT4_DIRECT_US at 4.5 TB/s; 4096 x 2048 experts, 6 of 256:
-// 1 / 2 / 4 / 8 tokens 24 / 36 / 64 / 130 us so, tiled 8 / 12 / 16 tokens 149 / 178 / 227.
-#ifndef MOEQ_INT4_DIRECT_US
-#define MOEQ_INT4_DIRECT_US 15.0
-#endif
+// takes less than those launches, INT4_DIRECT_US at 4.5 TB/s. 4096 x 2048 experts, 6 of 256, 1 / 2 /
+// 4 / 8 / 12 tokens: 24 / 36 / 64 / 124 / 160 us so; tiled 8 / 12 / 16 tokens 149 / 178 / 206.
+constexpr double INT4_DIRECT_US = 15.0;
 bool int4_direct(const moeq_layer* L, int T) {
   if (T == 1) return true;
   const double extra = (double)T * L->top_k - touched_experts(L, T);
-  return (long)T * L->top_k <= 65535 && extra * 1.6 * L->hidden * L->inter < MOEQ_INT4_DIRECT_US * 4.5e6;
+  return (long)T * L->top_k <= 65535 && extra * 1.6 * L->hidden * L->inter < INT4_DIRECT_US * 4.5e6;
 }
 bool int4_gu_direct(const moeq_layer* L, int T) { return int4_direct(L, T) && int4_one_fits(I4_GATE_UP, L->top_k, L->hidden); }
 bool int4_dn_direct(const moeq_layer* L, int T) { return int4_direct(L, T) && int4_one_fits(I4_DOWN_SUM, L->top_k, L->inter); }

@@ -99,8 +99,8 @@ __global__ __launch_bounds__(256) void k_router_choose(RouterParams P) {
 //      known from the norms and more than a few would be slow.)
 //
 // Groups: between 1. and 2. the same bounds and lower ones give every group's merit from above and
-// below; while that leaves the kept groups open, an exact logit at a time closes it (a token in
-// ten, a few logits each). Experts of other groups then drop out. 2048 tokens, 4096 x 256 in 8
+// below; while that leaves the kept groups open, an exact logit at a time closes it. Experts of
+// other groups then drop out. 2048 tokens, 4096 x 256 in 8
 // groups: k_router_pick 44 us.
 //
 // The bound d_e = router_unit() |W_e| |x| + 2^-100: moeq_router_bound.h.

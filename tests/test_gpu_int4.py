@@ -99,6 +99,15 @@ def test_linear_columns_that_end_inside_a_tile(fmt, cols):
         check(p, w, T, seed=T, out=torch.float32, bias=False)
 
 
+@pytest.mark.parametrize("cols", list(range(128, 1300, 128)))
+def test_linear_steps_that_several_waves_share(cols):
+    p = Parts(mq.FMT_INT4Z_G32 if cols % 256 else mq.FMT_INT4_G128, 1, 70, cols, seed=cols)
+    w = p.pack()
+    for T in (20, 32, 33, 70):
+        say("linear shared", cols, T)
+        check(p, w, T, seed=T, out=torch.float32, bias=T == 33)
+
+
 @pytest.mark.parametrize("scale", [2.0 ** -100, 2.0 ** 80])
 def test_linear_of_very_small_and_large_tokens(scale):
     p = Parts(mq.FMT_INT4Z_G64, 1, 48, 512, seed=5)

@@ -159,6 +159,70 @@ def test_stages_and_noalloc(T):
     assert torch.equal(mq.expert_forward_noalloc(ex.layer, xt, ti, tr, dev_err=err), y) and int(err) == 0
 
 
+@pytest.mark.parametrize("shape", [(256, 2944, 7, 6), (128, 5888, 4, 3)])
+def test_pairs_whose_h_is_too_long_for_one_work_group(shape):
+    """A few tokens with gate/up pair by pair and down by expert, the stages of one token without route."""
+    H, I, E, K = shape
+    ex = Experts(H, I, E, K, Z64, G64, seed=21)
+    for T in (1, 2, 5):
+        say("experts long", shape, T)
+        xt, ti, tr, y, ref, tol = check(ex, T, seed=T)
+        if T == 1:
+            ws = ex.layer.workspace(1)
+            h = mq.gate_up(ex.layer, xt, ti, ws=ws)
+            got = mq.down(ex.layer, h, ti, tr, ws=ws)
+            assert np.all(np.abs(got.double().cpu().numpy() - ref) <= tol)
+
+
+@pytest.mark.parametrize("T", [1, 3, 30, 200])
+def test_the_same_expert_twice(T):
+    say("experts twice", T)
+    ex = Experts(256, 192, 6, 3, G128, Z64, seed=31)
+    ids = ex.routing(T, 8)[0]
+    ids[:, 2] = ids[:, 0]
+    check(ex, T, seed=T, ids=ids)
+    ids[:] = 5
+    check(ex, T, seed=T, ids=ids)
+
+
+@pytest.mark.parametrize("T", [1, 6, 45, 330])
+def test_graphs_and_streams(T):
+    """Two captured graphs on workspaces of their own, replayed in turn with other inputs beside eager calls
+    on another stream."""
+    say("experts graph", T)
+    ex = Experts(384, 192, 8, 3, G64, G64, seed=41)
+    calls = []
+    for i in range(2):
+        xt, ti, tr, y, _, _ = check(ex, T, seed=50 + i)
+        out, ws = torch.empty_like(y), torch.zeros(mq.workspace_bytes(ex.layer, T) + 256, dtype=torch.uint8, device="cuda")
+        ws = ws[-ws.data_ptr() % 256:]
+        mq.expert_forward(ex.layer, xt, ti, tr, y=out, ws=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            mq.expert_forward(ex.layer, xt, ti, tr, y=out, ws=ws)
+        calls.append((graph, xt, ti, tr, out, ws))  # the graph's workspace lives as long as it
+    side = torch.cuda.Stream()
+    for r in range(3):
+        want = []
+        for i, (_, xt, ti, tr, out, _) in enumerate(calls):
+            g = torch.Generator(device="cuda")
+            g.manual_seed(100 * r + i)
+            xt.copy_(torch.randn(xt.shape, generator=g, device="cuda"))
+            ti.copy_(torch.from_numpy(ex.routing(T, 7 * r + i)[0]))
+            out.zero_()
+            want.append(mq.expert_forward(ex.layer, xt, ti, tr).clone())
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            other = mq.expert_forward(ex.layer, calls[0][1], calls[0][2], calls[0][3])
+        for graph, *_ in calls:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(other, want[0])
+        for call, w in zip(calls, want):
+            assert torch.equal(call[4], w)
+
+
 @pytest.mark.parametrize("T", [1, 6, 30, 150])
 @pytest.mark.parametrize("int4_down", [True, False])
 def test_beside_another_format(T, int4_down):
