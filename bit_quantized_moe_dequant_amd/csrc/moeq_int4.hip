@@ -16,8 +16,11 @@
 // T tokens fill the first output register of four lanes first (token i of a tile in row 4 i):
 // for up to four tokens a group's end costs two vector operations instead of eight.
 //
-// What bounds it: the weight stream. A tile of 512 weights costs a SIMD 8 vector operations
-// (32 clocks) and one matrix instruction of 16.
+// What bounds it: the weight stream, and where that is short the launch and one round of loads.
+// Measured, groups of 128: linear 1 x 4096 x 4096 5.3 us, 16 x 2048 x 4096 7.3 (groups of 64, zero
+// points); 6 experts of 4096 x 2048 for one token 12.9 + 10.2 us (4.0 and 2.5 TB/s), for eight
+// tokens 76 + 55 (5.5 and 3.8 TB/s). A tile of 512 weights costs a SIMD 8 vector operations (32
+// clocks) and one matrix instruction of 16.
 #include <hip/hip_ext.h>
 
 #include <algorithm>
@@ -496,7 +499,7 @@ template <int GP, int TERMS, int KIND, int DEPTH>
 hipError_t one(const Int4Params& p, int items, int rows, hipStream_t s, const LaunchEvents* ev) {
   const int steps = int4_ktiles(p.cols) * (KIND == I4_DOWN_SUM ? p.top_k : 1);
   // Row tiles of a work-group: one while every CU has up to three work-groups, then more (at most
-  // 16), which saves their beginnings: 8 tokens of 4096 x 2048 experts (6 of 256) 130 us, 169 with
+  // 16), which saves their beginnings: 8 tokens of 4096 x 2048 experts (6 of 256) 130 us then, 169 with
   // one each. (With 512, 1024 and 1536 work-groups instead of 768: 140, 147 and 138.)
   const long rt = int4_rtiles(p.rows);
   const int rb = (int)std::min(16l, std::max(1l, rt * items / 768));

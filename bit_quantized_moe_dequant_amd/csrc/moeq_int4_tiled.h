@@ -25,6 +25,12 @@
 // next step's first operands are read under those products. A wave decodes the next fragment of
 // weights between the products of one, as spread by the scheduling groups: left to the compiler,
 // the vector unit's and the matrix unit's work took turns.
+//
+// Measured, groups of 128: linear 2048 x 4096 x 4096 in bf16 69 us (1.0 PFLOP/s; its rows 8), 8192 x
+// 8192 x 4096 with zero points about 540 (454 with the decoding taken out: the vector unit's work
+// beside the products is what bounds it); 256 experts of 4096 x 2048, 6 to a token, 2048 tokens:
+// gate/up 650, down 590. For few tokens to an expert the weight stream bounds it: 16 tokens, groups
+// of 32, 4.9 TB/s.
 #pragma once
 #include "moeq_int4.h"
 #include "moeq_int8.h"
