@@ -324,3 +324,27 @@ def test_whole_layer_with_groups(T, shared, kind, by):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+def test_a_prompt_through_the_whole_layer_with_groups():
+    """1100 tokens x 4096 x 240 experts in 8 groups: the ids are the router's own, the sum the experts' for them."""
+    say("moe int4 prompt")
+    T, H, I, E, K = 1100, 4096, 64, 240, 3
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+
+    def int4(rows, cols):
+        codes = torch.randint(0, 256, (E, rows, cols // 2), generator=g, device="cuda", dtype=torch.uint8)
+        s = (0.5 + torch.rand((E, rows, cols // 64), generator=g, device="cuda")) / (4 * cols ** 0.5)
+        return mq.pack_int4(codes, s.to(torch.bfloat16))
+
+    layer = mq.Layer(H, I, E, K, int4(I, H), int4(I, H), int4(H, I))
+    x = torch.randn((T, H), generator=g, device="cuda").to(torch.bfloat16)
+    w = (torch.randn((E, H), generator=g, device="cuda") / 64).to(torch.bfloat16)
+    r = mq.Router(w, K, scoring="sigmoid", normalize=True, n_groups=8, top_groups=3)
+    y, ids, rw = mq.moe_forward(mq.MoeLayer(layer, r), x)
+    ids2, rw2 = mq.router_topk(r, x)
+    assert torch.equal(ids, ids2) and torch.equal(rw, rw2)
+    want = mq.expert_forward(layer, x, ids, rw)
+    # one rounding of the same sum to bf16, 2^-8, and 2^-20 of the row for sums in another order
+    assert bool(((y.float() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * want.abs().amax(dim=1, keepdim=True)).all())
