@@ -108,6 +108,26 @@ def test_linear_steps_that_several_waves_share(cols):
         check(p, w, T, seed=T, out=torch.float32, bias=T == 33)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_linear_of_large_tiles(fmt):
+    """Enough rows and tokens for the largest tiles, fp32 and bf16, odd in each size; all zero points."""
+    for rows, cols, T in ((8190, 128, 833), (6001, 544 if (fmt - mq.FMT_INT4_G32) % 3 == 0 else 640, 1100)):
+        p = Parts(fmt, 1, rows, cols, seed=rows + fmt, spread=0.5, zmax=255)
+        w = p.pack()
+        for out in (torch.float32, torch.bfloat16):
+            say("linear large", fmt, rows, cols, T, out)
+            check(p, w, T, seed=T, out=out, bias=True)
+
+
+@pytest.mark.parametrize("fmt", FMTS[3:])
+def test_linear_with_all_zero_points(fmt):
+    p = Parts(fmt, 1, 90, 640, seed=fmt, scale="fp16", zmax=255)
+    w = p.pack()
+    for T in (1, 3, 6, 12, 30, 90, 300):
+        say("linear zero points", fmt, T)
+        check(p, w, T, seed=T, out=torch.float32, bias=False)
+
+
 @pytest.mark.parametrize("scale", [2.0 ** -100, 2.0 ** 80])
 def test_linear_of_very_small_and_large_tokens(scale):
     p = Parts(mq.FMT_INT4Z_G64, 1, 48, 512, seed=5)
