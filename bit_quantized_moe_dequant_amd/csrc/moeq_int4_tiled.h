@@ -338,12 +338,11 @@ __global__ __launch_bounds__(64 * WM, WAVES) void k_int4_experts(Int4Rows P) {
   const int p0 = P.route.offsets()[e], m0 = P.route.chunk_m0()[q];
   const int count = min(PREFILL_MC, P.route.offsets()[e + 1] - p0 - m0);
   const int32_t* perm = P.route.perm() + p0 + m0;
-  if (e >= P.n_experts) {  // ids out of range
-    if constexpr (KIND == I4_DOWN_PART)
-      for (int i = threadIdx.x; i < count * 16 * WM * RT; i += 64 * WM) {
-        const int r = bm * 16 * WM * RT + i % (16 * WM * RT);
-        if (r < P.rows) ((float*)P.y)[(size_t)perm[i / (16 * WM * RT)] * P.rows + r] = 0.f;
-      }
+  if (e >= P.n_experts) {  // ids out of range: their h, or parts, are zeros
+    for (int i = threadIdx.x; i < count * 16 * WM * RT; i += 64 * WM) {
+      const int r = bm * 16 * WM * RT + i % (16 * WM * RT);
+      if (r < P.rows) ((float*)P.y)[(size_t)perm[i / (16 * WM * RT)] * P.rows + r] = 0.f;
+    }
     return;
   }
   for (int m = 0; m < count; m += TOK) {
