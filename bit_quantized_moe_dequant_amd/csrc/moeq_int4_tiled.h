@@ -7,12 +7,11 @@
 // packed addition takes 1024 + z away, nine vector operations for eight values. Activations come
 // as fp16, every row times a power of two of its own (k_int4_rows): a bf16 value keeps all its
 // bits down to 2^-39 of its row's largest; the intermediate h, fp32, is two fp16 terms, 22 bits.
-// Sums are fp32. Two ways to the scale:
-//   exact   a group's sum, of exact products, is multiplied by its scale in fp32 and added up
-//           (a vector operation per output and group);
-//   SCALED  the scale is multiplied into the weight, rounded to fp16 (2^-12 relative on average
-//           at most, each weight for itself; 1e-4 of the result), for outputs that are rounded
-//           to bf16 (2^-9) anyway.
+// A group's sum, of exact products, is multiplied by its scale in fp32 and added up (a vector
+// operation per output and group); sums are fp32. The scale multiplied into the weight instead,
+// rounded to fp16, would save those operations (bf16 outputs, tiles of 256 x 128: 2048 x 4096 x 4096
+// 80 us instead of 92, 8192 x 8192 x 4096 560 instead of 710), but every weight would be off by up to
+// 2^-11 and a token's outputs would differ with the batch it is in, by 8e-4.
 //
 // Activations are operand A (its rows: tokens), so a lane's outputs belong to one weight row and
 // need one scale per group. A work-group's waves stand WM x WN, each with NM row tiles of weights
@@ -26,9 +25,9 @@
 // weights between the products of one, as spread by the scheduling groups: left to the compiler,
 // the vector unit's and the matrix unit's work took turns.
 //
-// Measured, groups of 128: linear 2048 x 4096 x 4096 in bf16 69 us (1.0 PFLOP/s; its rows 8), 8192 x
-// 8192 x 4096 with zero points about 540 (454 with the decoding taken out: the vector unit's work
-// beside the products is what bounds it); 256 experts of 4096 x 2048, 6 to a token, 2048 tokens:
+// Measured: linear 2048 x 4096 x 4096, groups of 128, 84 us (0.82 PFLOP/s; its rows 8), 8192 x 8192 x
+// 4096, groups of 64, zero points, 690: the vector unit's work beside the products, decoding and
+// scales, is what bounds it. 256 experts of 4096 x 2048, 6 to a token, 2048 tokens, groups of 128:
 // gate/up 650, down 590. For few tokens to an expert the weight stream bounds it: 16 tokens, groups
 // of 32, 4.9 TB/s.
 #pragma once
@@ -51,9 +50,6 @@ constexpr int I4_STAGES = 3;  // buffers of activations, and sets of weights in 
 __device__ __forceinline__ uint32_t pk_add(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, a) + __builtin_bit_cast(f16x2_t, b));
 }
-__device__ __forceinline__ uint32_t pk_mul(uint32_t a, uint32_t b) {
-  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, a) * __builtin_bit_cast(f16x2_t, b));
-}
 __device__ __forceinline__ uint32_t pk_half(float v) {
   const uint32_t h = __builtin_bit_cast(uint16_t, (_Float16)v);
   return h | (h << 16);
@@ -74,13 +70,13 @@ __device__ __forceinline__ void spread() {
 // One work-group's tile: row block bm of expert e, activation rows first .. + count (LINEAR), or
 // the pairs perm[0 .. count); count at most 16 NT WN. WK: waves that share an output, each with
 // every WK-th step of columns; a step below is then WK of those, and the first wave adds up.
-template <int KIND, int GP, bool ZEROS, bool SCALED, int WM, int WN, int NM, int NT, int WK = 1>
+template <int KIND, int GP, bool ZEROS, int WM, int WN, int NM, int NT, int WK = 1>
 __device__ __forceinline__ void int4_tile(const Int4Rows& P, uint8_t* lds, int bm, int e, int first, int count,
                                           const int32_t* perm) {
   constexpr int TOK = 16 * NT * WN;
   constexpr int TERMS = KIND == I4_DOWN_PART ? 2 : 1, ROWS = WK * TERMS * TOK, STAGE = ROWS * 256;
   constexpr int WAVES = WM * WN * WK;
-  static_assert(WK == 1 || (KIND == I4_LINEAR && !SCALED), "steps shared by waves");
+  static_assert(WK == 1 || KIND == I4_LINEAR, "steps shared by waves");
   // copies of a wave per step, four LDS rows each (the waves past the last row repeat the first)
   constexpr int COPIES = (ROWS / 4 + WAVES - 1) / WAVES;
   static_assert(ROWS % (4 * COPIES) == 0, "no copy passes the end");
@@ -181,11 +177,6 @@ __device__ __forceinline__ void int4_tile(const Int4Rows& P, uint8_t* lds, int b
     const float z = ZEROS ? (float)(v.z[m] >> (8 * gi) & 255u) : 8.0f;
     const uint32_t c0 = pk_half(-1024.0f - z), c1 = pk_half(-64.0f - z), lo = v.w[m][j], hi = lo >> 8;
     d = u32x4{pk_add((lo & m0) | o0, c0), pk_add((lo & m1) | o1, c1), pk_add((hi & m0) | o0, c0), pk_add((hi & m1) | o1, c1)};
-    if constexpr (SCALED) {
-      const uint32_t sc = __builtin_amdgcn_perm(0u, v.s[m][gi / 2], gi & 1 ? 0x03020302u : 0x01000100u);
-#pragma unroll
-      for (int i = 0; i < 4; i++) d[i] = pk_mul(d[i], sc);
-    }
   };
   // Copies and fetches past the last step repeat it (into buffers that nobody reads), so that
   // every wait counts the same. Waits for copies count the copies behind them alone.
@@ -226,13 +217,12 @@ __device__ __forceinline__ void int4_tile(const Int4Rows& P, uint8_t* lds, int b
         else decode(w[nb], 0, 0);
 #pragma unroll
         for (int t = 0; t < NT; t++) {
-          f32x4_t c = SCALED ? tot[m][t] : begin ? f32x4_t{0.f, 0.f, 0.f, 0.f} : acc[m][t];
+          f32x4_t c = begin ? f32x4_t{0.f, 0.f, 0.f, 0.f} : acc[m][t];
           c = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv[j & 1][0][t], now, c, 0, 0, 0);
           if constexpr (TERMS == 2) c = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv[j & 1][TERMS - 1][t], now, c, 0, 0, 0);
-          if constexpr (SCALED) tot[m][t] = c;
-          else acc[m][t] = c;
+          acc[m][t] = c;
         }
-        if (!SCALED && end) {
+        if (end) {
           float f = half_bits_f32(w[b].s[m][(j * GP / 4) / 2] >> (16 * (j * GP / 4 & 1)));
           if (WK > 1 && s * WK + wk >= ktiles) f = 0.f;  // past the end: the last step again
 #pragma unroll
@@ -241,8 +231,7 @@ __device__ __forceinline__ void int4_tile(const Int4Rows& P, uint8_t* lds, int b
             for (int r = 0; r < 4; r++) tot[m][t][r] = __builtin_fmaf(f, acc[m][t][r], tot[m][t][r]);
         }
       }
-      if (SCALED) spread<NM * NT * TERMS, NM * 15, TERMS * NT>();
-      else if (end) spread<NM * NT * TERMS, NM * (11 + 4 * NT), TERMS * NT>();
+      if (end) spread<NM * NT * TERMS, NM * (11 + 4 * NT), TERMS * NT>();
       else spread<NM * NT * TERMS, NM * 11, TERMS * NT>();
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -314,13 +303,13 @@ __device__ __forceinline__ void int4_tile(const Int4Rows& P, uint8_t* lds, int b
   }
 }
 
-template <int GP, bool ZEROS, bool SCALED, int WM, int WN, int NM, int NT, int WK>
+template <int GP, bool ZEROS, int WM, int WN, int NM, int NT, int WK>
 __global__ __launch_bounds__(64 * WM * WN * WK, WM * WN * WK / 4) void k_int4_linear(Int4Rows P) {
   constexpr int TOK = 16 * NT * WN;
   __shared__ __attribute__((aligned(16))) uint8_t lds[I4_STAGES * WK * TOK * 256];
   int bm, bn;
   tile_of(blockIdx.x, (int4_rtiles(P.rows) + WM * NM - 1) / (WM * NM), (P.T + TOK - 1) / TOK, bm, bn);
-  int4_tile<I4_LINEAR, GP, ZEROS, SCALED, WM, WN, NM, NT, WK>(P, lds, bm, P.expert, bn * TOK, min(TOK, P.T - bn * TOK), nullptr);
+  int4_tile<I4_LINEAR, GP, ZEROS, WM, WN, NM, NT, WK>(P, lds, bm, P.expert, bn * TOK, min(TOK, P.T - bn * TOK), nullptr);
 }
 
 // A chunk of up to PREFILL_MC pairs of an expert, 16 NT of them at a time; as many token tiles are
@@ -348,19 +337,19 @@ __global__ __launch_bounds__(64 * WM, WAVES) void k_int4_experts(Int4Rows P) {
   for (int m = 0; m < count; m += TOK) {
     const int here = min(TOK, count - m);
     if (m > 0) __syncthreads();  // the tile before has been read
-    if (NT == 1 || here <= 16) int4_tile<KIND, GP, ZEROS, false, WM, 1, NM, 1>(P, lds, bm, e, 0, here, perm + m);
-    else if (NT == 2 || here <= 32) int4_tile<KIND, GP, ZEROS, false, WM, 1, NM, NT == 1 ? 1 : 2>(P, lds, bm, e, 0, here, perm + m);
-    else if (here <= 48) int4_tile<KIND, GP, ZEROS, false, WM, 1, NM, NT == 4 ? 3 : 1>(P, lds, bm, e, 0, here, perm + m);
-    else int4_tile<KIND, GP, ZEROS, false, WM, 1, NM, NT>(P, lds, bm, e, 0, here, perm + m);
+    if (NT == 1 || here <= 16) int4_tile<KIND, GP, ZEROS, WM, 1, NM, 1>(P, lds, bm, e, 0, here, perm + m);
+    else if (NT == 2 || here <= 32) int4_tile<KIND, GP, ZEROS, WM, 1, NM, NT == 1 ? 1 : 2>(P, lds, bm, e, 0, here, perm + m);
+    else if (here <= 48) int4_tile<KIND, GP, ZEROS, WM, 1, NM, NT == 4 ? 3 : 1>(P, lds, bm, e, 0, here, perm + m);
+    else int4_tile<KIND, GP, ZEROS, WM, 1, NM, NT>(P, lds, bm, e, 0, here, perm + m);
   }
 }
 
-template <int GP, bool SCALED, int WM, int WN, int NM, int NT, int WK = 1>
+template <int GP, int WM, int WN, int NM, int NT, int WK = 1>
 hipError_t linear(const Int4Rows& p, hipStream_t s) {
   const long rows = 16 * WM * NM, tok = 16 * WN * NT;
   const dim3 g((unsigned)((p.rows + rows - 1) / rows * ((p.T + tok - 1) / tok))), b(64 * WM * WN * WK);
-  if (int4_zeros(p.fmt)) hipLaunchKernelGGL((k_int4_linear<GP, true, SCALED, WM, WN, NM, NT, WK>), g, b, 0, s, p);
-  else hipLaunchKernelGGL((k_int4_linear<GP, false, SCALED, WM, WN, NM, NT, WK>), g, b, 0, s, p);
+  if (int4_zeros(p.fmt)) hipLaunchKernelGGL((k_int4_linear<GP, true, WM, WN, NM, NT, WK>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((k_int4_linear<GP, false, WM, WN, NM, NT, WK>), g, b, 0, s, p);
   return hipGetLastError();
 }
 

@@ -1,6 +1,4 @@
 // Launches of the tiled INT4 products (moeq_int4_tiled.h), and the activation rows they take.
-// The kernels with scaled weights are compiled apart (moeq_int4_scaled.hip), where the compiler
-// keeps their sums in accumulation registers; here the vector unit reads them.
 #include "moeq_int4_tiled.h"
 
 namespace moeq {
@@ -83,15 +81,14 @@ template <int GP>
 hipError_t tiled_kind(int kind, const Int4Rows& p, hipStream_t s) {
   auto blocks = [&](int rows, int tok) { return (p.rows + (long)rows - 1) / rows * ((p.T + tok - 1) / tok); };
   if (kind == I4_LINEAR) {
-    if (p.out_bf16 && blocks(256, 128) >= 192) return launch_int4_scaled(p, s);
-    if (blocks(256, 64) >= 192) return linear<GP, false, 8, 1, 2, 4>(p, s);
+    if (blocks(256, 64) >= 192) return linear<GP, 8, 1, 2, 4>(p, s);
     // Too few tiles of 256 rows x 64 tokens to fill the chip: 64 x 32, with two waves to an output,
     // or four where all tokens lie in one tile. us, against one wave and tiles of 64 tokens (of 32):
     // 100 tokens x 5003 x 4128, groups of 32, 21.0 (25.6); 256 x 4096 x 4096, groups of 128, 18.6
     // (22.0); 24 x 2048 x 4096 11.4 (14.3). More buffers in place of waves changed nothing: what
     // binds a step is the vector unit (four waves to a CU or eight alike), not memory.
-    if (p.T > 32) return linear<GP, false, 4, 1, 1, 2, 2>(p, s);
-    return linear<GP, false, 4, 1, 1, 2, 4>(p, s);
+    if (p.T > 32) return linear<GP, 4, 1, 1, 2, 2>(p, s);
+    return linear<GP, 4, 1, 1, 2, 4>(p, s);
   }
   const long pairs = (long)p.T * p.top_k;
   if (kind == I4_GATE_UP)

@@ -294,7 +294,6 @@ hipError_t launch_int4_terms(const float* h, size_t n_rows, int cols, uint16_t* 
 size_t int4_rows_bytes(size_t n_rows, int terms, int cols);
 // bf16 rows -> one fp16 term, fp32 rows -> two (see Int4Rows).
 hipError_t launch_int4_rows(bool in_f32, const void* x, size_t n_rows, int cols, uint16_t* out, float* scale, hipStream_t s);
-hipError_t launch_int4_scaled(const Int4Rows& p, hipStream_t s);  // bf16 linear in tiles of 256 rows x 128 tokens
 hipError_t launch_int4_tiled(int kind, const Int4Rows& p, hipStream_t s);
 
 // Chunk geometry: weights per 16-byte chunk; lanes per row and chunks per lane.
