@@ -8,6 +8,7 @@
 #include "moeq_int4.h"
 #include "moeq_kernels.h"
 
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 
@@ -142,6 +143,18 @@ bool int4_direct(const moeq_layer* L, int T) {
 bool int4_gu_direct(const moeq_layer* L, int T) { return int4_direct(L, T) && int4_one_fits(I4_GATE_UP, L->top_k, L->hidden); }
 bool int4_dn_direct(const moeq_layer* L, int T) { return int4_direct(L, T) && int4_one_fits(I4_DOWN_SUM, L->top_k, L->inter); }
 
+// The most tokens, fewer than T, whose down goes pair by pair, given that T's does not (what is read
+// twice grows with the tokens); 0 if none.
+int int4_dn_direct_tokens(const moeq_layer* L, int T) {
+  int a = 0, b = T;
+  while (b - a > 1) {
+    const int m = a + (b - a) / 2;
+    (int4_dn_direct(L, m) ? a : b) = m;
+  }
+  return a;
+}
+size_t int4_terms_bytes(const moeq_layer* L, int T) { return align_up((size_t)T * L->top_k * L->inter * 6, 256); }
+
 struct WsLayout {
   size_t route, h, partial, xq, xs, hq, hs, dq, ds, h4, xr, xrs, hr, hrs, total;
   int P;
@@ -177,12 +190,13 @@ WsLayout ws_layout(const moeq_layer* L, int T) {
   }
   if (is_int4(L->down.fmt) && !int4_dn_direct(L, T)) {  // and those of h
     w.hr = off;
-    off += align_up(int4_rows_bytes(P, 2, L->inter), 256);
-    w.hrs = off;
-    off += align_up(P * 4, 256);
+    w.hrs = w.hr + align_up(int4_rows_bytes(P, 2, L->inter), 256);
+    // not less than fewer tokens' bf16 terms: a workspace for more tokens serves fewer
+    const size_t terms = int4_terms_bytes(L, int4_dn_direct_tokens(L, T));
+    off += std::max(w.hrs - w.hr + align_up(P * 4, 256), terms);
   } else if (is_int4(L->down.fmt)) {  // h as three bf16 terms
     w.h4 = off;
-    off += align_up(P * L->inter * 6, 256);
+    off += int4_terms_bytes(L, T);
   }
   if (prefill_buffers(L, T)) {
     w.xq = off;
