@@ -215,15 +215,15 @@ __device__ __forceinline__ float int4_offset(const Side<GP, ZEROS, NMAT>& side, 
 // What becomes of the sums v (one per matrix) of weight row r and activation row t of the tile:
 // `pair` is its (token, slot) pair, or the token.
 template <int KIND, int NMAT>
-__device__ __forceinline__ void int4_store(const Int4Params& P, int e, bool ok, size_t pair, int r, const float (&v)[NMAT]) {
+__device__ __forceinline__ void int4_store(const Int4Params& P, bool ok, size_t pair, int r, const float (&v)[NMAT]) {
   if constexpr (KIND == I4_LINEAR) {
     const size_t at = pair * P.rows + r;
-    float f = v[0] * P.w[0].scale2[e];
+    float f = v[0];
     if (P.bias) f += P.bias[r];
     if (P.out_bf16) ((uint16_t*)P.y)[at] = (uint16_t)f32_bf16_rne_nan(f);
     else ((float*)P.y)[at] = f;
   } else if constexpr (KIND == I4_GATE_UP) {
-    const float h = ok ? silu_mul(v[0] * P.w[0].scale2[e], v[NMAT - 1] * P.w[1].scale2[e]) : 0.f;
+    const float h = ok ? silu_mul(v[0], v[NMAT - 1]) : 0.f;
     if (P.out_terms) {
       uint32_t b[3];
       bf16_terms(h, b);
@@ -308,6 +308,11 @@ __global__ __launch_bounds__(64 * one_waves(KIND)) void k_int4_one(Int4Params P,
     }
   }
 
+  // scale2, in every group's scale: the stored ones, 64 to 128, would carry the sums out of range first
+  float s2[NMAT];
+#pragma unroll
+  for (int m = 0; m < NMAT; m++) s2[m] = KIND == I4_DOWN_SUM ? 1.f : P.w[m].scale2[e];
+
   // A wave's tiles: row tile by row tile, step wave, wave + waves, ... of each
   struct At {
     int rt, u;
@@ -373,7 +378,7 @@ __global__ __launch_bounds__(64 * one_waves(KIND)) void k_int4_one(Int4Params P,
         v[m] = 0.f;
         for (int w = 0; w < waves; w++) v[m] += red[buf][w][m][t][n];
       }
-      if (r < P.rows) int4_store<KIND, NMAT>(P, e, ok, KIND == I4_LINEAR ? t : item, r, v);
+      if (r < P.rows) int4_store<KIND, NMAT>(P, ok, KIND == I4_LINEAR ? t : item, r, v);
     }
     buf ^= 1;
   };
@@ -382,7 +387,7 @@ __global__ __launch_bounds__(64 * one_waves(KIND)) void k_int4_one(Int4Params P,
     for (int d = 0; d < DEPTH; d++) {
       if (at.rt >= rt1) break;
       bool live = ok;
-      float f = 1.f;
+      float f = 1.f;  // I4_DOWN_SUM: its factor, scale2 in it
       int k = 0, kt = at.u;
       if constexpr (KIND == I4_DOWN_SUM) {
         k = at.u / ktiles;
@@ -405,8 +410,7 @@ __global__ __launch_bounds__(64 * one_waves(KIND)) void k_int4_one(Int4Params P,
             const int gi = j * GP / 4;
 #pragma unroll
             for (int m = 0; m < NMAT; m++) {
-              float s = int4_scale(side[d], m, gi);
-              if constexpr (KIND == I4_DOWN_SUM) s *= f;
+              const float s = int4_scale(side[d], m, gi) * (KIND == I4_DOWN_SUM ? f : s2[m]);
               const float c = int4_offset(side[d], m, gi);
 #pragma unroll
               for (int r = 0; r < NR; r++) tot[m][r] = __builtin_fmaf(s, __builtin_fmaf(-c, sx[r], acc[m][r]), tot[m][r]);
@@ -443,6 +447,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_int4_few(Int4Params P) {
   const int ai = (n & 3) + (n >> 2) * NR;
   const bool a_on = (n & 3) < NR && ai < P.T;
   const uint16_t* ap = P.act + (size_t)(a_on ? ai : 0) * P.pitch + 8 * g;
+  const float s2 = P.w[0].scale2[P.expert];
   float tot[NR];
 #pragma unroll
   for (int r = 0; r < NR; r++) tot[r] = 0.f;
@@ -472,7 +477,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_int4_few(Int4Params P) {
           sx = mfma(xv[i][j], ones(), sx);
           acc = mfma(xv[i][j], int4_operand(wv[i][0][j]), acc);
         }
-        const float s = int4_scale(side[i], 0, q), c = int4_offset(side[i], 0, q);
+        const float s = int4_scale(side[i], 0, q) * s2, c = int4_offset(side[i], 0, q);
 #pragma unroll
         for (int r = 0; r < NR; r++) tot[r] = __builtin_fmaf(s, __builtin_fmaf(-c, sx[r], acc[r]), tot[r]);
         hold(tot[NR - 1], acc, sx);
@@ -487,7 +492,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_int4_few(Int4Params P) {
     float v[1] = {0.f};
 #pragma unroll
     for (int w = 0; w < FEW_WAVES; w++) v[0] += red[w][t][n];
-    int4_store<I4_LINEAR, 1>(P, P.expert, true, t, r, v);
+    int4_store<I4_LINEAR, 1>(P, true, t, r, v);
   }
 }
 

@@ -403,10 +403,10 @@ int moeq_pack_int4(int fmt, const void* codes, const void* scales, int scale_typ
  * on shapes alone; out_type decides nothing but the last rounding.
  * x bf16 [T][cols], 16-byte aligned; bias fp32 [rows] or NULL; y [T][rows] overwritten, fp32
  * or bf16 (MOEQ_OUT_*), aligned to its element. A token that holds an infinity or a NaN
- * gives NaN, and nobody else's outputs change. Up to 16 tokens, sums over a group have to stay
- * inside fp32's range, which |x| < 2^112 ensures. ws: moeq_linear_int4_workspace_bytes(T, cols) bytes,
- * 256-byte aligned, contents arbitrary, not shared with an overlapping call; NULL for up to
- * 16 tokens. Any T; T == 0 is a no-op. */
+ * gives NaN, and nobody else's outputs change. Partial sums of an output have to stay inside
+ * fp32's range; up to 16 tokens also a group's sum of (16 + q) x, which |x| < 2^112 ensures.
+ * ws: moeq_linear_int4_workspace_bytes(T, cols) bytes, 256-byte aligned, contents arbitrary, not
+ * shared with an overlapping call; NULL for up to 16 tokens. Any T; T == 0 is a no-op. */
 size_t moeq_linear_int4_workspace_bytes(int T, int cols);
 int moeq_linear_int4(const moeq_weight* w, int expert, const void* x, int T, const float* bias, int out_type, void* y, void* ws,
                      size_t ws_bytes, void* stream);
