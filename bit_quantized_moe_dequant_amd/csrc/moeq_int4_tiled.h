@@ -6,7 +6,9 @@
 // nibble is laid into the mantissa of 1024 (or of 64, four bits higher) by a mask-and-or, and a
 // packed addition takes 1024 + z away, nine vector operations for eight values. Activations come
 // as fp16, every row times a power of two of its own (k_int4_rows): a bf16 value keeps all its
-// bits down to 2^-39 of its row's largest; the intermediate h, fp32, is two fp16 terms, 22 bits.
+// bits down to 2^-31 of its row's largest (fp16's last bit, 2^-24, is the eighth of 2^-17 there, and
+// the largest is 2^14 or more) and is rounded by up to 2^-39 of it below; the intermediate h, fp32, is
+// two fp16 terms, 22 bits down to 2^-17 of its row's largest, by up to 2^-39 of it off below.
 // A group's sum, of exact products, is multiplied by its scale in fp32 and added up (a vector
 // operation per output and group); sums are fp32. The scale multiplied into the weight instead,
 // rounded to fp16, would save those operations (bf16 outputs, tiles of 256 x 128: 2048 x 4096 x 4096

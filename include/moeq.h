@@ -399,8 +399,9 @@ int moeq_pack_int4(int fmt, const void* codes, const void* scales, int scale_typ
 
 /* y[t][r] = sum_k W[r][k] x[t][k] (+ bias[r]) for expert `expert` of an INT4 weight. Sums of
  * exact products in fp32, scales applied to each group's sum, one rounding to the output type;
- * beyond 16 tokens a value below 2^-39 of its token's largest loses low bits. The kernel depends
- * on shapes alone; out_type decides nothing but the last rounding.
+ * beyond 16 tokens a value keeps all its bits down to 2^-31 of its token's largest and is rounded
+ * by up to 2^-39 of that largest below. The kernel depends on shapes alone; out_type decides
+ * nothing but the last rounding.
  * x bf16 [T][cols], 16-byte aligned; bias fp32 [rows] or NULL; y [T][rows] overwritten, fp32
  * or bf16 (MOEQ_OUT_*), aligned to its element. A token that holds an infinity or a NaN
  * gives NaN, and nobody else's outputs change. Partial sums of an output have to stay inside

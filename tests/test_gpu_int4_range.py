@@ -1,4 +1,12 @@
-"""INT4 products at the ends of the value range."""
+"""INT4 products at the ends of the value range.
+
+Between rows of bf16 and fp16 (beyond 16 tokens): a row is multiplied by a power of two that brings its
+largest value into [2^14, 2^15), where fp16's smallest step is 2^-24. A bf16 value of eight bits keeps
+them all down to 2^-31 of that power of two (2^-31 is 2^-17 there, whose eighth bit is 2^-24); below, it
+is rounded to half a step, 2^-25 there, 2^-39 of the power of two.
+
+An intermediate value of fp32 (the tiled down) is two such numbers: 22 bits, 2^-23 of it, while the second
+is normal, and 2^-39 of the power of two at most where it is not."""
 import numpy as np
 import pytest
 import torch
@@ -48,3 +56,63 @@ def test_gate_up_near_the_largest_numbers(T):
     a, b = xd @ gate.values(1).T, xd @ up.values(1).T
     ref = (a / (1 + np.exp(-a)) * b)[:, None, :]
     assert np.isfinite(ref).all() and np.all(np.abs(h - ref) <= 1e-3 * np.abs(ref))
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("low", [30, 36, 44])
+@pytest.mark.parametrize("T", [3, 16, 17, 70])
+def test_small_values_beside_a_large_one(low, out, T):
+    """One value of 1 to a token, where the weights are 0, and the others 2^-low of it: up to 16 tokens
+    and down to 2^-31 nothing is lost, below that half a step, 2^-39 for each value."""
+    say("small beside large", low, out, T)
+    p = Parts(mq.FMT_INT4_G64, 1, 50, 640, seed=low)
+    p.q[:, :, 77] = 8
+    w = p.pack()
+    g = np.random.default_rng(T)
+    x = (1 + g.random((T, 640))) * np.where(g.random((T, 640)) < 0.5, -1, 1) * 2.0 ** -low
+    x[:, 77] = 1.0
+    xt, xd = bf16(x)
+    ref = xd @ p.values().T
+    small = xd.copy()
+    small[:, 77] = 0
+    tol = p.tol(small, 0) + 2.0 ** -23 * np.abs(ref)
+    if T <= mq.INT4_FEW_T:  # there the group that holds the 1 has it in its sum as 24 x 1 before it is taken off
+        one = np.zeros_like(xd)
+        one[:, 77] = 1
+        tol = tol + p.tol(one, 0)
+    elif low > 30:  # 2^-25 of the scaled value: 2^-39 of 1, for each of the row's values
+        tol = tol + 2.0 ** -39 * np.abs(p.values()).sum(axis=1)
+    if out == torch.bfloat16:
+        tol = tol + 1.01 * 2.0 ** -8 * np.abs(ref)
+    y = mq.linear_int4(w, xt, out_dtype=out).double().cpu().numpy()
+    assert np.all(np.abs(y - ref) <= tol), float((np.abs(y - ref) / tol).max())
+
+
+@pytest.mark.parametrize("low", [8, 18, 30, 45])
+def test_small_intermediate_values_beside_a_large_one(low):
+    """The down stage of 40 tokens by expert, every h with one value of 1 where the weights are 0."""
+    say("small h beside large", low)
+    T, H, I, E, K = 40, 1024, 768, 6, 3
+    gate, up, down = (Parts(mq.FMT_INT4_G64, E, *s, 5 + i) for i, s in enumerate([(I, H), (I, H), (H, I)]))
+    down.q[:, :, 77] = 8
+    layer = mq.Layer(H, I, E, K, gate.pack(), up.pack(), down.pack())
+    g = np.random.default_rng(low)
+    h = (1 + g.random((T, K, I))) * np.where(g.random((T, K, I)) < 0.5, -1, 1) * 2.0 ** -low
+    h[:, :, 77] = 1.0
+    h = h.astype(np.float32)
+    ids = np.stack([g.permutation(E)[:K] for _ in range(T)]).astype(np.int32)
+    rw = (0.2 + g.random((T, K))).astype(np.float32)
+    ti, tr = torch.from_numpy(ids).cuda(), torch.from_numpy(rw).cuda()
+    ws = layer.workspace(T)
+    mq.route(layer, ti, ws=ws)
+    y = mq.down(layer, torch.from_numpy(h).cuda(), ti, tr, ws=ws).double().cpu().numpy()
+    hd = h.astype(np.float64)
+    hd[:, :, 77] = 0
+    ref, tol = np.zeros((T, H)), np.zeros((T, H))
+    for e in range(E):
+        t, k = np.nonzero(ids == e)
+        r, v, w = rw[t, k].astype(np.float64)[:, None], hd[t, k], down.values(e)
+        o, off = v @ w.T, np.maximum(2.0 ** -23 * np.abs(v), 2.0 ** -39) @ np.abs(w).T
+        np.add.at(ref, t, r * o)
+        np.add.at(tol, t, r * (off + down.tol(v, e) + 2.0 ** -22 * np.abs(o)))
+    assert np.all(np.abs(y - ref) <= tol), float((np.abs(y - ref) / tol).max())
