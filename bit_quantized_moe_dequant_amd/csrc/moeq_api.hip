@@ -409,7 +409,7 @@ int run_gate_up_int4(const moeq_layer* L, const void* x, const int32_t* ids, int
     Int4Rows p = int4_rows(L->gate, L, T, xr, xrs, h);
     p.w[1] = ref_of(L->up);
     p.route = route_view(L, ws, lay);
-    return hip_rc(launch_int4_tiled(I4_GATE_UP, p, s));
+    return hip_rc(launch_int4_tiled(I4_GATE_UP, p, s, ev));
   }
   Int4Params p = int4_params(L->gate, x, L->hidden, 0, T, h);
   p.w[1] = ref_of(L->up);
@@ -449,11 +449,11 @@ int run_gate_up(const moeq_layer* L, const void* x, const int32_t* ids, int T, f
   int slots = L->n_experts + 1;
   if (T * L->top_k + 1 < slots) slots = T * L->top_k + 1;
   if (L->gate.fmt == MOEQ_FMT_IQ2_XXS && gu_iq2_fits(L->inter, L->hidden))
-    return hip_rc(launch_gu_iq2(p, slots, (double)T * L->top_k >= MOEQ_IQ2_WIDE_FROM * L->n_experts, s));
+    return hip_rc(launch_gu_iq2(p, slots, (double)T * L->top_k >= MOEQ_IQ2_WIDE_FROM * L->n_experts, s, ev));
   const bool fp4_g = (MOEQ_MX4_BATCHED && L->gate.fmt == MOEQ_FMT_MXFP4) ||
                      (L->gate.fmt == MOEQ_FMT_NVFP4 && pairs_per_expert(L, T) >= MOEQ_NV4_GROUPED_FROM);
   if (fp4_g && gu_mx4_g_fits(L->inter, L->hidden) && scales16(L->gate) && scales16(L->up))
-    return hip_rc(launch_gu_fp4_g(L->gate.fmt, p, slots, s));
+    return hip_rc(launch_gu_fp4_g(L->gate.fmt, p, slots, s, ev));
   return hip_rc(launch_gemv(L->gate.fmt, EPI_SWIGLU, p, slots, grouped_wide(L, T) ? 4 : 1, s, ev));
 }
 

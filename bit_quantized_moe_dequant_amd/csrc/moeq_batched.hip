@@ -35,6 +35,7 @@
 // term t of x on 16-block d of the step (zeros elsewhere); the lane holding output
 // rows 4 q .. 4 q + 3 multiplies them by their blocks' E4M3 scales (one 32-bit word
 // of the row's scale plane, converted once per step for all pairs of the tile).
+#include <hip/hip_ext.h>
 #include <hip/hip_runtime.h>
 
 #include "moeq_device.h"
@@ -481,13 +482,12 @@ __global__ __launch_bounds__(GB_NT) void k_dn_mx4_g(GemvParams P) {
 bool gu_mx4_g_fits(int rows, int cols) { return rows > 0 && cols > 0 && cols % 512 == 0 && cols <= GU_KMAX; }
 bool dn_mx4_g_fits(int rows, int cols) { return rows > 0 && cols > 0 && cols % 512 == 0 && cols <= DN_KMAX; }
 
-hipError_t launch_gu_fp4_g(int fmt, const GemvParams& p, int n_slots, hipStream_t s) {
+hipError_t launch_gu_fp4_g(int fmt, const GemvParams& p, int n_slots, hipStream_t s, const LaunchEvents* ev) {
   if (!gu_mx4_g_fits(p.rows, p.cols) || (fmt != FMT_MXFP4 && fmt != FMT_NVFP4)) return hipErrorInvalidValue;
   const dim3 g((unsigned)((p.rows + 15) / 16), (unsigned)n_slots);
-  if (fmt == FMT_NVFP4)
-    hipLaunchKernelGGL(k_gu_fp4_g<FMT_NVFP4>, g, dim3(GU_NT), 0, s, p);
-  else
-    hipLaunchKernelGGL(k_gu_fp4_g<FMT_MXFP4>, g, dim3(GU_NT), 0, s, p);
+  auto k = fmt == FMT_NVFP4 ? k_gu_fp4_g<FMT_NVFP4> : k_gu_fp4_g<FMT_MXFP4>;
+  if (ev) hipExtLaunchKernelGGL(k, g, dim3(GU_NT), 0, s, ev->start, ev->stop, 0, p);
+  else hipLaunchKernelGGL(k, g, dim3(GU_NT), 0, s, p);
   return hipGetLastError();
 }
 

@@ -27,6 +27,7 @@
 // four lanes per row loading the whole row the kernel was bound by those loads.
 // Token lanes past the expert's last token read that token again (same
 // addresses) and are not stored.
+#include <hip/hip_ext.h>
 #include <hip/hip_runtime.h>
 
 #include "moeq_device.h"
@@ -742,11 +743,12 @@ bool gu_iq2_fits(int rows, int cols) {
   return rows > 0 && cols > 0 && cols % 256 == 0 && (long)rows * (cols / 256) * 64 < (1L << 31);
 }
 
-hipError_t launch_gu_iq2(const GemvParams& p, int n_slots, bool wide, hipStream_t s) {
+hipError_t launch_gu_iq2(const GemvParams& p, int n_slots, bool wide, hipStream_t s, const LaunchEvents* ev) {
   if (!gu_iq2_fits(p.rows, p.cols) || (long)p.T * p.cols * 2 >= (1L << 31)) return hipErrorInvalidValue;
   dim3 g((unsigned)((p.rows + GI_ROWS - 1) / GI_ROWS), (unsigned)n_slots);
-  if (wide) hipLaunchKernelGGL(k_gu_iq2_wide, g, dim3(64 * GI_WAVES), 0, s, p);
-  else hipLaunchKernelGGL(k_gu_iq2, g, dim3(64 * GI_WAVES), 0, s, p);
+  auto k = wide ? k_gu_iq2_wide : k_gu_iq2;
+  if (ev) hipExtLaunchKernelGGL(k, g, dim3(64 * GI_WAVES), 0, s, ev->start, ev->stop, 0, p);
+  else hipLaunchKernelGGL(k, g, dim3(64 * GI_WAVES), 0, s, p);
   return hipGetLastError();
 }
 

@@ -33,6 +33,8 @@
 // gate/up 650, down 590. For few tokens to an expert the weight stream bounds it: 16 tokens, groups
 // of 32, 4.9 TB/s.
 #pragma once
+#include <hip/hip_ext.h>
+
 #include "moeq_int4.h"
 #include "moeq_int8.h"
 #include "moeq_tiled.h"
@@ -356,12 +358,13 @@ hipError_t linear(const Int4Rows& p, hipStream_t s) {
 }
 
 template <int KIND, int GP, int WM, int NM, int NT, int WAVES>
-hipError_t experts(const Int4Rows& p, hipStream_t s) {
+hipError_t experts(const Int4Rows& p, hipStream_t s, const LaunchEvents* ev = nullptr) {
   constexpr int RT = NM / (KIND == I4_GATE_UP ? 2 : 1);
   const long items = RouteView::max_chunks(p.n_experts, p.T * p.top_k);
   const dim3 g((unsigned)((int4_rtiles(p.rows) + WM * RT - 1) / (WM * RT) * ((items + 7) / 8 * 8)));
-  if (int4_zeros(p.fmt)) hipLaunchKernelGGL((k_int4_experts<KIND, GP, true, WM, NM, NT, WAVES>), g, dim3(64 * WM), 0, s, p);
-  else hipLaunchKernelGGL((k_int4_experts<KIND, GP, false, WM, NM, NT, WAVES>), g, dim3(64 * WM), 0, s, p);
+  auto k = int4_zeros(p.fmt) ? k_int4_experts<KIND, GP, true, WM, NM, NT, WAVES> : k_int4_experts<KIND, GP, false, WM, NM, NT, WAVES>;
+  if (ev) hipExtLaunchKernelGGL(k, g, dim3(64 * WM), 0, s, ev->start, ev->stop, 0, p);
+  else hipLaunchKernelGGL(k, g, dim3(64 * WM), 0, s, p);
   return hipGetLastError();
 }
 

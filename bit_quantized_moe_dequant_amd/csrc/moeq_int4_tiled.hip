@@ -78,7 +78,7 @@ constexpr long WIDE_PAIRS = 27;
 constexpr long MID_PAIRS = 10;
 
 template <int GP>
-hipError_t tiled_kind(int kind, const Int4Rows& p, hipStream_t s) {
+hipError_t tiled_kind(int kind, const Int4Rows& p, hipStream_t s, const LaunchEvents* ev) {
   auto blocks = [&](int rows, int tok) { return (p.rows + (long)rows - 1) / rows * ((p.T + tok - 1) / tok); };
   if (kind == I4_LINEAR) {
     if (blocks(256, 64) >= 192) return linear<GP, 8, 1, 2, 4>(p, s);
@@ -92,8 +92,8 @@ hipError_t tiled_kind(int kind, const Int4Rows& p, hipStream_t s) {
   }
   const long pairs = (long)p.T * p.top_k;
   if (kind == I4_GATE_UP)
-    return pairs >= WIDE_PAIRS * p.n_experts ? experts<I4_GATE_UP, GP, 4, 2, 4, 3>(p, s)
-                                             : experts<I4_GATE_UP, GP, 4, 2, 2, 4>(p, s);
+    return pairs >= WIDE_PAIRS * p.n_experts ? experts<I4_GATE_UP, GP, 4, 2, 4, 3>(p, s, ev)
+                                             : experts<I4_GATE_UP, GP, 4, 2, 2, 4>(p, s, ev);
   return pairs >= MID_PAIRS * p.n_experts ? experts<I4_DOWN_PART, GP, 8, 2, 2, 4>(p, s)
                                           : experts<I4_DOWN_PART, GP, 8, 2, 1, 4>(p, s);
 }
@@ -117,15 +117,15 @@ hipError_t launch_int4_rows(bool in_f32, const void* x, size_t n_rows, int cols,
   return hipGetLastError();
 }
 
-hipError_t launch_int4_tiled(int kind, const Int4Rows& p, hipStream_t s) {
+hipError_t launch_int4_tiled(int kind, const Int4Rows& p, hipStream_t s, const LaunchEvents* ev) {
   if (!is_int4(p.fmt) || p.T < 1 || p.rows < 1 || p.rows > INT4_MAX_ROWS || p.cols < 32 || p.cols > INT4_MAX_COLS ||
       p.cols % int4_group(p.fmt))
     return hipErrorInvalidValue;
   auto run = [&](const Int4Rows& q) {
     switch (int4_group(q.fmt)) {
-      case 32: return tiled_kind<4>(kind, q, s);
-      case 64: return tiled_kind<2>(kind, q, s);
-      default: return tiled_kind<1>(kind, q, s);
+      case 32: return tiled_kind<4>(kind, q, s, ev);
+      case 64: return tiled_kind<2>(kind, q, s, ev);
+      default: return tiled_kind<1>(kind, q, s, ev);
     }
   };
   if (kind != I4_LINEAR) return run(p);

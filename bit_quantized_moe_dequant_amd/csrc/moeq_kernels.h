@@ -233,7 +233,7 @@ hipError_t launch_dn_iq2(const GemvParams& p, int n_slots, hipStream_t s);
 bool gu_iq2_fits(int rows, int cols);  // cols % 256 == 0
 // Grouped gate/up + SwiGLU for IQ2_XXS on the bf16 matrix instruction (T > 1).
 // wide: decode each superblock once for two 16-token tiles (many tokens per expert).
-hipError_t launch_gu_iq2(const GemvParams& p, int n_slots, bool wide, hipStream_t s);
+hipError_t launch_gu_iq2(const GemvParams& p, int n_slots, bool wide, hipStream_t s, const LaunchEvents* ev = nullptr);
 bool linear_fp8_fits(int rows, int cols);  // rows % 128 == 0, cols % 256 == 0
 hipError_t launch_linear_fp8(const LinearParams& p, hipStream_t s);
 
@@ -241,7 +241,8 @@ hipError_t launch_linear_fp8(const LinearParams& p, hipStream_t s);
 // matrix instruction, each routed expert's weights read once per step.
 bool gu_mx4_g_fits(int rows, int cols);  // cols % 512 == 0, cols <= 4096
 bool dn_mx4_g_fits(int rows, int cols);  // cols % 512 == 0, cols <= 2048
-hipError_t launch_gu_fp4_g(int fmt, const GemvParams& p, int n_slots, hipStream_t s);  // MXFP4 or NVFP4
+hipError_t launch_gu_fp4_g(int fmt, const GemvParams& p, int n_slots, hipStream_t s,
+                           const LaunchEvents* ev = nullptr);  // MXFP4 or NVFP4
 hipError_t launch_dn_mx4_g(const GemvParams& p, int n_slots, hipStream_t s);
 
 bool linear_mx8_fits(int fmt, int rows, int cols);  // rows % 16, cols % 128 (pre-stored: % 512), cols <= 8192
@@ -294,7 +295,8 @@ hipError_t launch_int4_terms(const float* h, size_t n_rows, int cols, uint16_t* 
 size_t int4_rows_bytes(size_t n_rows, int terms, int cols);
 // bf16 rows -> one fp16 term, fp32 rows -> two (see Int4Rows).
 hipError_t launch_int4_rows(bool in_f32, const void* x, size_t n_rows, int cols, uint16_t* out, float* scale, hipStream_t s);
-hipError_t launch_int4_tiled(int kind, const Int4Rows& p, hipStream_t s);
+// ev: I4_GATE_UP only.
+hipError_t launch_int4_tiled(int kind, const Int4Rows& p, hipStream_t s, const LaunchEvents* ev = nullptr);
 
 // Chunk geometry: weights per 16-byte chunk; lanes per row and chunks per lane.
 int weights_per_chunk(int fmt);

@@ -300,7 +300,8 @@ int moeq_down(const moeq_layer* L, const float* h, const int32_t* ids, const flo
 
 /* moeq_gate_up with its kernel launched so that start_event / stop_event (two
  * hipEvent_t created with timing, passed as void*) record the kernel's own start
- * and end, for timing that excludes queue gaps. Same arguments and outputs. */
+ * and end, for timing that excludes queue gaps (of the product, where a launch before it
+ * prepares the tokens). Same arguments and outputs. T == 0 records nothing. */
 int moeq_gate_up_timed(const moeq_layer* L, const void* x, const int32_t* ids, int T, float* h, void* ws,
                        size_t ws_bytes, void* stream, void* start_event, void* stop_event);
 
