@@ -132,8 +132,10 @@ double touched_experts(const moeq_layer* L, int T);
 
 // INT4 projections pair by pair (each pair's expert read for itself, h in one launch more) or
 // tiled over each expert's tokens (four launches more): pair by pair while what is read twice
-// takes less than those launches, INT4_DIRECT_US at 4.5 TB/s. 4096 x 2048 experts, 6 of 256, 1 / 2 /
-// 4 / 8 / 12 tokens: 24 / 36 / 64 / 124 / 160 us so; tiled 8 / 12 / 16 tokens 149 / 178 / 206.
+// takes less than those launches, INT4_DIRECT_US at 4.5 TB/s. us of a call pair by pair | tiled, groups
+// of 128: 4096 x 2048 experts, 6 of 256, 2 tokens 36 | 56, 4 65 | 76, 6 110 | 100, 8 128 | 141, 10 180 | 152,
+// 12 198 | 164, 16 237 | 209 (tiled from 10 on); 2048 x 1024, 6 of 64, 8 39 | 46, 12 56 | 48 (from 11 on);
+// 1024 x 512, 4 of 32, 16 24 | 34, 32 36 | 35 (from 28 on).
 constexpr double INT4_DIRECT_US = 15.0;
 bool int4_direct(const moeq_layer* L, int T) {
   if (T == 1) return true;
