@@ -143,7 +143,16 @@ bool int4_direct(const moeq_layer* L, int T) {
   return (long)T * L->top_k <= 65535 && extra * 1.6 * L->hidden * L->inter < INT4_DIRECT_US * 4.5e6;
 }
 bool int4_gu_direct(const moeq_layer* L, int T) { return int4_direct(L, T) && int4_one_fits(I4_GATE_UP, L->top_k, L->hidden); }
-bool int4_dn_direct(const moeq_layer* L, int T) { return int4_direct(L, T) && int4_one_fits(I4_DOWN_SUM, L->top_k, L->inter); }
+// A down that leaves one work-group to a CU reads slower, which costs more than the tiled form's
+// launches from INT4_DOWN_ALONE weights of all pairs on. us of a call, groups of 128, pair by pair |
+// down tiled: 4096 x 2048, 8 of 256, 1 token (67M weights) 29 | 42, 2 (134M) 50 | 55, 3 (201M) 73 | 73,
+// 4 (268M) 112 | 100; 7168 x 2048, 8 of 256, 1 (117M) 46 | 53, 2 (235M) 99 | 88; 1024 x 2048, 8 of 64, 6 (101M)
+// 44 | 48, 8 (134M) 54 | 54.
+constexpr double INT4_DOWN_ALONE = 170e6;
+bool int4_dn_direct(const moeq_layer* L, int T) {
+  if (!int4_direct(L, T) || !int4_one_fits(I4_DOWN_SUM, L->top_k, L->inter)) return false;
+  return int4_down_two_to_a_cu(L->top_k, L->inter) || (double)T * L->top_k * L->hidden * L->inter < INT4_DOWN_ALONE;
+}
 
 // The most tokens, fewer than T, whose down goes pair by pair, given that T's does not (what is read
 // twice grows with the tokens); 0 if none.

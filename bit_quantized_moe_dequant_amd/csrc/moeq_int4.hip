@@ -496,8 +496,11 @@ __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_int4_few(Int4Params P) {
   }
 }
 
-// LDS of k_int4_one's rows (each term one); more than this and the other kernel takes them.
-constexpr size_t ONE_LDS = 96 << 10;
+// LDS of k_int4_one's rows (each term one); more than this and the other kernels take them. A linear
+// of up to four tokens: longer rows are faster in k_int4_few (4 x 4096 x 14336, 112 KB, 10.0 us there
+// and 11.9 here; 4 x 8192 x 16384 20.5 and 28.3). A down's parts may fill a CU (160 KB, the sums' LDS among
+// them): where more than half of that leaves one work-group to a CU, the caller decides.
+constexpr size_t ONE_LDS = 96 << 10, ONE_LDS_DOWN = 150 << 10;
 size_t one_lds(int rows, int cols) { return 16 + (size_t)rows * (int4_ktiles(cols) * 256 + 16); }
 
 template <int GP, int TERMS, int KIND, int DEPTH>
@@ -547,8 +550,10 @@ hipError_t few_kind(int kind, const Int4Params& p, int items, hipStream_t s, con
 }  // namespace
 
 bool int4_one_fits(int kind, int top_k, int cols) {
-  return one_lds(kind == I4_DOWN_SUM ? 3 * top_k : 1, cols) <= ONE_LDS;
+  return kind == I4_DOWN_SUM ? one_lds(3 * top_k, cols) <= ONE_LDS_DOWN : one_lds(1, cols) <= ONE_LDS;
 }
+
+bool int4_down_two_to_a_cu(int top_k, int cols) { return one_lds(3 * top_k, cols) <= 78 << 10; }
 
 hipError_t launch_int4_few(int kind, const Int4Params& p, int items, hipStream_t s, const LaunchEvents* ev) {
   if (!is_int4(p.fmt) || p.T < 1 || items < 1 || items > 65535 || p.rows < 1 || p.rows > INT4_MAX_ROWS || p.cols < 32 ||

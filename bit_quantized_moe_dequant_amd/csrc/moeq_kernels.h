@@ -289,6 +289,7 @@ hipError_t launch_dequant_int4(int fmt, const WeightRef& w, int rows, int cols, 
 // items: pairs (I4_GATE_UP) or tokens (I4_DOWN_SUM), whose activations have to fit a work-group
 // (int4_one_fits); I4_LINEAR: up to INT4_FEW_T tokens.
 bool int4_one_fits(int kind, int top_k, int cols);
+bool int4_down_two_to_a_cu(int top_k, int cols);  // of the work-groups of I4_DOWN_SUM
 hipError_t launch_int4_few(int kind, const Int4Params& p, int items, hipStream_t s, const LaunchEvents* ev = nullptr);
 // fp32 rows -> their three bf16 terms [n_rows][3][cols].
 hipError_t launch_int4_terms(const float* h, size_t n_rows, int cols, uint16_t* planes, hipStream_t s);
