@@ -17,4 +17,8 @@ constexpr long int8_tokens(int rows) {
 // size is not split at that number), and 2^20 work-groups of four tokens.
 constexpr long ROUTER_TOKENS = 1 << 22;
 
+// Packing and dequantisation of INT4 tensors: work-groups of 256 threads to a launch, with four tiles
+// of 2048 weights or 256 times eight weights each.
+constexpr long INT4_BLOCKS = 1 << 23;
+
 }  // namespace moeq

@@ -26,6 +26,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "moeq_grid.h"
 #include "moeq_int4.h"
 #include "moeq_int8.h"
 
@@ -63,9 +64,9 @@ __device__ __forceinline__ int int4_exponent(uint32_t max_bits) {
 __global__ __launch_bounds__(256) void k_int4_pack(int group, const uint8_t* codes, const uint16_t* scales, int bf16,
                                                    const uint8_t* zeros, int rows, int cols, uint8_t* data, uint8_t* out,
                                                    size_t data_bytes, size_t scale_bytes, size_t zeros_at,
-                                                   const uint32_t* max_bits) {
+                                                   const uint32_t* max_bits, size_t block0) {
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4, kt_n = int4_ktiles(cols);
-  const size_t tile = (size_t)blockIdx.x * 4 + (threadIdx.x >> 6), e = blockIdx.y;
+  const size_t tile = (block0 + blockIdx.x) * 4 + (threadIdx.x >> 6), e = blockIdx.y;
   if (tile >= int4_tiles(rows, cols)) return;
   const int r = (int)(tile / kt_n) * 16 + n, k0 = (int)(tile % kt_n) * 128;
   u32x4 w;
@@ -105,8 +106,9 @@ __global__ void k_int4_scale2(float* scale2, int n) {
 
 // One thread per 8 columns of a row.
 __global__ __launch_bounds__(256) void k_int4_dequant(int group, const uint8_t* data, const uint8_t* scales, size_t zeros_at,
-                                                      bool zeros, const float* scale2, int rows, int cols, float* out) {
-  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+                                                      bool zeros, const float* scale2, int rows, int cols, float* out,
+                                                      size_t block0) {
+  const size_t i = (block0 + blockIdx.x) * 256 + threadIdx.x;
   const int per_row = cols / 8;
   if (i >= (size_t)rows * per_row) return;
   const int r = (int)(i / per_row), k = (int)(i % per_row) * 8;
@@ -590,19 +592,22 @@ hipError_t launch_pack_int4(int fmt, const uint8_t* codes, const uint16_t* scale
     const uint16_t* sc = scales + (size_t)e0 * per;
     const unsigned mb = (unsigned)(per + 4095 < 4096 * 64 ? (per + 4095) / 4096 : 64);
     hipLaunchKernelGGL(k_int4_max, dim3(mb, m), dim3(256), 0, s, sc, (int)scales_bf16, per, (uint32_t*)scale2 + e0);
-    hipLaunchKernelGGL(k_int4_pack, dim3((unsigned)((tiles + 3) / 4), m), dim3(256), 0, s, group, c, sc, (int)scales_bf16,
-                       zeros ? zeros + (size_t)e0 * per : nullptr, rows, cols, data + e0 * db, out_scales + e0 * sb, db, sb,
-                       int4_zeros_at(fmt, rows, cols), (const uint32_t*)scale2 + e0);
+    const size_t blocks = (tiles + 3) / 4;
+    for (size_t b0 = 0; b0 < blocks; b0 += INT4_BLOCKS)
+      hipLaunchKernelGGL(k_int4_pack, dim3((unsigned)std::min<size_t>(blocks - b0, INT4_BLOCKS), m), dim3(256), 0, s, group, c, sc,
+                         (int)scales_bf16, zeros ? zeros + (size_t)e0 * per : nullptr, rows, cols, data + e0 * db,
+                         out_scales + e0 * sb, db, sb, int4_zeros_at(fmt, rows, cols), (const uint32_t*)scale2 + e0, b0);
   }
   hipLaunchKernelGGL(k_int4_scale2, dim3((n + 255) / 256), dim3(256), 0, s, scale2, n);
   return hipGetLastError();
 }
 
 hipError_t launch_dequant_int4(int fmt, const WeightRef& w, int rows, int cols, int expert, float* out, hipStream_t s) {
-  const size_t n = (size_t)rows * (cols / 8);
-  hipLaunchKernelGGL(k_int4_dequant, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, int4_group(fmt),
-                     w.data + (size_t)expert * w.estride, w.scales + (size_t)expert * w.sestride, int4_zeros_at(fmt, rows, cols),
-                     int4_zeros(fmt), w.scale2 + expert, rows, cols, out);
+  const size_t blocks = ((size_t)rows * (cols / 8) + 255) / 256;
+  for (size_t b0 = 0; b0 < blocks; b0 += INT4_BLOCKS)
+    hipLaunchKernelGGL(k_int4_dequant, dim3((unsigned)std::min<size_t>(blocks - b0, INT4_BLOCKS)), dim3(256), 0, s, int4_group(fmt),
+                       w.data + (size_t)expert * w.estride, w.scales + (size_t)expert * w.sestride,
+                       int4_zeros_at(fmt, rows, cols), int4_zeros(fmt), w.scale2 + expert, rows, cols, out, b0);
   return hipGetLastError();
 }
 
