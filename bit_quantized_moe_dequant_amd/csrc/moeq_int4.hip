@@ -17,10 +17,11 @@
 // for up to four tokens a group's end costs two vector operations instead of eight.
 //
 // What bounds it: the weight stream, and where that is short the launch and one round of loads.
-// Measured, groups of 128: linear 1 x 4096 x 4096 5.3 us, 16 x 2048 x 4096 7.3 (groups of 64, zero
-// points); 6 experts of 4096 x 2048 for one token 12.9 + 10.2 us (4.0 and 2.5 TB/s), for eight
-// tokens 76 + 55 (5.5 and 3.8 TB/s). A tile of 512 weights costs a SIMD 8 vector operations (32
-// clocks) and one matrix instruction of 16.
+// Measured, groups of 128: linear 1 x 4096 x 4096 5.3 us, 16 x 2048 x 4096 7.5 (groups of 64, zero
+// points); 6 experts of 4096 x 2048 for one token 13.4 + 10.4 us (3.8 and 2.5 TB/s), for eight
+// tokens 75 to 87 + 55 (4.8 to 5.5 and 3.8 TB/s; from box to box). The one-token down is short of the
+// stream because each of its 256 work-groups first stages all of h, 74 KB, for its 98 KB of weights.
+// A tile of 512 weights costs a SIMD 8 vector operations (32 clocks) and one matrix instruction of 16.
 #include <hip/hip_ext.h>
 
 #include <algorithm>
@@ -193,7 +194,8 @@ __device__ __forceinline__ u32x4 ones() { return u32x4{0x3F803F80u, 0x3F803F80u,
 
 // Keeps every register of the matrix instructions' results a and b until `v`, computed from them,
 // is there. Where only some of them are used, the compiler gives the others to vector operations
-// between the instruction and its end without the wait that this takes, and the result lands in them.
+// as soon as its wait states (eight here) allow; earlier kernels without this had wrong sums now and
+// then (that those waits fell short is not shown). It costs nothing.
 __device__ __forceinline__ void hold(float& v, const f32x4_t& a, const f32x4_t& b) {
   asm volatile("" : "+v"(v) : "v"(a), "v"(b));
 }

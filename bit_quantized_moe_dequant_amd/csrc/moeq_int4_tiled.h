@@ -12,7 +12,7 @@
 // A group's sum, of exact products, is multiplied by its scale in fp32 and added up (a vector
 // operation per output and group); sums are fp32. The scale multiplied into the weight instead,
 // rounded to fp16, would save those operations (bf16 outputs, tiles of 256 x 128: 2048 x 4096 x 4096
-// 80 us instead of 92, 8192 x 8192 x 4096 560 instead of 710), but every weight would be off by up to
+// 76 us a call instead of 83-92, 8192 x 8192 x 4096 565 instead of 710-755), but every weight would be off by up to
 // 2^-11 and a token's outputs would differ with the batch it is in, by 8e-4.
 //
 // Activations are operand A (its rows: tokens), so a lane's outputs belong to one weight row and
@@ -27,9 +27,11 @@
 // weights between the products of one, as spread by the scheduling groups: left to the compiler,
 // the vector unit's and the matrix unit's work took turns.
 //
-// Measured: linear 2048 x 4096 x 4096, groups of 128, 84 us (0.82 PFLOP/s; its rows 8), 8192 x 8192 x
-// 4096, groups of 64, zero points, 690: the vector unit's work beside the products, decoding and
-// scales, is what bounds it. 256 experts of 4096 x 2048, 6 to a token, 2048 tokens, groups of 128:
+// Measured: linear 2048 x 4096 x 4096, groups of 128, 81 us (0.84 PFLOP/s; its rows 7), 8192 x 8192 x
+// 4096, groups of 64, zero points, about 690 in a stream of calls: the vector unit's work beside the
+// products, decoding and scales, is what bounds it. Tiles of 96 and 128 tokens instead of 64 were
+// slower (2048 x 4096 x 4096 107 and 111 us a call; 8192 x 8192 x 4096 640, two rounds fewer, and 964,
+// where registers spill). 256 experts of 4096 x 2048, 6 to a token, 2048 tokens, groups of 128:
 // gate/up 650, down 590. For few tokens to an expert the weight stream bounds it: 16 tokens, groups
 // of 32, 4.9 TB/s.
 #pragma once

@@ -520,8 +520,10 @@ hipError_t launch_router(const RouterParams& p, hipStream_t s) {
   // The denominator of a softmax takes all logits, and fp32 ones would be off by up to
   // 274 x 2^-23 |W_e| |x| each. It cancels where the K weights are normalised, unless a bias makes
   // the choice depend on it.
-  // With groups a softmax's merits depend on it too; and there the keys' ends and the undecided
-  // groups' exact logits cost more, so that few logits are sooner all taken in fp64. us, bounds |
+  // With groups a softmax's merits are sums of e^(z - max), over that denominator where there is a
+  // bias (without one it drops out of their comparison); the ends below bound no such sums, so all
+  // its logits are taken in fp64. And with groups the keys' ends and the undecided groups' exact
+  // logits cost more, so that few logits are sooner all taken in fp64. us, bounds |
   // fp64, experts in 8 groups: 512 tokens x 4096 x 256 47 | 33, 1024 49 | 54, 1536 59 | 75, 2048 57 | 95;
   // 2048 x 4096 x 64 45 | 34; 512 x 4096 x 1024 79 | 105; 1024 x 8192 x 512 90 | 180.
   const bool many = (double)p.T * p.n_experts * p.hidden >= 0x1p30;
