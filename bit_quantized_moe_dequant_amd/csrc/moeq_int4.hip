@@ -193,9 +193,9 @@ __device__ __forceinline__ f32x4_t mfma(u32x4 x, u32x4 w, f32x4_t c) {
 __device__ __forceinline__ u32x4 ones() { return u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}; }
 
 // Keeps every register of the matrix instructions' results a and b until `v`, computed from them,
-// is there. Where only some of them are used, the compiler gives the others to vector operations
-// as soon as its wait states (eight here) allow; earlier kernels without this had wrong sums now and
-// then (that those waits fell short is not shown). It costs nothing.
+// is there. Where only some of them are used, the compiler gives the others to other operations
+// behind the instruction, and in early forms of these kernels not always after the eight wait states
+// that this takes: sums were wrong now and then. It costs nothing.
 __device__ __forceinline__ void hold(float& v, const f32x4_t& a, const f32x4_t& b) {
   asm volatile("" : "+v"(v) : "v"(a), "v"(b));
 }
