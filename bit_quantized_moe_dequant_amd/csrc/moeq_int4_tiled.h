@@ -269,21 +269,30 @@ __device__ __forceinline__ void int4_tile(const Int4Rows& P, uint8_t* lds, int b
         for (int t = 0; t < NT; t++) tot[m][t] += *sums(k, m, t);
   }
 
-  // lane (n, g), register r of token tile t: token 16 t + 4 g + r, weight row n of the tile
+  // lane (n, g), register r of token tile t: token 16 t + 4 g + r, weight row n of the tile. Of the
+  // token's and the tensor's powers of two, a sum takes the token's first where the tensor's is 1 or
+  // more, and last where it is less: one by itself may carry it out of fp32's range and the other back.
   const int t0 = wn * NT * 16 + 4 * g;
+  float s2[PAIRS];
+#pragma unroll
+  for (int m = 0; m < PAIRS; m++) s2[m] = P.w[m].scale2[e];
 #pragma unroll
   for (int t = 0; t < NT; t++) {
-    float as[4];
+    float c[PAIRS][4][2];
     size_t at[4];
 #pragma unroll
     for (int r = 0; r < 4; r++) {
       const int i = min(t0 + 16 * t + r, count - 1);
       const size_t a = KIND == I4_LINEAR ? (size_t)(first + i) : (size_t)perm[i];
-      as[r] = P.act_scale[KIND == I4_GATE_UP ? a / P.top_k : a];
-      if constexpr (KIND == I4_DOWN_PART) as[r] *= P.rw[a];
+      float as = P.act_scale[KIND == I4_GATE_UP ? a / P.top_k : a];
+      if constexpr (KIND == I4_DOWN_PART) as *= P.rw[a];
+#pragma unroll
+      for (int m = 0; m < PAIRS; m++) {
+        c[m][r][0] = s2[m] >= 1.f ? as : s2[m];
+        c[m][r][1] = s2[m] >= 1.f ? s2[m] : as;
+      }
       at[r] = a * P.rows;
     }
-    const float s0 = P.w[0].scale2[e], s1 = PAIRS == 2 ? P.w[1].scale2[e] : 0.f;
 #pragma unroll
     for (int m = 0; m < RT; m++) {
       const int row = ((bm * WM + wm) * RT + m) * 16 + n;
@@ -294,8 +303,8 @@ __device__ __forceinline__ void int4_tile(const Int4Rows& P, uint8_t* lds, int b
 #pragma unroll
       for (int r = 0; r < 4; r++) {
         if (t0 + 16 * t + r >= count) continue;
-        float v = tot[m][t][r] * s0 * as[r];
-        if constexpr (PAIRS == 2) v = silu_mul(v, tot[RT + m][t][r] * s1 * as[r]);
+        float v = tot[m][t][r] * c[0][r][0] * c[0][r][1];
+        if constexpr (PAIRS == 2) v = silu_mul(v, tot[RT + m][t][r] * c[1][r][0] * c[1][r][1]);
         if constexpr (KIND == I4_LINEAR) {
           v += bias;
           if (P.out_bf16) {

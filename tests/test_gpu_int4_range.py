@@ -116,3 +116,19 @@ def test_small_intermediate_values_beside_a_large_one(low):
         np.add.at(ref, t, r * o)
         np.add.at(tol, t, r * (off + down.tol(v, e) + 2.0 ** -22 * np.abs(o)))
     assert np.all(np.abs(y - ref) <= tol), float((np.abs(y - ref) / tol).max())
+
+@pytest.mark.parametrize("scale,x", [(2.0 ** 110, 2.0 ** -120), (2.0 ** -121, 2.0 ** 111), (2.0 ** 120, 2.0 ** -125)])
+@pytest.mark.parametrize("T", [1, 5, 16, 17, 33, 200])
+def test_scales_and_tokens_at_opposite_ends(scale, x, T):
+    """Outputs near 1 from factors whose partial products leave fp32's range, at every number of tokens."""
+    say("opposite ends", scale, x, T)
+    g = np.random.default_rng(T)
+    p = Parts(mq.FMT_INT4Z_G64, 1, 40, 1024, seed=3)
+    p.st = (torch.from_numpy(1 + g.random(p.st.shape)) * scale).to(torch.bfloat16)
+    w = p.pack()
+    xt, xd = bf16(g.standard_normal((T, 1024)) * x)
+    ref = xd @ p.values().T
+    assert np.abs(ref).max() < 1e5
+    y = mq.linear_int4(w, xt, out_dtype=torch.float32).double().cpu().numpy()
+    # x of subnormal size has its last bits at 2^-133 (bf16) already; sums as in tests/int4_ref.py
+    assert np.all(np.abs(y - ref) <= p.tol(xd) + 2.0 ** -23 * np.abs(ref)), float((np.abs(y - ref) / (p.tol(xd) + 1e-30)).max())
