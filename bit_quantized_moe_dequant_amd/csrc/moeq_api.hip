@@ -202,9 +202,11 @@ WsLayout ws_layout(const moeq_layer* L, int T) {
   if (is_int4(L->down.fmt) && !int4_dn_direct(L, T)) {  // and those of h
     w.hr = off;
     w.hrs = w.hr + align_up(int4_rows_bytes(P, 2, L->inter), 256);
+    size_t need = w.hrs - w.hr + align_up(P * 4, 256);
     // not less than fewer tokens' bf16 terms: a workspace for more tokens serves fewer
-    const size_t terms = int4_terms_bytes(L, int4_dn_direct_tokens(L, T));
-    off += std::max(w.hrs - w.hr + align_up(P * 4, 256), terms);
+    const int fit = (int)(need / ((size_t)L->top_k * L->inter * 6));
+    if (fit + 1 < T && int4_dn_direct(L, fit + 1)) need = std::max(need, int4_terms_bytes(L, int4_dn_direct_tokens(L, T)));
+    off += need;
   } else if (is_int4(L->down.fmt)) {  // h as three bf16 terms
     w.h4 = off;
     off += int4_terms_bytes(L, T);
