@@ -19,7 +19,7 @@
 // What bounds it: the weight stream, and where that is short the launch and one round of loads.
 // Measured, groups of 128: linear 1 x 4096 x 4096 5.3 us, 16 x 2048 x 4096 7.5 (groups of 64, zero
 // points); 6 experts of 4096 x 2048 for one token 13.4 + 10.4 us (3.8 and 2.5 TB/s), for eight
-// tokens 75 to 87 + 55 (4.8 to 5.5 and 3.8 TB/s; from box to box). The one-token down is short of the
+// tokens 75 to 87 + 55 (4.8 to 5.5 and 3.8 TB/s; from card to card). The one-token down is short of the
 // stream because each of its 256 work-groups first stages all of h, 74 KB, for its 98 KB of weights.
 // A tile of 512 weights costs a SIMD 8 vector operations (32 clocks) and one matrix instruction of 16.
 #include <hip/hip_ext.h>
